@@ -10,6 +10,9 @@ from ._lib import (fp8_quantize, fp8_quantize_bf16, fp8_quantize_tensor, gemm_fp
                    grouped_gemm_fp8_contiguous_workspace_size, grouped_gemm_fp8_contiguous_ws,
                    grouped_gemm_fp8_contiguous_noalloc,
                    grouped_gemm_fp8_masked, gemm_fp8_pertensor_fmt, fp8_quantize_delayed,
+                   moe_route, moe_route_workspace_size, moe_route_backward,
+                   fp8_quantize_transpose, grouped_gemm_fp8_wgrad,
+                   grad_norm_sq, grad_norm_sq_workspace_size, grad_clip,
                    fp8g_clock_probe, fp8g_warmup,
                    fp8g_set_shape_specialisation, fp8g_gemm_kernel_name, fp8g_abi_version,
                    status_string, load,
@@ -20,6 +23,9 @@ __all__ = ["fp8_quantize", "fp8_quantize_bf16", "fp8_quantize_tensor", "gemm_fp8
            "grouped_gemm_fp8_contiguous_workspace_size", "grouped_gemm_fp8_contiguous_ws",
            "grouped_gemm_fp8_contiguous_noalloc",
            "grouped_gemm_fp8_masked", "gemm_fp8_pertensor_fmt", "fp8_quantize_delayed",
+           "moe_route", "moe_route_workspace_size", "moe_route_backward",
+           "fp8_quantize_transpose", "grouped_gemm_fp8_wgrad",
+           "grad_norm_sq", "grad_norm_sq_workspace_size", "grad_clip",
            "fp8g_clock_probe", "fp8g_warmup",
            "fp8g_set_shape_specialisation", "fp8g_gemm_kernel_name", "fp8g_abi_version",
            "status_string", "load",

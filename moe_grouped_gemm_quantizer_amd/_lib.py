@@ -20,12 +20,16 @@ ENTRY_POINTS = ("fp8_quantize", "fp8_quantize_bf16", "fp8_quantize_tensor", "gem
                 "grouped_gemm_fp8_contiguous_ws", "grouped_gemm_fp8_contiguous_noalloc",
                 "grouped_gemm_fp8_masked", "fp8g_clock_probe", "fp8g_warmup",
                 "fp8g_set_shape_specialisation", "fp8g_gemm_kernel_name",
+                "moe_route", "moe_route_workspace_size", "moe_route_backward",
+                "fp8_quantize_transpose", "grouped_gemm_fp8_wgrad", "grad_norm_sq",
+                "grad_norm_sq_workspace_size", "grad_clip",
                 "fp8g_status_string", "fp8g_abi_version")
 
 _c_i64 = ctypes.c_int64
 _c_int = ctypes.c_int
 _c_vp = ctypes.c_void_p
 _c_sz = ctypes.c_size_t
+_c_f = ctypes.c_float
 
 _SIGS = {
     "fp8_quantize": [_c_vp, _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp],
@@ -55,6 +59,18 @@ _SIGS = {
     "fp8g_set_shape_specialisation": [_c_int],
     "fp8g_gemm_kernel_name": [_c_int, _c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int,
                               ctypes.c_char_p, _c_sz],
+    "moe_route": [_c_vp, _c_int, _c_i64, _c_int, _c_i64, _c_vp, _c_int, _c_int, _c_f, _c_int, _c_i64,
+                  _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_sz, _c_vp],
+    "moe_route_workspace_size": [_c_i64, _c_int, ctypes.POINTER(_c_sz)],
+    "moe_route_backward": [_c_vp, _c_int, _c_i64, _c_int, _c_i64, _c_vp, _c_int, _c_int, _c_f, _c_vp,
+                           _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp],
+    "fp8_quantize_transpose": [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_i64, _c_vp,
+                               _c_vp],
+    "grouped_gemm_fp8_wgrad": [_c_vp, _c_int, _c_i64, _c_vp, _c_vp, _c_int, _c_i64, _c_vp, _c_vp,
+                               _c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp],
+    "grad_norm_sq": [_c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_sz, _c_vp],
+    "grad_norm_sq_workspace_size": [_c_vp, _c_int, ctypes.POINTER(_c_sz)],
+    "grad_clip": [_c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_f, _c_vp, _c_vp],
 }
 
 LAYOUTS = {"dense": 0, "contiguous": 1, "masked": 2, "pertensor": 3}
@@ -377,6 +393,205 @@ def grouped_gemm_fp8_masked(a, sa, b, sb, d, masked_m, expected_m=0, stream=None
                                         _ptr(masked_m), G, max_m, N, K, int(expected_m),
                                         _stream(stream))
     _check(st, "grouped_gemm_fp8_masked")
+
+
+_TYPES = None
+
+
+def _type(t):
+    """FP8G_TYPE_* of a tensor, None for any other element type."""
+    global _TYPES
+    if _TYPES is None:
+        import torch
+        _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    return _TYPES.get(t.dtype)
+
+
+def _rows(t, what):
+    """Row stride of a matrix whose rows are contiguous."""
+    _need(t.dim() == 2 and t.is_cuda, f"{what} must be a matrix on the GPU")
+    _need(t.shape[1] <= 1 or t.stride(1) == 1, f"{what}: the elements of a row must be contiguous")
+    # (a single row has any stride, and so have empty ones)
+    return t.stride(0) if t.shape[0] > 1 and t.shape[1] > 0 else t.shape[1]
+
+
+def _out(t, shape, dtype, what):
+    _need(tuple(t.shape) == shape and t.dtype == dtype, f"{what} must be {dtype} {list(shape)}")
+    _need(t.is_cuda and t.is_contiguous(), f"{what} must be contiguous and on the GPU")
+
+
+def _room(workspace):
+    if workspace is None:
+        return None, 0
+    _dev(workspace)
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def moe_route_workspace_size(T, E):
+    """Bytes of workspace moe_route needs for T tokens and E experts (0: none)."""
+    out = ctypes.c_size_t(0)
+    _check(load().moe_route_workspace_size(int(T), int(E), ctypes.byref(out)),
+           "moe_route_workspace_size")
+    return int(out.value)
+
+
+def moe_route(logits, top_k, expert_ids, weights, counts, routed, prob_sum, loss, group_offsets, slots,
+              workspace=None, token_mask=None, renormalise=False, loss_coef=1.0, align=128, max_m=0,
+              stream=None):
+    """Routing of T tokens to top_k of E experts, with the balance loss.
+
+    logits [T][E] (float32, bfloat16 or float16; rows may be strided), token_mask
+    bool or uint8 [T] or None. Written: expert_ids int32 [T][top_k] (-1: none),
+    weights float32 [T][top_k], counts int32 [E], routed int32 [1], prob_sum
+    float32 [E], loss float32 [1], group_offsets int32 [E+1] (contiguous layout,
+    multiples of align; with max_m > 0 the masked layout's slabs), slots int32
+    [T][top_k] (row of each pair in that layout, -1: none). workspace: a device
+    tensor of at least moe_route_workspace_size(T, E) bytes."""
+    import torch
+    ld = _rows(logits, "logits")
+    T, E = logits.shape
+    top_k = int(top_k)
+    typ = _type(logits)
+    _need(typ is not None, "logits must be float32, bfloat16 or float16")
+    i32, f32 = torch.int32, torch.float32
+    _out(expert_ids, (T, top_k), i32, "expert_ids")
+    _out(weights, (T, top_k), f32, "weights")
+    _out(counts, (E,), i32, "counts")
+    _out(routed, (1,), i32, "routed")
+    _out(prob_sum, (E,), f32, "prob_sum")
+    _out(loss, (1,), f32, "loss")
+    _out(group_offsets, (E + 1,), i32, "group_offsets")
+    _out(slots, (T, top_k), i32, "slots")
+    if token_mask is not None:
+        _need(token_mask.dtype in (torch.bool, torch.uint8) and tuple(token_mask.shape) == (T,),
+              "token_mask must be bool or uint8 [T]")
+        _dev(token_mask)
+    wp, wb = _room(workspace)
+    _check(load().moe_route(_ptr(logits), typ, T, E, ld, _ptr(token_mask), top_k,
+                            1 if renormalise else 0, float(loss_coef), int(align), int(max_m),
+                            _ptr(expert_ids), _ptr(weights), _ptr(counts), _ptr(routed),
+                            _ptr(prob_sum), _ptr(loss), _ptr(group_offsets), _ptr(slots), wp, wb,
+                            _stream(stream)), "moe_route")
+
+
+def moe_route_backward(logits, expert_ids, d_weights, d_loss, counts, routed, d_logits,
+                       renormalise=False, loss_coef=1.0, stream=None):
+    """Gradient of moe_route's weights and loss with respect to the logits.
+
+    logits, expert_ids, counts, routed, renormalise, loss_coef as given to and
+    written by moe_route; d_weights float32 [T][top_k] or None, d_loss float32
+    [1] or None; d_logits [T][E] of the logits' type (rows may be strided)."""
+    import torch
+    ld, ldd = _rows(logits, "logits"), _rows(d_logits, "d_logits")
+    T, E = logits.shape
+    typ = _type(logits)
+    _need(typ is not None and d_logits.dtype == logits.dtype and d_logits.shape == logits.shape,
+          "logits and d_logits must be float32, bfloat16 or float16, alike in type and shape")
+    _need(expert_ids.dim() == 2 and expert_ids.shape[0] == T, "expert_ids must be int32 [T][top_k]")
+    top_k = expert_ids.shape[1]
+    _out(expert_ids, (T, top_k), torch.int32, "expert_ids")
+    if d_weights is not None:
+        _out(d_weights, (T, top_k), torch.float32, "d_weights")
+    if d_loss is not None:
+        _out(d_loss, (1,), torch.float32, "d_loss")
+    _out(counts, (E,), torch.int32, "counts")
+    _out(routed, (1,), torch.int32, "routed")
+    _check(load().moe_route_backward(_ptr(logits), typ, T, E, ld, _ptr(expert_ids), top_k,
+                                     1 if renormalise else 0, float(loss_coef), _ptr(d_weights),
+                                     _ptr(d_loss), _ptr(counts), _ptr(routed), _ptr(d_logits), ldd,
+                                     _stream(stream)), "moe_route_backward")
+
+
+def fp8_quantize_transpose(x, fmt, qt, st, stream=None):
+    """x [rows][cols] (float32, bfloat16 or float16; rows may be strided) ->
+    qt uint8 [cols][R] codes in fmt ('e4m3' or 'e5m2'), R = rows rounded up to
+    128, and st uint8 [R/128][cols]: one power-of-two scale per column and 128
+    rows, as its exponent + 127."""
+    import torch
+    ldx = _rows(x, "x")
+    rows, cols = x.shape
+    typ = _type(x)
+    _need(typ is not None, "x must be float32, bfloat16 or float16")
+    _need(qt.dtype == torch.uint8 and st.dtype == torch.uint8, "qt and st must be uint8")
+    _need(tuple(qt.shape) == (cols, _nb(rows) * 128), "qt must be [cols][rows rounded up to 128]")
+    _need(tuple(st.shape) == (_nb(rows), cols), "st must be [ceil(rows/128)][cols]")
+    ldq = _rows(qt, "qt")
+    _dev(st)
+    _check(load().fp8_quantize_transpose(_ptr(x), typ, rows, cols, ldx, _fmt(fmt), _ptr(qt), ldq,
+                                         _ptr(st), _stream(stream)), "fp8_quantize_transpose")
+
+
+def grouped_gemm_fp8_wgrad(a, fmt_a, sa, b, fmt_b, sb, d, group_offsets=None, stream=None):
+    """Weight gradients of G experts: d bf16 [G][M][N] from a [M][T], sa
+    [T/128][M], b [N][T], sb [T/128][N] as fp8_quantize_transpose writes them
+    (T a multiple of 128); group_offsets int32 [G+1] (device) or None (G = 1,
+    all tokens)."""
+    import torch
+    lda, ldb = _rows(a, "a"), _rows(b, "b")
+    M, T = a.shape
+    N = b.shape[0]
+    fa, fb = _fmt(fmt_a), _fmt(fmt_b)
+    _need(b.shape[1] == T and T % 128 == 0, "a and b must have the same tokens, a multiple of 128")
+    _need(_codes_dtype_ok(a, fmt_a) and _codes_dtype_ok(b, fmt_b),
+          "a and b must be codes of their formats (uint8 or the matching float8 dtype)")
+    _need(tuple(sa.shape) == (T // 128, M) and tuple(sb.shape) == (T // 128, N)
+          and sa.dtype == torch.uint8 and sb.dtype == torch.uint8,
+          "sa and sb must be uint8 [T/128][M] and [T/128][N]")
+    _need(d.dim() == 3 and d.shape[1] == M and d.shape[2] == N
+          and d.dtype in (torch.int16, torch.bfloat16, torch.uint16), "d must be bf16 [G][M][N]")
+    G = d.shape[0]
+    if group_offsets is None:
+        _need(G == 1, "group_offsets may be None for one expert only")
+    else:
+        _out(group_offsets, (G + 1,), torch.int32, "group_offsets")
+    _dev(sa, sb, d)
+    _check(load().grouped_gemm_fp8_wgrad(_ptr(a), fa, lda, _ptr(sa), _ptr(b), fb, ldb, _ptr(sb),
+                                         _ptr(d), _ptr(group_offsets), G, T, M, N, _stream(stream)),
+           "grouped_gemm_fp8_wgrad")
+
+
+def _grad_list(ts, what):
+    """HOST arrays of the tensors' pointers, sizes and types."""
+    n = len(ts)
+    types = [_type(t) for t in ts]
+    _need(None not in types, f"{what} must be float32, bfloat16 or float16")
+    _need(all(t.is_cuda and t.is_contiguous() for t in ts), f"{what} must be contiguous and on the GPU")
+    return (_c_vp * n)(*[t.data_ptr() for t in ts]), (_c_i64 * n)(*[t.numel() for t in ts]), (_c_int * n)(*types)
+
+
+def grad_norm_sq_workspace_size(grads):
+    """Bytes of workspace grad_norm_sq needs for this list of tensors."""
+    out = ctypes.c_size_t(0)
+    n = len(grads)
+    _check(load().grad_norm_sq_workspace_size((_c_i64 * n)(*[t.numel() for t in grads]), n,
+                                              ctypes.byref(out)), "grad_norm_sq_workspace_size")
+    return int(out.value)
+
+
+def grad_norm_sq(grads, sumsq, workspace, stream=None):
+    """Sum of squares over a list of contiguous tensors (float32, bfloat16,
+    float16, mixed) into sumsq, a float64 device tensor of one element.
+    workspace: at least grad_norm_sq_workspace_size(grads) bytes."""
+    import torch
+    ptrs, numels, types = _grad_list(grads, "grads")
+    _out(sumsq, (1,), torch.float64, "sumsq")
+    wp, wb = _room(workspace)
+    _check(load().grad_norm_sq(ptrs, numels, types, len(grads), _ptr(sumsq), wp, wb, _stream(stream)),
+           "grad_norm_sq")
+
+
+def grad_clip(grads, outs, sumsq, max_norm, norm, stream=None):
+    """outs[i] = grads[i] * min(1, max_norm / (norm + 1e-6)), norm = sqrt(sumsq)
+    (float32 device tensor of one element, written). outs[i] may be grads[i]."""
+    import torch
+    ptrs, numels, types = _grad_list(grads, "grads")
+    optrs, onumels, otypes = _grad_list(outs, "outs")
+    _need(len(outs) == len(grads) and onumels[:] == numels[:] and otypes[:] == types[:],
+          "outs must match grads in number, size and type")
+    _out(sumsq, (1,), torch.float64, "sumsq")
+    _out(norm, (1,), torch.float32, "norm")
+    _check(load().grad_clip(ptrs, optrs, numels, types, len(grads), _ptr(sumsq), float(max_norm),
+                            _ptr(norm), _stream(stream)), "grad_clip")
 
 
 def fp8g_clock_probe(out, ticks=2000, stream=None):

@@ -1,0 +1,244 @@
+// Global gradient norm and clipping over a list of tensors.
+//
+// norm = sqrt(sum over all tensors of x^2); each gradient is multiplied by
+// min(1, max_norm / (norm + 1e-6)). Both passes are HBM streams. Squares are
+// formed and added in fp64: an fp32 square overflows from 1.8e19 on and
+// vanishes below 1e-23, and the vector unit's fp64 rate (one fma per lane
+// and cycle as in fp32) is far above what HBM feeds it.
+//
+// The list travels in the kernel's arguments, up to 112 tensors a launch
+// (4 KB of arguments): nothing of it stays on the device or in the library.
+
+#include <vector>
+
+#include "elem.h"
+#include "internal.h"
+
+namespace fp8g {
+namespace {
+
+using namespace elem;
+
+constexpr int THREADS = 256;
+constexpr int MAX_T = 112;                             // tensors of a launch
+constexpr int64_t CHUNK = 32768;                       // elements of a chunk
+constexpr int64_t MAX_GRID = 2048;                     // eight workgroups per CU
+
+struct Table {
+  const void* x[MAX_T];
+  void* y[MAX_T];
+  int64_t numel[MAX_T];
+  int end[MAX_T];                                      // chunks of this tensor and those before it
+  uint8_t type[MAX_T];
+  int n;
+};
+
+int64_t chunks_of(int64_t numel) { return (numel + CHUNK - 1) / CHUNK; }
+
+// The tensor of chunk c and the chunk's place in it.
+__device__ __forceinline__ int find(const Table& t, int c, int64_t& at) {
+  int lo = 0, hi = t.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (c < t.end[mid]) hi = mid;
+    else lo = mid + 1;
+  }
+  at = (int64_t)(c - (lo ? t.end[lo - 1] : 0)) * CHUNK;
+  return lo;
+}
+
+template <typename T>
+__device__ __forceinline__ double chunk_sum(const T* __restrict__ x, int n) {
+  constexpr int W = 16 / (int)sizeof(T);
+  double s = 0.0;
+  int done = 0;
+  if ((uintptr_t)x % 16 == 0) {
+    const int packs = n / W;
+    done = packs * W;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < packs; i += THREADS) {
+      const Pack<T, W> p = reinterpret_cast<const Pack<T, W>*>(x)[i];
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const double v = (double)to_f32(p.v[w]);
+        s = __builtin_fma(v, v, s);
+      }
+    }
+  }
+  for (int i = done + threadIdx.x; i < n; i += THREADS) {
+    const double v = (double)to_f32(x[i]);
+    s = __builtin_fma(v, v, s);
+  }
+  return s;
+}
+
+// Sum over the workgroup, in lane and wave order.
+__device__ __forceinline__ double group_sum(double s, double* lds) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
+  __syncthreads();
+  return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
+// Chunks blockIdx.x, + gridDim.x, ...: one partial sum per workgroup.
+__global__ void __launch_bounds__(THREADS)
+norm_partial_kernel(Table t, double* __restrict__ part) {
+  __shared__ double lds[THREADS / 64];
+  double s = 0.0;
+  const int chunks = t.end[t.n - 1];
+  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+    int64_t at;
+    const int i = find(t, c, at);
+    const int64_t left = t.numel[i] - at;
+    const int n = (int)(left < CHUNK ? left : CHUNK);
+    if (t.type[i] == TYPE_F32) s += chunk_sum((const float*)t.x[i] + at, n);
+    else if (t.type[i] == TYPE_BF16) s += chunk_sum((const bf16_t*)t.x[i] + at, n);
+    else s += chunk_sum((const f16_t*)t.x[i] + at, n);
+  }
+  s = group_sum(s, lds);
+  if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+__global__ void __launch_bounds__(THREADS)
+norm_finish_kernel(const double* __restrict__ part, int n, double* __restrict__ sumsq) {
+  __shared__ double lds[THREADS / 64];
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n; i += THREADS) s += part[i];
+  s = group_sum(s, lds);
+  if (threadIdx.x == 0) *sumsq = s;
+}
+
+// The product rounded to fp32, then to the type. (Left to itself the compiler
+// turns some fp16 products into a mixed-precision fma, which rounds once, so
+// that an element's result would depend on the path it takes.)
+template <typename T>
+__device__ __forceinline__ T scaled(T x, float f) {
+  float p = to_f32(x) * f;
+  asm("" : "+v"(p));
+  return from_f32<T>(p);
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_scale(const T* x, T* y, int n, float f) {
+  constexpr int W = 16 / (int)sizeof(T);
+  int done = 0;
+  if (((uintptr_t)x | (uintptr_t)y) % 16 == 0) {
+    const int packs = n / W;
+    done = packs * W;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < packs; i += THREADS) {
+      Pack<T, W> p = reinterpret_cast<const Pack<T, W>*>(x)[i];
+#pragma unroll
+      for (int w = 0; w < W; ++w) p.v[w] = scaled(p.v[w], f);
+      reinterpret_cast<Pack<T, W>*>(y)[i] = p;
+    }
+  }
+  for (int i = done + threadIdx.x; i < n; i += THREADS) y[i] = scaled(x[i], f);
+}
+
+// (n == 0: one workgroup writes the norm)
+__global__ void __launch_bounds__(THREADS)
+clip_kernel(Table t, const double* __restrict__ sumsq, float max_norm, float* __restrict__ norm,
+            int write_norm) {
+  const double nrm = sqrt(*sumsq);
+  if (write_norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)nrm;
+  const double q = (double)max_norm / (nrm + 1e-6);
+  const float f = q >= 1.0 ? 1.0f : (float)q;          // (NaN stays NaN)
+  const int chunks = t.n ? t.end[t.n - 1] : 0;
+  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+    int64_t at;
+    const int i = find(t, c, at);
+    if (t.x[i] == t.y[i] && f == 1.0f) continue;
+    const int64_t left = t.numel[i] - at;
+    const int n = (int)(left < CHUNK ? left : CHUNK);
+    if (t.type[i] == TYPE_F32)
+      chunk_scale((const float*)t.x[i] + at, (float*)t.y[i] + at, n, f);
+    else if (t.type[i] == TYPE_BF16)
+      chunk_scale((const bf16_t*)t.x[i] + at, (bf16_t*)t.y[i] + at, n, f);
+    else
+      chunk_scale((const f16_t*)t.x[i] + at, (f16_t*)t.y[i] + at, n, f);
+  }
+}
+
+// The next tensors of the list that fit a launch; empty ones are left out.
+// Returns the launch's grid, 0 when the list is done.
+int64_t fill(Table& t, int& i, const void* const* xs, void* const* ys, const int64_t* numels,
+             const int* types, int n) {
+  t.n = 0;
+  int64_t chunks = 0;
+  for (; i < n && t.n < MAX_T; ++i) {
+    if (numels[i] == 0) continue;
+    const int64_t c = chunks_of(numels[i]);
+    if (chunks + c > 0x7FFFFFFF) break;                // (each tensor fits by itself: checked before)
+    chunks += c;
+    t.x[t.n] = xs[i];
+    t.y[t.n] = ys ? ys[i] : nullptr;
+    t.numel[t.n] = numels[i];
+    t.type[t.n] = (uint8_t)types[i];
+    t.end[t.n] = (int)chunks;
+    ++t.n;
+  }
+  return chunks < MAX_GRID ? chunks : MAX_GRID;
+}
+
+}  // namespace
+
+// One fp64 partial sum per workgroup of every launch: a launch has at most
+// MAX_GRID of them, and at most one per chunk.
+size_t grad_norm_workspace_bytes(const int64_t* numels, int n) {
+  int64_t parts = 0, chunks = 0;
+  int tensors = 0;
+  for (int i = 0; i < n; ++i) {
+    if (numels[i] == 0) continue;
+    const int64_t c = chunks_of(numels[i]);
+    if (tensors == MAX_T || chunks + c > 0x7FFFFFFF) {
+      parts += chunks < MAX_GRID ? chunks : MAX_GRID;
+      chunks = 0;
+      tensors = 0;
+    }
+    chunks += c;
+    ++tensors;
+  }
+  parts += chunks < MAX_GRID ? chunks : MAX_GRID;
+  return (size_t)parts * sizeof(double);
+}
+
+hipError_t launch_grad_norm_sq(const void* const* grads, const int64_t* numels, const int* types,
+                               int n, double* sumsq, void* workspace, hipStream_t stream) {
+  Table t;
+  double* part = (double*)workspace;
+  int parts = 0, i = 0;
+  for (;;) {
+    const int64_t grid = fill(t, i, grads, nullptr, numels, types, n);
+    if (grid == 0) break;
+    norm_partial_kernel<<<dim3((unsigned)grid), dim3(THREADS), 0, stream>>>(t, part + parts);
+    parts += (int)grid;
+  }
+  norm_finish_kernel<<<dim3(1), dim3(THREADS), 0, stream>>>(part, parts, sumsq);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels,
+                            const int* types, int n, const double* sumsq, float max_norm,
+                            float* norm, hipStream_t stream) {
+  Table t;
+  int i = 0, first = 1;
+  for (;;) {
+    const int64_t grid = fill(t, i, grads, outs, numels, types, n);
+    if (grid == 0 && !first) break;
+    clip_kernel<<<dim3((unsigned)(grid ? grid : 1)), dim3(THREADS), 0, stream>>>(
+        t, sumsq, max_norm, norm, first);
+    first = 0;
+    if (grid == 0) break;
+  }
+  return hipGetLastError();
+}
+
+void clip_kernels(std::vector<const void*>& out) {
+  out.push_back((const void*)norm_partial_kernel);
+  out.push_back((const void*)norm_finish_kernel);
+  out.push_back((const void*)clip_kernel);
+}
+
+}  // namespace fp8g

@@ -96,6 +96,9 @@ fp8g_status fp8g_warmup(void) {
   std::vector<const void*> kernels;
   gemm_kernels(kernels);
   quantize_kernels(kernels);
+  route_kernels(kernels);
+  wgrad_kernels(kernels);
+  clip_kernels(kernels);
   for (const void* k : kernels) {
     hipFuncAttributes attr;
     if (hipFuncGetAttributes(&attr, k) != hipSuccess) {

@@ -100,6 +100,60 @@ void set_shape_specialisation(int enable);
 void gemm_kernels(std::vector<const void*>& out);
 void quantize_kernels(std::vector<const void*>& out);
 
+// Element types of inputs that are not 8-bit codes (FP8G_TYPE_*).
+enum ElemType { TYPE_F32 = 0, TYPE_BF16 = 1, TYPE_F16 = 2 };
+
+// Routing (route.hip); arguments as for moe_route and moe_route_backward.
+struct RouteCall {
+  const void* logits;
+  int type;
+  int64_t T, ld, max_m;
+  int E, k, renorm, align;
+  float coef;
+  const uint8_t* mask;
+  int32_t *ids, *counts, *routed, *offsets, *slots;
+  float *weights, *prob_sum, *loss;
+  void* workspace;
+};
+struct RouteBwdCall {
+  const void* logits;
+  int type;
+  int64_t T, ld, ldd;
+  int E, k, renorm;
+  float coef;
+  const int32_t *ids, *counts, *routed;
+  const float *dw, *dloss;
+  void* d_logits;
+};
+size_t route_workspace_bytes(int64_t T, int E);
+hipError_t launch_route(const RouteCall& c, hipStream_t stream);
+hipError_t launch_route_backward(const RouteBwdCall& c, hipStream_t stream, int cu_count);
+void route_kernels(std::vector<const void*>& out);
+
+// The weight gradient (wgrad.hip).
+hipError_t launch_quantize_transpose(const void* x, int type, int64_t rows, int64_t cols,
+                                     int64_t ldx, int fmt, uint8_t* qt, int64_t ldq, uint8_t* st,
+                                     hipStream_t stream);
+struct WgradArgs {
+  const uint8_t *a, *sa, *b, *sb;      // codes [M][lda], [N][ldb]; exponent bytes [T/128][M], [T/128][N]
+  uint16_t* d;                         // bf16 bits [G][M][N]
+  const int32_t* group;                // offsets [G + 1], or null (one expert, all T tokens)
+  int64_t lda, ldb, T, M, N;
+  int G;
+};
+hipError_t launch_wgrad(const WgradArgs& args, int fmt_a, int fmt_b, const DeviceInfo& dev,
+                        hipStream_t stream);
+void wgrad_kernels(std::vector<const void*>& out);
+
+// Gradient norm and clipping (clip.hip).
+size_t grad_norm_workspace_bytes(const int64_t* numels, int n);
+hipError_t launch_grad_norm_sq(const void* const* grads, const int64_t* numels, const int* types,
+                               int n, double* sumsq, void* workspace, hipStream_t stream);
+hipError_t launch_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels,
+                            const int* types, int n, const double* sumsq, float max_norm,
+                            float* norm, hipStream_t stream);
+void clip_kernels(std::vector<const void*>& out);
+
 // The allocation-free contiguous entry point's scratch: its size, and its
 // device address on `device` (looked up once per device; nullptr on failure;
 // call with that device current).

@@ -1,0 +1,633 @@
+// Routing of tokens to experts: softmax over the experts, the k largest
+// logits, the balance loss with its gradient, per-expert counts, and each
+// (token, expert) pair's row in the experts' operand.
+//
+// Mathematics, for a row x of E logits: p = exp(x - max x) / sum exp(x - max x);
+// the choice goes by the logits themselves (the softmax is monotone), so it
+// does not depend on how p is rounded. Loss: coef sum_e (E c_e / (k n)) (P_e / n)
+// with c_e tokens that chose e, n routed tokens, P_e their summed p. Its
+// gradient, with the one of the weights, through the softmax's Jacobian:
+// dx = p (dp - <p, dp>).
+//
+// A row's pairs need the number of earlier tokens that chose the same
+// expert, over all tokens, so the work has three steps: rows in blocks of 64
+// (choice, weights, each block's counts, sums of p, and ranks inside the
+// block), a scan of the counts over the blocks, and the final slots. Up to
+// 64 tokens are one block, and one launch does everything.
+
+#include <type_traits>
+#include <vector>
+
+#include "elem.h"
+#include "internal.h"
+
+namespace fp8g {
+namespace {
+
+using namespace elem;
+
+constexpr int ROWS = 64;          // tokens of a block
+constexpr int THREADS = 256;
+constexpr int MAX_E = 1024;
+constexpr int MAX_K = 16;
+
+// Where a lane's VPT elements of a row lie: groups of W consecutive ones
+// (one access), LPR lanes side by side.
+template <typename T, int LPR, int VPT>
+struct Lay {
+  static constexpr int WMAX = 16 / (int)sizeof(T);
+  static constexpr int W = VPT < WMAX ? VPT : WMAX;
+  static constexpr int ROWS_AT_ONCE = THREADS / LPR;
+  __device__ static __forceinline__ int at(int v, int l) {
+    return (v / W) * (W * LPR) + l * W + v % W;
+  }
+};
+
+// A row's logits as fp32; past E (and for a row that takes no part) -inf.
+template <typename T, int LPR, int VPT>
+__device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int l, bool on, bool vec,
+                                         float (&x)[VPT]) {
+  using L = Lay<T, LPR, VPT>;
+#pragma unroll
+  for (int g = 0; g < VPT / L::W; ++g) {
+    const int e0 = L::at(g * L::W, l);
+    if (vec && on && e0 + L::W <= E) {
+      const Pack<T, L::W> p = *reinterpret_cast<const Pack<T, L::W>*>(row + e0);
+#pragma unroll
+      for (int w = 0; w < L::W; ++w) x[g * L::W + w] = to_f32(p.v[w]);
+    } else {
+#pragma unroll
+      for (int w = 0; w < L::W; ++w)
+        x[g * L::W + w] = on && e0 + w < E ? to_f32(row[e0 + w]) : -__builtin_inff();
+    }
+  }
+}
+
+// Unsigned keys in the order of the values (-0 as +0); 0 for what is never
+// chosen: -inf and NaN.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  const uint32_t k = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return x > -__builtin_inff() ? k : 0u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
+}
+
+// The largest remaining logit of each row, and its removal. 16-bit inputs
+// pack the order of their value and the expert's number (lower first) into
+// one word, so that one maximum finds both; 32-bit ones find the value and
+// then the lowest expert that has it.
+template <typename T, int LPR, int VPT>
+struct Picker {
+  using L = Lay<T, LPR, VPT>;
+  uint32_t key[VPT];
+  static constexpr bool PACKED = sizeof(T) == 2;
+
+  // (a 16-bit value's fp32 key: bf16 has its order in the upper half; fp16
+  // is widened, so it is brought back to its own 16 bits)
+  __device__ static __forceinline__ uint32_t half_key(float x) {
+    if constexpr (std::is_same<T, f16_t>::value) {
+      const uint16_t u = __builtin_bit_cast(uint16_t, (f16_t)(x + 0.0f));
+      const uint32_t k = (u & 0x8000u) ? (uint16_t)~u : (uint16_t)(u | 0x8000u);
+      return x > -__builtin_inff() ? k : 0u;
+    } else {
+      return order_key(x) >> 16;
+    }
+  }
+  __device__ static __forceinline__ float half_value(uint32_t k) {
+    if constexpr (std::is_same<T, f16_t>::value) {
+      const uint16_t u = (uint16_t)((k & 0x8000u) ? (k ^ 0x8000u) : ~k);
+      return (float)__builtin_bit_cast(f16_t, u);
+    } else {
+      // (the lower half of a negative value's key is all ones, cut off above)
+      return key_value((k << 16) | ((k & 0x8000u) ? 0u : 0xFFFFu));
+    }
+  }
+
+  __device__ __forceinline__ void start(const float (&x)[VPT], int l) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      if constexpr (PACKED) {
+        const uint32_t h = half_key(x[v]);
+        key[v] = h ? (h << 16) | (0xFFFFu - (uint32_t)L::at(v, l)) : 0u;
+      } else {
+        key[v] = order_key(x[v]);
+      }
+    }
+  }
+  // expert (-1: none is left) and its logit, the same in all the row's lanes
+  __device__ __forceinline__ int next(int l, float& value) {
+    const auto umax = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+    uint32_t best = key[0];
+#pragma unroll
+    for (int v = 1; v < VPT; ++v) best = umax(best, key[v]);
+    best = reduce_u32<LPR>(best, umax);
+    int e;
+    if constexpr (PACKED) {
+      e = (int)(0xFFFFu - (best & 0xFFFFu));
+      value = half_value(best >> 16);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) key[v] = key[v] == best ? 0u : key[v];
+    } else {
+      uint32_t low = 0xFFFFFFFFu;
+#pragma unroll
+      for (int v = VPT - 1; v >= 0; --v) low = key[v] == best ? (uint32_t)L::at(v, l) : low;
+      low = reduce_u32<LPR>(low, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+      e = (int)low;
+      value = key_value(best);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) key[v] = (uint32_t)L::at(v, l) == low ? 0u : key[v];
+    }
+    return best ? e : -1;
+  }
+};
+
+// exp(x - max) of a row and their sum's reciprocal. A row of -inf alone has
+// p = 0; NaN or +inf in a row make its p NaN.
+template <int LPR, int VPT>
+__device__ __forceinline__ float row_softmax(const float (&x)[VPT], float& top, float (&ex)[VPT]) {
+  float m = x[0];
+#pragma unroll
+  for (int v = 1; v < VPT; ++v) m = __builtin_fmaxf(m, x[v]);
+  m = max_lanes<LPR>(m);
+  top = m > -__builtin_inff() ? m : 0.0f;        // (m is NaN for a row of NaN alone)
+  float s = 0.0f;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    ex[v] = expf(x[v] - top);
+    s += ex[v];
+  }
+  s = sum_lanes<LPR>(s);
+  return s == 0.0f ? 0.0f : 1.0f / s;
+}
+
+// Expert offsets of the contiguous layout: exclusive prefix sums of the
+// counts rounded up to `align`, by the whole workgroup (E <= 4 THREADS).
+__device__ __forceinline__ void offsets_of(const int* __restrict__ counts, int E, int align,
+                                           int* __restrict__ off, int* __restrict__ wave_sum) {
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  int c[4], s = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = t * 4 + i;
+    c[i] = e < E ? (counts[e] + align - 1) / align * align : 0;
+    s += c[i];
+  }
+  int inc = s;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 63) wave_sum[wave] = inc;
+  __syncthreads();
+  int at = inc - s;
+  for (int w = 0; w < wave; ++w) at += wave_sum[w];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = t * 4 + i;
+    if (e < E) off[e] = at;
+    at += c[i];
+    if (e == E - 1) off[E] = at;
+  }
+  __syncthreads();
+}
+
+// loss = coef sum_e (E c_e / (k n)) (P_e / n), by the first wave.
+__device__ __forceinline__ void write_loss(const int* counts, const float* prob_sum, int routed,
+                                           int E, int k, float coef, float* loss) {
+  if (threadIdx.x >= 64) return;
+  double s = 0.0;
+  for (int e = threadIdx.x; e < E; e += 64) s += (double)counts[e] * (double)prob_sum[e];
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o);
+  const double n = routed > 0 ? (double)routed : 1.0;
+  if (threadIdx.x == 0) *loss = (float)((double)coef * E / ((double)k * n * n) * s);
+}
+
+struct RouteArgs {
+  const void* logits;
+  const uint8_t* mask;
+  int64_t T, ld, max_m;
+  int E, k, renorm, align, vec;
+  float coef;
+  int32_t *ids, *counts, *routed, *offsets, *slots;
+  float *weights, *prob_sum, *loss;
+  // one row of counts (the routed tokens last) and of sums of p per block
+  int* part_count;
+  float* part_prob;
+};
+
+__device__ __forceinline__ int slot_of(const RouteArgs& a, int e, int first, int rank) {
+  if (a.max_m == 0) return first + rank;
+  return rank < a.max_m ? (int)(e * a.max_m) + rank : -1;
+}
+
+// One block of 64 tokens per workgroup; LPR lanes per row.
+template <typename T, int LPR, int VPT>
+__global__ void __launch_bounds__(THREADS)
+route_rows_kernel(RouteArgs a) {
+  using L = Lay<T, LPR, VPT>;
+  constexpr int GROUPS = 64 / LPR;                     // rows of a wave at once
+  __shared__ uint32_t took[2][MAX_E];                  // tokens of the block that chose e, as bits
+  __shared__ short chosen[ROWS][MAX_K];
+  __shared__ float psum[THREADS / 64][LPR * VPT];
+  __shared__ int off[MAX_E + 1];
+  __shared__ int wave_sum[THREADS / 64];
+  __shared__ int n_routed;
+  const int E = a.E, k = a.k;
+  for (int e = threadIdx.x; e < E; e += THREADS) took[0][e] = took[1][e] = 0u;
+  if (threadIdx.x == 0) n_routed = 0;
+  __syncthreads();
+  const int l = threadIdx.x & (LPR - 1), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t0 = (int64_t)blockIdx.x * ROWS;
+  float acc[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) acc[v] = 0.0f;
+  for (int r0 = 0; r0 < ROWS && t0 + r0 < a.T; r0 += L::ROWS_AT_ONCE) {
+    const int r = r0 + (int)threadIdx.x / LPR;
+    const int64_t t = t0 + r;
+    const bool in = t < a.T;
+    const bool on = in && (!a.mask || a.mask[t] != 0);
+    float x[VPT], ex[VPT];
+    load_row<T, LPR, VPT>((const T*)a.logits + (in ? t : 0) * a.ld, E, l, on, a.vec != 0, x);
+    float top;
+    const float inv = row_softmax<LPR, VPT>(x, top, ex);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) acc[v] += ex[v] * inv;
+    Picker<T, LPR, VPT> pick;
+    pick.start(x, l);
+    int id = -1;                                       // lane j keeps the row's j-th choice
+    float w = 0.0f;
+    for (int j = 0; j < k; ++j) {
+      float value;
+      const int e = pick.next(l, value);
+      if (l == j && e >= 0) {
+        id = e;
+        w = expf(value - top);
+      }
+    }
+    const float s = a.renorm ? sum_lanes<LPR>(w) : 0.0f;
+    // (a NaN row: inv is NaN, and so is every weight)
+    w = inv != inv ? inv : (a.renorm ? (s > 0.0f ? w / s : 0.0f) : w * inv);
+    if (in && l < k) {
+      a.ids[t * k + l] = id;
+      a.weights[t * k + l] = w;
+      chosen[r][l] = (short)id;
+      if (id >= 0) {
+        atomicOr(&took[r >> 5][id], 1u << (r & 31));
+        if (l == 0) atomicAdd(&n_routed, 1);
+      }
+    }
+  }
+  // sums of p: the rows side by side in a wave, then the waves
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    if constexpr (GROUPS > 1) {
+      acc[v] += __shfl_xor(acc[v], 16);
+      acc[v] += __shfl_xor(acc[v], 32);
+    }
+    if (lane < LPR) psum[wave][L::at(v, l)] = acc[v];
+  }
+  __syncthreads();
+  const bool only = gridDim.x == 1;
+  for (int e = threadIdx.x; e < E; e += THREADS) {
+    const int c = __popc(took[0][e]) + __popc(took[1][e]);
+    const float p = (psum[0][e] + psum[1][e]) + (psum[2][e] + psum[3][e]);
+    if (only) {
+      a.counts[e] = c;
+      a.prob_sum[e] = p;
+      psum[0][e] = p;
+      off[e] = c;
+    } else {
+      a.part_count[(int64_t)blockIdx.x * (E + 1) + e] = c;
+      a.part_prob[(int64_t)blockIdx.x * E + e] = p;
+    }
+  }
+  if (threadIdx.x == 0) {
+    if (only) a.routed[0] = n_routed;
+    else a.part_count[(int64_t)blockIdx.x * (E + 1) + E] = n_routed;
+  }
+  if (only) {
+    __syncthreads();
+    write_loss(off, psum[0], n_routed, E, k, a.coef, a.loss);
+    __syncthreads();
+    if (a.max_m == 0) {
+      offsets_of(off, E, a.align, off, wave_sum);
+      for (int e = threadIdx.x; e <= E; e += THREADS) a.offsets[e] = off[e];
+    } else {
+      for (int e = threadIdx.x; e <= E; e += THREADS) a.offsets[e] = (int)(e * a.max_m);
+    }
+  }
+  // ranks inside the block (its only block: the slots themselves)
+  const int64_t left = a.T - t0;
+  const int rows = left < ROWS ? (int)left : ROWS;
+  for (int i = threadIdx.x; i < rows * k; i += THREADS) {
+    const int r = i / k, e = chosen[r][i - r * k];
+    int s = -1;
+    if (e >= 0) {
+      const uint32_t below = (1u << (r & 31)) - 1u;
+      s = r < 32 ? __popc(took[0][e] & below)
+                 : __popc(took[0][e]) + __popc(took[1][e] & below);
+      if (only) s = slot_of(a, e, off[e], s);
+    }
+    a.slots[t0 * k + i] = s;
+  }
+}
+
+// Scan over the blocks, 64 experts per workgroup, 16 runs of blocks side by
+// side: counts become the tokens of earlier blocks (in place), the totals go
+// out. The last column holds the routed tokens.
+constexpr int RUNS = 16;
+__global__ void __launch_bounds__(64 * RUNS)
+route_scan_kernel(RouteArgs a, int nblk) {
+  __shared__ int cnt[RUNS][64];
+  __shared__ double prob[RUNS][64];
+  const int l = threadIdx.x & 63, run = threadIdx.x >> 6;
+  const int e = blockIdx.x * 64 + l;
+  const int E = a.E;
+  const int per = (nblk + RUNS - 1) / RUNS;
+  const int b0 = run * per, b1 = min(nblk, b0 + per);
+  int s = 0;
+  double p = 0.0;
+  if (e <= E) {
+    for (int b = b0; b < b1; ++b) {
+      s += a.part_count[(int64_t)b * (E + 1) + e];
+      if (e < E) p += (double)a.part_prob[(int64_t)b * E + e];
+    }
+  }
+  cnt[run][l] = s;
+  prob[run][l] = p;
+  __syncthreads();
+  if (e > E) return;
+  int at = 0;
+  for (int q = 0; q < run; ++q) at += cnt[q][l];
+  for (int b = b0; b < b1; ++b) {
+    int* c = a.part_count + (int64_t)b * (E + 1) + e;
+    const int v = *c;
+    *c = at;
+    at += v;
+  }
+  if (run == RUNS - 1) {
+    if (e == E) {
+      a.routed[0] = at;
+    } else {
+      a.counts[e] = at;
+      double ps = 0.0;
+      for (int q = 0; q < RUNS; ++q) ps += prob[q][l];
+      a.prob_sum[e] = (float)ps;
+    }
+  }
+}
+
+// Slots from the ranks; the first workgroup also writes offsets and loss.
+constexpr int PAIRS = 4 * THREADS;                     // pairs per workgroup
+__global__ void __launch_bounds__(THREADS)
+route_slots_kernel(RouteArgs a) {
+  __shared__ int off[MAX_E + 1];
+  __shared__ int wave_sum[THREADS / 64];
+  const int E = a.E, k = a.k;
+  if (a.max_m == 0) {
+    offsets_of(a.counts, E, a.align, off, wave_sum);
+  } else if (blockIdx.x == 0) {
+    for (int e = threadIdx.x; e <= E; e += THREADS) a.offsets[e] = (int)(e * a.max_m);
+  }
+  if (blockIdx.x == 0) {
+    if (a.max_m == 0)
+      for (int e = threadIdx.x; e <= E; e += THREADS) a.offsets[e] = off[e];
+    write_loss(a.counts, a.prob_sum, a.routed[0], E, k, a.coef, a.loss);
+  }
+  const int64_t pairs = a.T * k;
+  const int64_t i0 = (int64_t)blockIdx.x * PAIRS + threadIdx.x;
+#pragma unroll
+  for (int q = 0; q < PAIRS / THREADS; ++q) {
+    const int64_t i = i0 + q * THREADS;
+    if (i >= pairs) break;
+    const int e = a.ids[i];
+    if (e < 0) continue;                               // (its slot is -1 already)
+    const int64_t blk = i / ((int64_t)ROWS * k);
+    const int rank = a.part_count[blk * (E + 1) + e] + a.slots[i];
+    a.slots[i] = slot_of(a, e, a.max_m == 0 ? off[e] : 0, rank);
+  }
+}
+
+__global__ void route_empty_kernel(RouteArgs a) {
+  for (int e = threadIdx.x; e <= a.E; e += THREADS) {
+    if (e < a.E) {
+      a.counts[e] = 0;
+      a.prob_sum[e] = 0.0f;
+    }
+    a.offsets[e] = (int)(e * a.max_m);
+  }
+  if (threadIdx.x == 0) {
+    a.routed[0] = 0;
+    a.loss[0] = 0.0f;
+  }
+}
+
+struct RouteBwdArgs {
+  const void* logits;
+  void* d_logits;
+  const int32_t *ids, *counts, *routed;
+  const float *dw, *dloss;
+  int64_t T, ld, ldd;
+  int E, k, renorm, vec;
+  float coef;
+};
+
+// A workgroup walks rows; LPR lanes per row, the softmax computed again from
+// the logits (it is cheaper to form than to store and read).
+template <typename T, int LPR, int VPT>
+__global__ void __launch_bounds__(THREADS)
+route_backward_kernel(RouteBwdArgs a) {
+  using L = Lay<T, LPR, VPT>;
+  const int E = a.E, k = a.k;
+  const int l = threadIdx.x & (LPR - 1), group = threadIdx.x / LPR;
+  const int n = a.routed[0];
+  const float fac =
+      a.dloss && n > 0
+          ? (float)((double)a.dloss[0] * a.coef * E / ((double)k * (double)n * (double)n))
+          : 0.0f;
+  float f[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int e = L::at(v, l);
+    f[v] = e < E ? fac * (float)a.counts[e] : 0.0f;
+  }
+  for (int64_t t0 = (int64_t)blockIdx.x * L::ROWS_AT_ONCE; t0 < a.T;
+       t0 += (int64_t)gridDim.x * L::ROWS_AT_ONCE) {
+    const int64_t t = t0 + group;
+    const bool in = t < a.T;
+    const T* row = (const T*)a.logits + (in ? t : 0) * a.ld;
+    int id = -1;
+    if (in && l < k) id = a.ids[t * k + l];
+    if (id >= E || id < 0) id = -1;
+    const bool on = __shfl(id, 0, LPR) >= 0;
+    float x[VPT], ex[VPT], top;
+    load_row<T, LPR, VPT>(row, E, l, on, a.vec != 0, x);
+    const float inv = row_softmax<LPR, VPT>(x, top, ex);
+    const float pj = id >= 0 && on ? expf(to_f32(row[id]) - top) * inv : 0.0f;
+    float dwj = id >= 0 && a.dw ? a.dw[t * k + l] : 0.0f;
+    if (a.renorm) {
+      const float s = sum_lanes<LPR>(pj);
+      const float c = sum_lanes<LPR>(id >= 0 ? dwj * pj : 0.0f);
+      dwj = id >= 0 && !(s <= 0.0f) ? (dwj - c / s) / s : 0.0f;
+    }
+    float dot = id >= 0 ? pj * dwj : 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      ex[v] *= inv;
+      dot = __builtin_fmaf(ex[v], f[v], dot);
+    }
+    dot = sum_lanes<LPR>(dot);
+    float g[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) g[v] = f[v] - dot;
+    for (int j = 0; j < k; ++j) {
+      const int e = __shfl(id, j, LPR);
+      const float d = __shfl(dwj, j, LPR);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) g[v] += L::at(v, l) == e ? d : 0.0f;
+    }
+    if (!in) continue;                                 // (whole rows: no lane of a row is left out)
+    T* out = (T*)a.d_logits + t * a.ldd;
+#pragma unroll
+    for (int q = 0; q < VPT / L::W; ++q) {
+      const int e0 = L::at(q * L::W, l);
+      Pack<T, L::W> p;
+#pragma unroll
+      for (int w = 0; w < L::W; ++w) {
+        const int v = q * L::W + w;
+        p.v[w] = from_f32<T>(on ? ex[v] * g[v] : 0.0f);
+      }
+      if (a.vec != 0 && e0 + L::W <= E) {
+        *reinterpret_cast<Pack<T, L::W>*>(out + e0) = p;
+      } else {
+#pragma unroll
+        for (int w = 0; w < L::W; ++w)
+          if (e0 + w < E) out[e0 + w] = p.v[w];
+      }
+    }
+  }
+}
+
+// The kernels for a type and an E: 16 lanes per row up to 256 experts (a DPP
+// row, so that every reduction stays in registers), 64 above.
+typedef void (*RowsFn)(RouteArgs);
+typedef void (*BwdFn)(RouteBwdArgs);
+struct Pick {
+  RowsFn rows;
+  BwdFn bwd;
+  int rows_at_once;
+};
+template <typename T>
+Pick pick_for(int E) {
+#define FP8G_PICK(LPR_, VPT_)                                                     \
+  Pick { route_rows_kernel<T, LPR_, VPT_>, route_backward_kernel<T, LPR_, VPT_>,  \
+         THREADS / LPR_ }
+  if (E <= 16) return FP8G_PICK(16, 1);
+  if (E <= 32) return FP8G_PICK(16, 2);
+  if (E <= 64) return FP8G_PICK(16, 4);
+  if (E <= 128) return FP8G_PICK(16, 8);
+  if (E <= 256) return FP8G_PICK(16, 16);
+  if (E <= 512) return FP8G_PICK(64, 8);
+  return FP8G_PICK(64, 16);
+#undef FP8G_PICK
+}
+Pick pick(int type, int E) {
+  return type == TYPE_F32 ? pick_for<float>(E) : type == TYPE_BF16 ? pick_for<bf16_t>(E)
+                                                                   : pick_for<f16_t>(E);
+}
+
+bool vec_ok(const void* p, int64_t ld, int type) {
+  const int64_t size = type == TYPE_F32 ? 4 : 2;
+  return (uintptr_t)p % 16 == 0 && ld * size % 16 == 0;
+}
+
+}  // namespace
+
+int64_t route_blocks(int64_t T) { return (T + ROWS - 1) / ROWS; }
+
+size_t route_workspace_bytes(int64_t T, int E) {
+  const int64_t nblk = route_blocks(T);
+  if (nblk <= 1) return 0;
+  return ((size_t)nblk * (E + 1) * sizeof(int) + 15) / 16 * 16 + (size_t)nblk * E * sizeof(float);
+}
+
+hipError_t launch_route(const RouteCall& c, hipStream_t stream) {
+  RouteArgs a;
+  a.logits = c.logits;
+  a.mask = c.mask;
+  a.T = c.T;
+  a.ld = c.ld;
+  a.max_m = c.max_m;
+  a.E = c.E;
+  a.k = c.k;
+  a.renorm = c.renorm;
+  a.align = c.align;
+  a.vec = vec_ok(c.logits, c.ld, c.type);
+  a.coef = c.coef;
+  a.ids = c.ids;
+  a.counts = c.counts;
+  a.routed = c.routed;
+  a.offsets = c.offsets;
+  a.slots = c.slots;
+  a.weights = c.weights;
+  a.prob_sum = c.prob_sum;
+  a.loss = c.loss;
+  const int64_t nblk = route_blocks(c.T);
+  a.part_count = (int*)c.workspace;
+  a.part_prob = nblk > 1 ? (float*)((char*)c.workspace +
+                                    ((size_t)nblk * (c.E + 1) * sizeof(int) + 15) / 16 * 16)
+                         : nullptr;
+  if (nblk == 0) {
+    route_empty_kernel<<<dim3(1), dim3(THREADS), 0, stream>>>(a);
+    return hipGetLastError();
+  }
+  pick(c.type, c.E).rows<<<dim3((unsigned)nblk), dim3(THREADS), 0, stream>>>(a);
+  if (nblk > 1) {
+    route_scan_kernel<<<dim3((unsigned)(c.E / 64 + 1)), dim3(64 * RUNS), 0, stream>>>(a, (int)nblk);
+    const int64_t grid = (c.T * c.k + PAIRS - 1) / PAIRS;
+    route_slots_kernel<<<dim3((unsigned)grid), dim3(THREADS), 0, stream>>>(a);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_route_backward(const RouteBwdCall& c, hipStream_t stream, int cu_count) {
+  RouteBwdArgs a;
+  a.logits = c.logits;
+  a.d_logits = c.d_logits;
+  a.ids = c.ids;
+  a.counts = c.counts;
+  a.routed = c.routed;
+  a.dw = c.dw;
+  a.dloss = c.dloss;
+  a.T = c.T;
+  a.ld = c.ld;
+  a.ldd = c.ldd;
+  a.E = c.E;
+  a.k = c.k;
+  a.renorm = c.renorm;
+  a.vec = vec_ok(c.logits, c.ld, c.type) && vec_ok(c.d_logits, c.ldd, c.type);
+  a.coef = c.coef;
+  const Pick p = pick(c.type, c.E);
+  int64_t grid = (c.T + p.rows_at_once - 1) / p.rows_at_once;
+  if (grid > (int64_t)cu_count * 8) grid = (int64_t)cu_count * 8;
+  p.bwd<<<dim3((unsigned)grid), dim3(THREADS), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+void route_kernels(std::vector<const void*>& out) {
+  for (int type : {TYPE_F32, TYPE_BF16, TYPE_F16})
+    for (int E : {16, 32, 64, 128, 256, 512, 1024}) {
+      const Pick p = pick(type, E);
+      out.push_back((const void*)p.rows);
+      out.push_back((const void*)p.bwd);
+    }
+  out.push_back((const void*)route_scan_kernel);
+  out.push_back((const void*)route_slots_kernel);
+  out.push_back((const void*)route_empty_kernel);
+}
+
+}  // namespace fp8g
