@@ -5,9 +5,11 @@
 // exponent bytes, so its fp32 accumulator holds the true sum over all tokens
 // and no vector instruction touches it before the final rounding to bf16.
 
+#include <type_traits>
 #include <vector>
 
 #include "elem.h"
+#include "gemm_index.h"
 #include "internal.h"
 
 namespace fp8g {
@@ -243,6 +245,342 @@ wgrad_kernel(WgradArgs a, int mblocks, int nblocks) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// 256x256 tiles: four waves of 128x128, one per SIMD, the 256 accumulators
+// of a lane in the accumulation registers (nothing but the matrix unit
+// touches them until the end, since the scales go into the instruction). Per
+// 128 tokens a wave reads (128 + 128) x 128 bytes of LDS for 64 matrix
+// instructions of 32 cycles: 64 bytes a cycle and CU, with the 32 of the
+// copies into LDS three quarters of what the LDS moves; eight waves of
+// 64x128 would need all of it.
+//
+// A workgroup walks tiles (expert, row block, column block); the 128-token
+// steps of all its tiles form one sequence with two LDS stages. A step, by
+// its eight slices of eight matrix instructions (one 16-row fragment of b
+// against all eight of a):
+//   slices 0-2  read the rest of the step's b fragments
+//   slice 4     wait for the next step's copies, barrier (everyone is done
+//               with this stage), then issue the copies of the step after next
+//               into it, and up to slice 7 read the next step's a fragments
+//               and first b fragments
+// so that every read has about a slice, and every copy a step, to arrive.
+//
+// Which global row lies in which LDS row is free, as each lane of a copy has
+// its own address. The rows of a 128-row band are dealt so that
+//   a: position r of fragment i is row 8 r + i: one 8-byte LDS read gives a
+//      lane the exponent bytes of its eight fragments;
+//   b: position 4 g + e of fragment j is row 32 e + 8 g + j: likewise, and a
+//      lane then ends up with 8 adjacent columns (j) of a row for each e, and
+//      the lanes of the four g with 64 adjacent bytes: no exchange between lanes is
+//      needed before the store.
+
+constexpr int TS = 256;                                // tile side
+constexpr int STAGE = 2 * TS * 128 + 2 * TS;           // codes of a and b, then their exponent bytes
+constexpr int COPIES = 17;                             // a wave's copies of a stage: 8 + 8, and one of exponents
+constexpr int STORES = 32;                             // a wave's stores of a full tile
+constexpr int MAX_G = 1024;
+
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr_t)p);
+}
+// Direct global -> LDS copies, through inline assembly so that the compiler
+// does not wait for all of them before the next LDS read; the waits are
+// explicit (the barrier of slice 4).
+__device__ __forceinline__ void copy16(const void* base, uint32_t voff, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "{m0}"(lds)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(const void* base, uint32_t voff, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "{m0}"(lds)
+               : "memory");
+}
+constexpr int vmcnt_only(int n) { return (n & 0xF) | (0x7 << 4) | (0xF << 8) | (((n >> 4) & 3) << 14); }
+
+// The experts that have tokens, in order, and those that have none.
+struct Experts {
+  int full[MAX_G], kb0[MAX_G], steps[MAX_G];
+  int empty[MAX_G];
+  int nfull, nempty;
+};
+
+struct Tile {
+  const uint8_t *a, *b, *sa, *sb;                      // first row, first token block
+  uint16_t* d;
+  int mv, nv, steps;                                   // rows and columns that exist
+};
+
+// Chunk swizzle of an LDS row of 128 bytes (16-byte chunks): fragment reads
+// of 16 consecutive rows meet every bank group equally.
+__device__ __forceinline__ int swz(int row, int chunk) {
+  return chunk ^ (row & 7) ^ ((row >> 3) & 1);
+}
+
+__device__ __forceinline__ void tile_of(const WgradArgs& a, const Experts& ex, int slot, int mblocks,
+                                        int nblocks, Tile& t) {
+  const int per = mblocks * nblocks;
+  const int at = __builtin_amdgcn_readfirstlane(slot / per);
+  int mb, nb;
+  gidx::swizzle_tile(slot - at * per, mblocks, nblocks, 4, mb, nb);
+  const int g = __builtin_amdgcn_readfirstlane(ex.full[at]);
+  const int64_t kb0 = __builtin_amdgcn_readfirstlane(ex.kb0[at]);
+  const int64_t m0 = (int64_t)mb * TS, n0 = (int64_t)nb * TS;
+  t.steps = __builtin_amdgcn_readfirstlane(ex.steps[at]);
+  t.mv = (int)min((int64_t)TS, a.M - m0);
+  t.nv = (int)min((int64_t)TS, a.N - n0);
+  t.a = a.a + m0 * a.lda + kb0 * 128;
+  t.b = a.b + n0 * a.ldb + kb0 * 128;
+  t.sa = a.sa + kb0 * a.M + m0;
+  t.sb = a.sb + kb0 * a.N + n0;
+  t.d = a.d + ((int64_t)g * a.M + m0) * a.N + n0;
+}
+
+// This lane's copy offsets for a tile. Wave w copies the LDS rows of band
+// w / 2 whose position has bit 3 = w % 2; copy i of them is fragment i. Rows
+// past the tile's last are copies of it (read in bounds, never stored).
+struct Plan {
+  uint32_t va, ma, vb, mb;                             // fragment 0's offset, the last row's
+  uint32_t vs;
+};
+__device__ __forceinline__ void make_plan(Plan& p, const WgradArgs& a, const Tile& t, int wave,
+                                          int lane) {
+  const int band = wave >> 1, h = wave & 1, r = h * 8 + (lane >> 3);
+  const uint32_t ch = (uint32_t)((lane & 7) ^ (lane >> 3) ^ h) * 16u;
+  const int ra = band * 128 + r * 8, rb = band * 128 + (r & 3) * 32 + (r >> 2) * 8;
+  p.va = (uint32_t)ra * (uint32_t)a.lda + ch;
+  p.vb = (uint32_t)rb * (uint32_t)a.ldb + ch;
+  p.ma = (uint32_t)(t.mv - 1) * (uint32_t)a.lda + ch;
+  p.mb = (uint32_t)(t.nv - 1) * (uint32_t)a.ldb + ch;
+  p.vs = (uint32_t)min(lane * 4, (h ? t.nv : t.mv) - 4);
+}
+
+// Copies [c0, c1) of a wave's share of a stage (the last is of exponents:
+// waves 0 and 2 a's, 1 and 3 b's, twice the same bytes).
+__device__ __forceinline__ void issue(const Plan& p, const WgradArgs& a, const Tile& t, int kb,
+                                      uint32_t stage, int wave, int c0, int c1) {
+  const uint32_t dst = stage + (uint32_t)((wave >> 1) * 16 + (wave & 1)) * 1024u;
+  const uint8_t* const ka = t.a + (int64_t)kb * 128;
+  const uint8_t* const kb_ = t.b + (int64_t)kb * 128;
+  // (opaque: formed at each copy, the 16 offsets would otherwise be kept in
+  // registers that the fragments need)
+  uint32_t lda = (uint32_t)a.lda, ldb = (uint32_t)a.ldb;
+  asm volatile("" : "+s"(lda), "+s"(ldb));
+#pragma unroll
+  for (int c = c0; c < c1; ++c) {
+    if (c < 8) copy16(ka, min(p.va + (uint32_t)c * lda, p.ma), dst + (uint32_t)c * 2048u);
+    else if (c < 16)
+      copy16(kb_, min(p.vb + (uint32_t)(c - 8) * ldb, p.mb),
+             dst + TS * 128 + (uint32_t)(c - 8) * 2048u);
+    else
+      copy4((wave & 1) ? t.sb + (int64_t)kb * a.N : t.sa + (int64_t)kb * a.M, p.vs,
+            stage + 2 * TS * 128 + (wave & 1) * TS);
+  }
+}
+
+__device__ __forceinline__ v8i read_frag(const uint8_t* band, int f, int lane) {
+  const int r = f * 16 + (lane & 15), c = (lane >> 4) * 2;
+  const uint4 lo = *reinterpret_cast<const uint4*>(band + r * 128 + swz(r, c) * 16);
+  const uint4 hi = *reinterpret_cast<const uint4*>(band + r * 128 + swz(r, c + 1) * 16);
+  v8i v;
+  v[0] = (int)lo.x; v[1] = (int)lo.y; v[2] = (int)lo.z; v[3] = (int)lo.w;
+  v[4] = (int)hi.x; v[5] = (int)hi.y; v[6] = (int)hi.z; v[7] = (int)hi.w;
+  return v;
+}
+
+// Fragments j of b and i of a; byte j & 3 of the register that holds the
+// exponents of fragments 4 (j / 4) .. +3, and the same for a. (i and j are
+// constants where this is inlined.)
+template <int FA, int FB>
+__device__ __forceinline__ v4f mfma(const v8i& b, const v8i& a, v4f c, int j, const uint2& sb, int i,
+                                    const uint2& sa) {
+  const int xb = (int)(j < 4 ? sb.x : sb.y), xa = (int)(i < 4 ? sa.x : sa.y);
+#define FP8G_M(J_, I_)                                                                          \
+  case J_ * 4 + I_:                                                                             \
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, FB, FA, J_, xb, I_, xa);
+#define FP8G_M4(J_) FP8G_M(J_, 0) FP8G_M(J_, 1) FP8G_M(J_, 2) FP8G_M(J_, 3)
+  switch ((j & 3) * 4 + (i & 3)) {
+    FP8G_M4(0) FP8G_M4(1) FP8G_M4(2) FP8G_M4(3)
+  }
+#undef FP8G_M4
+#undef FP8G_M
+  return c;
+}
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+template <int FA, int FB>
+__global__ void __launch_bounds__(256, 1)
+wgrad_tile_kernel(WgradArgs a, int mblocks, int nblocks, int xcd_remap) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
+  __shared__ Experts ex;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int grid = gridDim.x, w = blockIdx.x;
+  if (wave == 0) {
+    int nf = 0, ne = 0;
+    for (int g0 = 0; g0 < a.G; g0 += 64) {
+      const int g = g0 + lane;
+      int kb0 = 0, kb1 = 0;
+      if (g < a.G) token_blocks(a, g, kb0, kb1);
+      const bool has = kb1 > kb0, none = g < a.G && !has;
+      const uint64_t mf = __ballot(has), me = __ballot(none);
+      const uint64_t below = (1ull << lane) - 1;
+      if (has) {
+        const int i = nf + __popcll(mf & below);
+        ex.full[i] = g;
+        ex.kb0[i] = kb0;
+        ex.steps[i] = kb1 - kb0;
+      }
+      if (none) ex.empty[ne + __popcll(me & below)] = g;
+      nf += __popcll(mf);
+      ne += __popcll(me);
+    }
+    if (lane == 0) {
+      ex.nfull = nf;
+      ex.nempty = ne;
+    }
+  }
+  __syncthreads();
+  const int per = mblocks * nblocks;
+  const int nfull = __builtin_amdgcn_readfirstlane(ex.nfull);
+  const int nempty = __builtin_amdgcn_readfirstlane(ex.nempty);
+  // experts without tokens: zeros, row by row
+  for (int64_t r = w; r < (int64_t)nempty * a.M; r += grid) {
+    const int g = ex.empty[r / a.M];
+    uint16_t* row = a.d + ((int64_t)g * a.M + r % a.M) * a.N;
+    for (int64_t n = threadIdx.x * 8; n < a.N; n += 256 * 8)
+      __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, reinterpret_cast<u32x4*>(row + n));
+  }
+  const int tiles = nfull * per;
+  const int first = xcd_remap ? (w & 7) * (grid >> 3) + (w >> 3) : w;
+  if (first >= tiles) return;
+  int total = 0;
+  for (int s = first; s < tiles; s += grid)
+    total += __builtin_amdgcn_readfirstlane(ex.steps[s / per]);
+
+  const int wm = wave >> 1, wn = wave & 1;
+  const uint32_t base = lds_addr(lds);
+  // copy cursor
+  int p_slot = first, p_kb = 0, issued = 0;
+  Tile tp;
+  tile_of(a, ex, p_slot, mblocks, nblocks, tp);
+  Plan pl;
+  make_plan(pl, a, tp, wave, lane);
+  auto advance = [&]() __attribute__((always_inline)) {
+    ++issued;
+    if (++p_kb == tp.steps) {
+      p_kb = 0;
+      p_slot += grid;
+      if (p_slot < tiles) {
+        tile_of(a, ex, p_slot, mblocks, nblocks, tp);
+        make_plan(pl, a, tp, wave, lane);
+      }
+    }
+  };
+  for (int s = 0; s < 2 && issued < total; ++s) {
+    issue(pl, a, tp, p_kb, base + s * STAGE, wave, 0, COPIES);
+    advance();
+  }
+  v4f acc[8][8];
+  v8i af[8], bf[8];              // fragments of a and b
+  uint2 sa, sb, sa_n, sb_n;      // their exponent bytes
+  const int r16 = lane & 15, g4 = lane >> 4;
+  const int ea = 2 * TS * 128 + wm * 128 + r16 * 8;
+  const int eb = 2 * TS * 128 + TS + wn * 128 + (r16 & 3) * 32 + (r16 >> 2) * 8;
+  const int oa = wm * 128 * 128, ob = TS * 128 + wn * 128 * 128;
+  if (issued > 1) __builtin_amdgcn_s_waitcnt(vmcnt_only(COPIES));
+  else __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) af[i] = read_frag(lds + oa, i, lane);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) bf[j] = read_frag(lds + ob, j, lane);
+  sa = *reinterpret_cast<const uint2*>(lds + ea);
+  sb = *reinterpret_cast<const uint2*>(lds + eb);
+
+  bool fresh = false;   // the last tile's stores may still be on their way
+  int s = 0;            // step, over all tiles
+  for (int slot = first; slot < tiles; slot += grid) {
+    Tile tc;
+    tile_of(a, ex, slot, mblocks, nblocks, tc);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < tc.steps; ++k, ++s) {
+      const uint8_t* __restrict__ cur = lds + (s & 1) * STAGE;
+      const uint8_t* __restrict__ nxt = lds + ((s & 1) ^ 1) * STAGE;
+      const bool more = issued < total;
+      // first half: fragments 0-3 of b, each against all of a; read b's 4-7
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        bf[4 + j] = read_frag(cur + ob, 4 + j, lane);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          acc[i][j] = mfma<FA, FB>(bf[j], af[i], acc[i][j], j, sb, i, sa);
+          // (a pure instruction: without this it is moved to where it is used)
+          asm volatile("" : "+a"(acc[i][j]));
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // LDS read
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     // matrix instruction
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0): this stage is read
+      // (the stores of the tile before are newer than the copies waited for)
+      if (fresh) __builtin_amdgcn_s_waitcnt(vmcnt_only(STORES));
+      else __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+      fresh = false;
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("s_barrier" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      // second half: each fragment of a against 4-7 of b, after which the
+      // next step's takes its place; the stage is refilled meanwhile
+      sa_n = *reinterpret_cast<const uint2*>(nxt + ea);
+      sb_n = *reinterpret_cast<const uint2*>(nxt + eb);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i < 4) bf[i] = read_frag(nxt + ob, i, lane);
+#pragma unroll
+        for (int j = 4; j < 8; ++j) {
+          acc[i][j] = mfma<FA, FB>(bf[j], af[i], acc[i][j], j, sb, i, sa);
+          asm volatile("" : "+a"(acc[i][j]));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        af[i] = read_frag(nxt + oa, i, lane);
+        if (more) {
+          // (three copies in each of the first five parts, two in the sixth)
+          if (i < 6) issue(pl, a, tp, p_kb, base + (s & 1) * STAGE, wave, 3 * i, min(3 * i + 3, COPIES));
+          if (i == 6) advance();
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      sa = sa_n;
+      sb = sb_n;
+    }
+    fresh = tc.mv == TS && tc.nv == TS;
+    // lane (g4, r16): row 8 r16 + i of the wave's band, columns 32 e + 8 g4 + 0..7
+    uint16_t* const d0 = tc.d + (int64_t)(wm * 128 + r16 * 8) * a.N + wn * 128 + g4 * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint16_t* const to = d0 + (int64_t)i * a.N;
+      const bool row = wm * 128 + r16 * 8 + i < tc.mv;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        Pack<bf16_t, 8> o;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o.v[j] = from_f32<bf16_t>(acc[i][j][e]);
+        if (fresh || (row && wn * 128 + e * 32 + g4 * 8 < tc.nv))
+          *reinterpret_cast<u32x4*>(to + e * 32) = __builtin_bit_cast(u32x4, o);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
 template <typename T>
 void (*quant_kernel(int fmt))(const T*, int64_t, int64_t, int64_t, int, uint8_t*, int64_t,
                               uint8_t*) {
@@ -260,6 +598,11 @@ hipError_t quant_launch(const void* x, int64_t rows, int64_t cols, int64_t ldx, 
   return hipGetLastError();
 }
 
+typedef void (*TileFn)(WgradArgs, int, int, int);
+TileFn tile_pick(int fa, int fb) {
+  if (fa == FMT_E4M3) return fb == FMT_E4M3 ? wgrad_tile_kernel<0, 0> : wgrad_tile_kernel<0, 1>;
+  return fb == FMT_E4M3 ? wgrad_tile_kernel<1, 0> : wgrad_tile_kernel<1, 1>;
+}
 typedef void (*WgradFn)(WgradArgs, int, int);
 WgradFn wgrad_pick(int fa, int fb) {
   if (fa == FMT_E4M3) return fb == FMT_E4M3 ? wgrad_kernel<0, 0> : wgrad_kernel<0, 1>;
@@ -276,8 +619,15 @@ hipError_t launch_quantize_transpose(const void* x, int type, int64_t rows, int6
   return quant_launch<f16_t>(x, rows, cols, ldx, fmt, qt, ldq, st, stream);
 }
 
-hipError_t launch_wgrad(const WgradArgs& args, int fmt_a, int fmt_b, const DeviceInfo&,
+hipError_t launch_wgrad(const WgradArgs& args, int fmt_a, int fmt_b, const DeviceInfo& dev,
                         hipStream_t stream) {
+  const int64_t mb = (args.M + TS - 1) / TS, nb = (args.N + TS - 1) / TS, all = mb * nb * args.G;
+  if (all >= dev.cu_count / 2 && args.T > 0) {
+    const int64_t grid = all < dev.cu_count ? all : dev.cu_count;
+    tile_pick(fmt_a, fmt_b)<<<dim3((unsigned)grid), dim3(256), 0, stream>>>(
+        args, (int)mb, (int)nb, grid % 8 == 0 ? 1 : 0);
+    return hipGetLastError();
+  }
   const int64_t mblocks = (args.M + BT - 1) / BT, nblocks = (args.N + BT - 1) / BT;
   wgrad_pick(fmt_a, fmt_b)<<<dim3((unsigned)(mblocks * nblocks * args.G)), dim3(256), 0, stream>>>(
       args, (int)mblocks, (int)nblocks);
@@ -289,7 +639,10 @@ void wgrad_kernels(std::vector<const void*>& out) {
     out.push_back((const void*)quant_kernel<float>(fmt));
     out.push_back((const void*)quant_kernel<bf16_t>(fmt));
     out.push_back((const void*)quant_kernel<f16_t>(fmt));
-    for (int fb : {FMT_E4M3, FMT_E5M2}) out.push_back((const void*)wgrad_pick(fmt, fb));
+    for (int fb : {FMT_E4M3, FMT_E5M2}) {
+      out.push_back((const void*)wgrad_pick(fmt, fb));
+      out.push_back((const void*)tile_pick(fmt, fb));
+    }
   }
 }
 

@@ -242,3 +242,13 @@ def test_gradient_of_a_product_against_differences():
             dn[m, n] -= 0.5
             # (the sum is linear; bf16's rounding of an integer up to 2048)
             assert abs((f(up) - f(dn)) - d[m, n]) <= BF16 * abs(d[m, n]) + 1e-9
+
+
+@pytest.mark.parametrize("counts,M,N", [([300], 4096, 2304), ([130, 0, 500, 128, 0], 1040, 2064),
+                                        ([128] * 5 + [0, 1000], 1296, 1808), ([1] * 33, 512, 784)])
+def test_enough_tiles_for_the_large_kernel(counts, M, N):
+    ends = np.concatenate([[0], np.cumsum([-(-c // 128) * 128 for c in counts])]).astype(int)
+    banner(f"wgrad large counts={counts} M={M} N={N}")
+    ops = operands(int(ends[-1]), M, N, "e5m2", "e4m3", seed=len(counts))
+    d = product(ops, M, N, None if len(counts) == 1 else ends, len(counts))
+    check_product(ops, d, ends)
