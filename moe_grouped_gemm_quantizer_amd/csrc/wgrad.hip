@@ -277,6 +277,8 @@ wgrad_kernel(WgradArgs a, int mblocks, int nblocks) {
 constexpr int TS = 256;                                // tile side
 constexpr int STAGE = 2 * TS * 128 + 2 * TS;           // codes of a and b, then their exponent bytes
 constexpr int COPIES = 17;                             // a wave's copies of a stage: 8 + 8, and one of exponents
+constexpr int EARLY = 13;                              // those that are read a step ahead,
+constexpr int EARLY_FIRST = 8;                         // of these, issued in a step's first half
 constexpr int STORES = 32;                             // a wave's stores of a full tile
 constexpr int MAX_G = 1024;
 
@@ -354,26 +356,23 @@ __device__ __forceinline__ void make_plan(Plan& p, const WgradArgs& a, const Til
   p.vs = (uint32_t)min(lane * 4, (h ? t.nv : t.mv) - 4);
 }
 
-// Copies [c0, c1) of a wave's share of a stage (the last is of exponents:
-// waves 0 and 2 a's, 1 and 3 b's, twice the same bytes).
+// Copy c of a wave's share of a stage: a's eight fragments, b's 0-3, the
+// exponents (waves 0 and 2 a's, 1 and 3 b's, twice the same bytes), b's 4-7.
 __device__ __forceinline__ void issue(const Plan& p, const WgradArgs& a, const Tile& t, int kb,
-                                      uint32_t stage, int wave, int c0, int c1) {
+                                      uint32_t stage, int wave, int c) {
   const uint32_t dst = stage + (uint32_t)((wave >> 1) * 16 + (wave & 1)) * 1024u;
-  const uint8_t* const ka = t.a + (int64_t)kb * 128;
-  const uint8_t* const kb_ = t.b + (int64_t)kb * 128;
   // (opaque: formed at each copy, the 16 offsets would otherwise be kept in
   // registers that the fragments need)
   uint32_t lda = (uint32_t)a.lda, ldb = (uint32_t)a.ldb;
   asm volatile("" : "+s"(lda), "+s"(ldb));
-#pragma unroll
-  for (int c = c0; c < c1; ++c) {
-    if (c < 8) copy16(ka, min(p.va + (uint32_t)c * lda, p.ma), dst + (uint32_t)c * 2048u);
-    else if (c < 16)
-      copy16(kb_, min(p.vb + (uint32_t)(c - 8) * ldb, p.mb),
-             dst + TS * 128 + (uint32_t)(c - 8) * 2048u);
-    else
-      copy4((wave & 1) ? t.sb + (int64_t)kb * a.N : t.sa + (int64_t)kb * a.M, p.vs,
-            stage + 2 * TS * 128 + (wave & 1) * TS);
+  if (c < 8) {
+    copy16(t.a + (int64_t)kb * 128, min(p.va + (uint32_t)c * lda, p.ma), dst + (uint32_t)c * 2048u);
+  } else if (c == 12) {
+    copy4((wave & 1) ? t.sb + (int64_t)kb * a.N : t.sa + (int64_t)kb * a.M, p.vs,
+          stage + 2 * TS * 128 + (wave & 1) * TS);
+  } else {
+    const uint32_t j = c < 12 ? c - 8 : c - 9;
+    copy16(t.b + (int64_t)kb * 128, min(p.vb + j * ldb, p.mb), dst + TS * 128 + j * 2048u);
   }
 }
 
@@ -454,31 +453,32 @@ wgrad_tile_kernel(WgradArgs a, int mblocks, int nblocks, int xcd_remap) {
   const int tiles = nfull * per;
   const int first = xcd_remap ? (w & 7) * (grid >> 3) + (w >> 3) : w;
   if (first >= tiles) return;
-  int total = 0;
-  for (int s = first; s < tiles; s += grid)
-    total += __builtin_amdgcn_readfirstlane(ex.steps[s / per]);
-
   const int wm = wave >> 1, wn = wave & 1;
   const uint32_t base = lds_addr(lds);
   // copy cursor
-  int p_slot = first, p_kb = 0, issued = 0;
+  int p_slot = first, p_kb = 0;
   Tile tp;
   tile_of(a, ex, p_slot, mblocks, nblocks, tp);
   Plan pl;
   make_plan(pl, a, tp, wave, lane);
   auto advance = [&]() __attribute__((always_inline)) {
-    ++issued;
+    // (past the last step it stays there: two stages are copied once more at
+    // the end, for nothing, and every wait may count on the same copies)
     if (++p_kb == tp.steps) {
-      p_kb = 0;
-      p_slot += grid;
-      if (p_slot < tiles) {
+      if (p_slot + grid < tiles) {
+        p_kb = 0;
+        p_slot += grid;
         tile_of(a, ex, p_slot, mblocks, nblocks, tp);
         make_plan(pl, a, tp, wave, lane);
+      } else {
+        --p_kb;
       }
     }
   };
-  for (int s = 0; s < 2 && issued < total; ++s) {
-    issue(pl, a, tp, p_kb, base + s * STAGE, wave, 0, COPIES);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+#pragma unroll
+    for (int c = 0; c < COPIES; ++c) issue(pl, a, tp, p_kb, base + s * STAGE, wave, c);
     advance();
   }
   v4f acc[8][8];
@@ -488,8 +488,7 @@ wgrad_tile_kernel(WgradArgs a, int mblocks, int nblocks, int xcd_remap) {
   const int ea = 2 * TS * 128 + wm * 128 + r16 * 8;
   const int eb = 2 * TS * 128 + TS + wn * 128 + (r16 & 3) * 32 + (r16 >> 2) * 8;
   const int oa = wm * 128 * 128, ob = TS * 128 + wn * 128 * 128;
-  if (issued > 1) __builtin_amdgcn_s_waitcnt(vmcnt_only(COPIES));
-  else __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+  __builtin_amdgcn_s_waitcnt(vmcnt_only(2 * COPIES - EARLY));
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_barrier" ::: "memory");
 #pragma unroll
@@ -499,7 +498,21 @@ wgrad_tile_kernel(WgradArgs a, int mblocks, int nblocks, int xcd_remap) {
   sa = *reinterpret_cast<const uint2*>(lds + ea);
   sb = *reinterpret_cast<const uint2*>(lds + eb);
 
-  bool fresh = false;   // the last tile's stores may still be on their way
+  // Two points of a step where everyone waits for copies and meets: after
+  // slice 0 for b's late fragments of this step, half way for the early part of
+  // the next. N copies have been issued since those; for three points after
+  // a full tile its stores are newer too.
+  int fresh = 0;
+  auto meet = [&](auto n) __attribute__((always_inline)) {
+    constexpr int N = decltype(n)::value;
+    __builtin_amdgcn_s_waitcnt(0xC07F);                // lgkmcnt(0): own reads have arrived
+    if (fresh > 0) __builtin_amdgcn_s_waitcnt(vmcnt_only(N + STORES));
+    else __builtin_amdgcn_s_waitcnt(vmcnt_only(N));
+    --fresh;
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
   int s = 0;            // step, over all tiles
   for (int slot = first; slot < tiles; slot += grid) {
     Tile tc;
@@ -511,34 +524,26 @@ wgrad_tile_kernel(WgradArgs a, int mblocks, int nblocks, int xcd_remap) {
     for (int k = 0; k < tc.steps; ++k, ++s) {
       const uint8_t* __restrict__ cur = lds + (s & 1) * STAGE;
       const uint8_t* __restrict__ nxt = lds + ((s & 1) ^ 1) * STAGE;
-      const bool more = issued < total;
-      // first half: fragments 0-3 of b, each against all of a; read b's 4-7
+      const uint32_t stage = base + (s & 1) * STAGE;
+      // first half: fragments 0-3 of b, each against all of a
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        bf[4 + j] = read_frag(cur + ob, 4 + j, lane);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+          // (one read or copy between two matrix instructions at most: a
+          // run of them would leave the matrix unit waiting)
+          if ((j == 1 || j == 2) && i % 4 == 0) bf[2 * j + 2 + i / 4] = read_frag(cur + ob, 2 * j + 2 + i / 4, lane);
           acc[i][j] = mfma<FA, FB>(bf[j], af[i], acc[i][j], j, sb, i, sa);
           // (a pure instruction: without this it is moved to where it is used)
           asm volatile("" : "+a"(acc[i][j]));
+          const int m = (j - 1) * 8 + i;
+          if (j > 0 && m % 3 == 2) issue(pl, a, tp, p_kb, stage, wave, m / 3);
         }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // LDS read
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     // matrix instruction
-        }
-        __builtin_amdgcn_sched_barrier(0);
+        if (j == 0) meet(std::integral_constant<int, COPIES>{});
       }
-      __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0): this stage is read
-      // (the stores of the tile before are newer than the copies waited for)
-      if (fresh) __builtin_amdgcn_s_waitcnt(vmcnt_only(STORES));
-      else __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
-      fresh = false;
-      __builtin_amdgcn_sched_barrier(0);
-      asm volatile("s_barrier" ::: "memory");
-      __builtin_amdgcn_sched_barrier(0);
+      meet(std::integral_constant<int, COPIES - EARLY + EARLY_FIRST>{});
       // second half: each fragment of a against 4-7 of b, after which the
-      // next step's takes its place; the stage is refilled meanwhile
+      // next step's takes its place
       sa_n = *reinterpret_cast<const uint2*>(nxt + ea);
       sb_n = *reinterpret_cast<const uint2*>(nxt + eb);
 #pragma unroll
@@ -548,20 +553,18 @@ wgrad_tile_kernel(WgradArgs a, int mblocks, int nblocks, int xcd_remap) {
         for (int j = 4; j < 8; ++j) {
           acc[i][j] = mfma<FA, FB>(bf[j], af[i], acc[i][j], j, sb, i, sa);
           asm volatile("" : "+a"(acc[i][j]));
+          const int m = i * 4 + j - 4;
+          if (m % 3 == 2 && m / 3 < COPIES - EARLY_FIRST)
+            issue(pl, a, tp, p_kb, stage, wave, EARLY_FIRST + m / 3);
         }
-        __builtin_amdgcn_sched_barrier(0);
         af[i] = read_frag(nxt + oa, i, lane);
-        if (more) {
-          // (three copies in each of the first five parts, two in the sixth)
-          if (i < 6) issue(pl, a, tp, p_kb, base + (s & 1) * STAGE, wave, 3 * i, min(3 * i + 3, COPIES));
-          if (i == 6) advance();
-        }
-        __builtin_amdgcn_sched_barrier(0);
       }
+      advance();
       sa = sa_n;
       sb = sb_n;
     }
-    fresh = tc.mv == TS && tc.nv == TS;
+    const bool full = tc.mv == TS && tc.nv == TS;
+    fresh = full ? 3 : 0;
     // lane (g4, r16): row 8 r16 + i of the wave's band, columns 32 e + 8 g4 + 0..7
     uint16_t* const d0 = tc.d + (int64_t)(wm * 128 + r16 * 8) * a.N + wn * 128 + g4 * 8;
 #pragma unroll
@@ -573,12 +576,14 @@ wgrad_tile_kernel(WgradArgs a, int mblocks, int nblocks, int xcd_remap) {
         Pack<bf16_t, 8> o;
 #pragma unroll
         for (int j = 0; j < 8; ++j) o.v[j] = from_f32<bf16_t>(acc[i][j][e]);
-        if (fresh || (row && wn * 128 + e * 32 + g4 * 8 < tc.nv))
+        if (full || (row && wn * 128 + e * 32 + g4 * 8 < tc.nv))
           *reinterpret_cast<u32x4*>(to + e * 32) = __builtin_bit_cast(u32x4, o);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   }
+  // (no copy may arrive after the workgroup's LDS is someone else's)
+  __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
 }
 
 template <typename T>
