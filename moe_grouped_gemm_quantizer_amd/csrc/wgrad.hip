@@ -43,92 +43,184 @@ __device__ __forceinline__ int block_exponent(float amax) {
   return amax > 0.0f ? e : 0;
 }
 
-// Two codes from two values that are at most FP8max in magnitude, or NaN or
-// infinite; see the header for what those become.
+// Code of x 2^-e for an x that may be NaN or infinite.
 template <int FMT>
-__device__ __forceinline__ uint32_t code_pair(float x, float y) {
-  uint32_t w;
+__device__ __forceinline__ uint32_t code_any(float x, float down) {
+  const uint32_t sign = (__float_as_uint(x) >> 24) & 0x80u;
+  if (x != x) return sign | 0x7Fu;
+  if (__builtin_fabsf(x) == __builtin_inff()) return sign | (FMT == FMT_E4M3 ? 0x7Fu : 0x7Cu);
+  const float y = x * down;
   if constexpr (FMT == FMT_E4M3)
-    w = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x, y, 0, false) & 0xFFFFu;
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y, y, 0, false) & 0xFFu;
   else
-    w = (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(x, y, 0, false) & 0xFFFFu;
-  const float lim = FMT == FMT_E4M3 ? 448.0f : 57344.0f;
-  if (__builtin_expect(!(__builtin_fabsf(x) <= lim) || !(__builtin_fabsf(y) <= lim), 0)) {
-    const uint32_t inf = FMT == FMT_E4M3 ? 0x7Fu : 0x7Cu;
-    const uint32_t sx = (__float_as_uint(x) >> 24) & 0x80u, sy = (__float_as_uint(y) >> 24) & 0x80u;
-    if (x != x) w = (w & 0xFF00u) | sx | 0x7Fu;
-    else if (!(__builtin_fabsf(x) <= lim)) w = (w & 0xFF00u) | sx | inf;
-    if (y != y) w = (w & 0xFFu) | (sy | 0x7Fu) << 8;
-    else if (!(__builtin_fabsf(y) <= lim)) w = (w & 0xFFu) | (sy | inf) << 8;
-  }
-  return w;
+    return (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(y, y, 0, false) & 0xFFu;
 }
+
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef bf16_t bf16x2 __attribute__((ext_vector_type(2)));
+typedef f16_t f16x2 __attribute__((ext_vector_type(2)));
+
+// What the quantiser does with 16 bytes of a row (W words of 32 bits, each
+// one fp32 or two 16-bit values). Magnitudes are compared as integers, two
+// 16-bit ones at a time. Adding BUMP to a magnitude's bits takes NaN and
+// infinity over the sign bit, below every finite value in a signed maximum.
+// Codes: gfx950 converts two values, divided by a power of two, at once and
+// rounds to nearest even; the values are finite there.
+template <typename T>
+struct Row16;
+template <>
+struct Row16<float> {
+  static constexpr int PER = 1;                        // values in a word
+  static constexpr uint32_t BUMP = 0x00800000u, TOP = 0x7F800000u;
+  __device__ static __forceinline__ uint32_t mag(uint32_t w) { return w & 0x7FFFFFFFu; }
+  __device__ static __forceinline__ uint32_t max_any(uint32_t a, uint32_t b) { return a > b ? a : b; }
+  __device__ static __forceinline__ uint32_t max_finite(uint32_t a, uint32_t b) {
+    return (int)a > (int)b ? a : b;
+  }
+  __device__ static __forceinline__ uint32_t bump(uint32_t m) { return m + BUMP; }
+  __device__ static __forceinline__ uint32_t field(uint32_t w, int) { return w; }
+  __device__ static __forceinline__ float value(uint32_t w, int) { return __uint_as_float(w); }
+  // codes of a column's values in words a and b into one half of `old`
+  template <int FMT, bool HI>
+  __device__ static __forceinline__ uint32_t codes(uint32_t old, uint32_t a, uint32_t b, int,
+                                                   float scale) {
+    const s16x2 o = __builtin_bit_cast(s16x2, old);
+    const float x = __uint_as_float(a), y = __uint_as_float(b);
+    if constexpr (FMT == FMT_E4M3)
+      return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, x, y, scale, HI));
+    else
+      return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(o, x, y, scale, HI));
+  }
+};
+template <typename T>
+struct Row16 {
+  static constexpr int PER = 2;
+  static constexpr uint32_t TOP = std::is_same<T, bf16_t>::value ? 0x7F80u : 0x7C00u;
+  static constexpr uint32_t BUMP = (0x8000u - TOP) * 0x10001u;
+  __device__ static __forceinline__ uint32_t mag(uint32_t w) { return w & 0x7FFF7FFFu; }
+  __device__ static __forceinline__ uint32_t max_any(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                  __builtin_bit_cast(u16x2, b)));
+  }
+  __device__ static __forceinline__ uint32_t max_finite(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(s16x2, a),
+                                                                  __builtin_bit_cast(s16x2, b)));
+  }
+  __device__ static __forceinline__ uint32_t bump(uint32_t m) {
+    return __builtin_bit_cast(uint32_t,
+                              __builtin_bit_cast(u16x2, m) + __builtin_bit_cast(u16x2, BUMP));
+  }
+  __device__ static __forceinline__ uint32_t field(uint32_t w, int h) {
+    return h ? w >> 16 : w & 0xFFFFu;
+  }
+  __device__ static __forceinline__ float value(uint32_t w, int h) {
+    return to_f32(__builtin_bit_cast(T, (uint16_t)field(w, h)));
+  }
+  template <int FMT, bool HI>
+  __device__ static __forceinline__ uint32_t codes(uint32_t old, uint32_t a, uint32_t b, int h,
+                                                   float scale) {
+    const s16x2 o = __builtin_bit_cast(s16x2, old);
+    // (bytes 0, 1 or 2, 3 of a, then the same of b)
+    const uint32_t w = __builtin_amdgcn_perm(b, a, h ? 0x07060302u : 0x05040100u);
+    s16x2 r;
+    if constexpr (std::is_same<T, bf16_t>::value) {
+      const bf16x2 v = __builtin_bit_cast(bf16x2, w);
+      if constexpr (FMT == FMT_E4M3) r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(o, v, scale, HI);
+      else r = __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(o, v, scale, HI);
+    } else {
+      const f16x2 v = __builtin_bit_cast(f16x2, w);
+      if constexpr (FMT == FMT_E4M3) r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(o, v, scale, HI);
+      else r = __builtin_amdgcn_cvt_scalef32_pk_bf8_f16(o, v, scale, HI);
+    }
+    return __builtin_bit_cast(uint32_t, r);
+  }
+};
 
 template <typename T, int FMT>
 __global__ void __launch_bounds__(QTHREADS)
 quant_transpose_kernel(const T* __restrict__ x, int64_t rows, int64_t cols, int64_t ldx, int vec,
                        uint8_t* __restrict__ qt, int64_t ldq, uint8_t* __restrict__ st) {
-  constexpr int CV = 16 / (int)sizeof(T);              // columns of a thread
+  using R = Row16<T>;
+  constexpr int PER = R::PER;                          // values in a 32-bit word
+  constexpr int CV = 4 * PER;                          // columns of a thread
   constexpr int CG = QCOLS / CV;                       // column groups
   constexpr int RT = 64 / CV;                          // tokens of a thread
-  constexpr int RG = QTHREADS / CG;                    // token groups (RG * RT = 128)
-  static_assert(RG * RT == 128, "128 tokens");
-  __shared__ float part[QTHREADS / 64][QCOLS];
+  static_assert(QTHREADS / CG * RT == 128, "128 tokens");
+  __shared__ uint32_t part[QTHREADS / 64][CG][4];
   __shared__ __attribute__((aligned(16))) uint8_t tile[QCOLS * 128];
   const int cg = threadIdx.x % CG, rg = threadIdx.x / CG;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t c0 = (int64_t)blockIdx.x * QCOLS + cg * CV;
   const int64_t r0 = (int64_t)blockIdx.y * 128 + rg * RT;
   const bool has = c0 < cols;                          // (cols % 16 == 0: all CV or none)
-  float v[RT][CV];
+  uint4 v[RT];
+  const T* p = x + r0 * ldx + c0;
+  if (vec && has && r0 + RT <= rows) {
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    const bool in = has && r0 + i < rows;
-    const T* p = x + (r0 + i) * ldx + c0;
-    if (in && vec) {
-      const Pack<T, CV> w = *reinterpret_cast<const Pack<T, CV>*>(p);
-#pragma unroll
-      for (int c = 0; c < CV; ++c) v[i][c] = to_f32(w.v[c]);
-    } else {
-#pragma unroll
-      for (int c = 0; c < CV; ++c) v[i][c] = in ? to_f32(p[c]) : 0.0f;
-    }
-  }
-  // amax over the finite elements of each column
-  float m[CV];
-#pragma unroll
-  for (int c = 0; c < CV; ++c) {
-    m[c] = 0.0f;
+    for (int i = 0; i < RT; ++i) v[i] = *reinterpret_cast<const uint4*>(p + i * ldx);
+  } else {
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      const float y = __builtin_fabsf(v[i][c]);
-      m[c] = __builtin_fmaxf(m[c], y < __builtin_inff() ? y : 0.0f);
+      Pack<T, CV> w;
+#pragma unroll
+      for (int c = 0; c < CV; ++c) w.v[c] = has && r0 + i < rows ? p[i * ldx + c] : (T)0.0f;
+      v[i] = __builtin_bit_cast(uint4, w);
+    }
+  }
+  const auto word = [](const uint4& u, int k) { return k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w; };
+  // amax of each column over the finite values of all tokens, and the largest magnitude
+  // among this thread's own, NaN and infinity on top
+  uint32_t any[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t m = R::BUMP;
+    any[k] = 0u;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const uint32_t y = R::mag(word(v[i], k));
+      any[k] = R::max_any(any[k], y);
+      m = R::max_finite(m, R::bump(y));
     }
 #pragma unroll
-    for (int o = CG; o < 64; o <<= 1) m[c] = __builtin_fmaxf(m[c], __shfl_xor(m[c], o));
-    if (lane < CG) part[wave][cg * CV + c] = m[c];
+    for (int o = CG; o < 64; o <<= 1) m = R::max_finite(m, (uint32_t)__shfl_xor((int)m, o));
+    if (lane < CG) part[wave][cg][k] = m;
   }
   __syncthreads();
-  // one piece (RT codes of a column) per column; piece p of a row lies at
-  // p ^ (its column group's low bits), which spreads the lanes' writes over
-  // the banks
+  // a piece is RT codes of a column; piece q of a row lies at q ^ (its column
+  // group), which spreads the lanes' writes over the banks
   constexpr int PIECES = 128 / RT;
 #pragma unroll
-  for (int c = 0; c < CV; ++c) {
-    const int col = cg * CV + c;
-    const float top = __builtin_fmaxf(__builtin_fmaxf(part[0][col], part[1][col]),
-                                      __builtin_fmaxf(part[2][col], part[3][col]));
-    const int e = block_exponent<FMT>(top);
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-    uint32_t w[RT / 4];
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t top = R::max_finite(R::max_finite(part[0][cg][k], part[1][cg][k]),
+                                       R::max_finite(part[2][cg][k], part[3][cg][k]));
 #pragma unroll
-    for (int i = 0; i < RT / 4; ++i)
-      w[i] = code_pair<FMT>(v[4 * i][c] * down, v[4 * i + 1][c] * down) |
-             code_pair<FMT>(v[4 * i + 2][c] * down, v[4 * i + 3][c] * down) << 16;
-    uint32_t* to = reinterpret_cast<uint32_t*>(tile + col * 128 + ((rg ^ cg) % PIECES) * RT);
+    for (int h = 0; h < PER; ++h) {
+      const int col = cg * CV + k * PER + h;
+      const uint32_t bits = R::field(top, h) - R::field(R::BUMP, h);
+      const int e = block_exponent<FMT>(R::value(PER == 2 ? bits << (16 * h) : bits, h));
+      const float scale = __uint_as_float((uint32_t)(127 + e) << 23);
+      uint32_t w[RT / 4];
 #pragma unroll
-    for (int i = 0; i < RT / 4; ++i) to[i] = w[i];
-    if (rg == 0 && has) st[(int64_t)blockIdx.y * cols + c0 + c] = (uint8_t)(e + 127);
+      for (int i = 0; i < RT / 4; ++i) {
+        w[i] = R::template codes<FMT, false>(0u, word(v[4 * i], k), word(v[4 * i + 1], k), h, scale);
+        w[i] = R::template codes<FMT, true>(w[i], word(v[4 * i + 2], k), word(v[4 * i + 3], k), h, scale);
+      }
+      if (__builtin_expect(R::field(any[k], h) >= R::TOP, 0)) {
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < RT / 4; ++i) {
+          w[i] = 0u;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            w[i] |= code_any<FMT>(R::value(word(v[4 * i + q], k), h), down) << (8 * q);
+        }
+      }
+      uint32_t* to = reinterpret_cast<uint32_t*>(tile + col * 128 + ((rg ^ cg) % PIECES) * RT);
+#pragma unroll
+      for (int i = 0; i < RT / 4; ++i) to[i] = w[i];
+      if (rg == 0 && has) st[(int64_t)blockIdx.y * cols + c0 + k * PER + h] = (uint8_t)(e + 127);
+    }
   }
   __syncthreads();
   // 16 bytes per thread and step: eight lanes to a row
@@ -136,12 +228,11 @@ quant_transpose_kernel(const T* __restrict__ x, int64_t rows, int64_t cols, int6
   for (int q = 0; q < QCOLS * 128 / (16 * QTHREADS); ++q) {
     const int i = q * QTHREADS + threadIdx.x;
     const int col = i >> 3, b16 = i & 7;
-    const int g = col / CV;
     if ((int64_t)blockIdx.x * QCOLS + col >= cols) continue;
     Pack<uint32_t, 4> o;
 #pragma unroll
     for (int h = 0; h < 16 / RT; ++h) {
-      const int piece = (b16 * (16 / RT) + h) ^ (g % PIECES);
+      const int piece = ((b16 * (16 / RT) + h) ^ (col / CV)) % PIECES;
       const uint32_t* from = reinterpret_cast<const uint32_t*>(tile + col * 128 + piece * RT);
 #pragma unroll
       for (int d = 0; d < RT / 4; ++d) o.v[h * (RT / 4) + d] = from[d];
