@@ -19,6 +19,7 @@ using namespace elem;
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
 
 // ---------------------------------------------------------------------------
 // Quantisation along the tokens, written transposed.
@@ -358,12 +359,10 @@ wgrad_kernel(WgradArgs a, int mblocks, int nblocks) {
 //
 // Which global row lies in which LDS row is free, as each lane of a copy has
 // its own address. The rows of a 128-row band are dealt so that
-//   a: position r of fragment i is row 8 r + i: one 8-byte LDS read gives a
-//      lane the exponent bytes of its eight fragments;
-//   b: position 4 g + e of fragment j is row 32 e + 8 g + j: likewise, and a
-//      lane then ends up with 8 adjacent columns (j) of a row for each e, and
-//      the lanes of the four g with 64 adjacent bytes: no exchange between lanes is
-//      needed before the store.
+//   a: position r of fragment i is row 4 r + i: one 4-byte LDS read gives a
+//      lane the exponent bytes of its four fragments;
+//   b: position x of fragment j is row 4 col_of(x) + j: likewise, and a lane
+//      ends up with runs of 8 adjacent columns of a row (see the store).
 
 constexpr int TS = 256;                                // tile side
 constexpr int STAGE = 2 * TS * 128 + 2 * TS;           // codes of a and b, then their exponent bytes
@@ -429,26 +428,29 @@ __device__ __forceinline__ void tile_of(const WgradArgs& a, const Experts& ex, i
 }
 
 // This lane's copy offsets for a tile. Wave w copies the LDS rows of band
-// w / 2 whose position has bit 3 = w % 2; copy i of them is fragment i. Rows
-// past the tile's last are copies of it (read in bounds, never stored).
+// w / 2 whose bit 3 is w % 2: copy c of an operand is fragment c % 4, positions 16 (c / 4)
+// + 8 (w % 2) .. +7. Rows past the tile's last are copies of it (read in
+// bounds, never stored).
 struct Plan {
-  uint32_t va, ma, vb, mb;                             // fragment 0's offset, the last row's
+  uint32_t va, ma, vb, mb;                             // copy 0's offset, the last row's
   uint32_t vs;
 };
+__device__ __forceinline__ int col_of(int x) {         // position of b -> column / 4
+  return (x & 1) | ((x >> 2) & 1) << 1 | ((x >> 1) & 1) << 2 | (x >> 3) << 3;
+}
 __device__ __forceinline__ void make_plan(Plan& p, const WgradArgs& a, const Tile& t, int wave,
                                           int lane) {
   const int band = wave >> 1, h = wave & 1, r = h * 8 + (lane >> 3);
   const uint32_t ch = (uint32_t)((lane & 7) ^ (lane >> 3) ^ h) * 16u;
-  const int ra = band * 128 + r * 8, rb = band * 128 + (r & 3) * 32 + (r >> 2) * 8;
-  p.va = (uint32_t)ra * (uint32_t)a.lda + ch;
-  p.vb = (uint32_t)rb * (uint32_t)a.ldb + ch;
+  p.va = (uint32_t)(band * 128 + r * 4) * (uint32_t)a.lda + ch;
+  p.vb = (uint32_t)(band * 128 + col_of(r) * 4) * (uint32_t)a.ldb + ch;
   p.ma = (uint32_t)(t.mv - 1) * (uint32_t)a.lda + ch;
   p.mb = (uint32_t)(t.nv - 1) * (uint32_t)a.ldb + ch;
   p.vs = (uint32_t)min(lane * 4, (h ? t.nv : t.mv) - 4);
 }
 
-// Copy c of a wave's share of a stage: a's eight fragments, b's 0-3, the
-// exponents (waves 0 and 2 a's, 1 and 3 b's, twice the same bytes), b's 4-7.
+// Copy c of a wave's share of a stage: a's eight, b's fragments 0 and 1, the
+// exponents (waves 0 and 2 a's, 1 and 3 b's, twice the same bytes), b's 2 and 3.
 __device__ __forceinline__ void issue(const Plan& p, const WgradArgs& a, const Tile& t, int kb,
                                       uint32_t stage, int wave, int c) {
   const uint32_t dst = stage + (uint32_t)((wave >> 1) * 16 + (wave & 1)) * 1024u;
@@ -457,18 +459,23 @@ __device__ __forceinline__ void issue(const Plan& p, const WgradArgs& a, const T
   uint32_t lda = (uint32_t)a.lda, ldb = (uint32_t)a.ldb;
   asm volatile("" : "+s"(lda), "+s"(ldb));
   if (c < 8) {
-    copy16(t.a + (int64_t)kb * 128, min(p.va + (uint32_t)c * lda, p.ma), dst + (uint32_t)c * 2048u);
+    const int f = c & 3, half = c >> 2;
+    copy16(t.a + (int64_t)kb * 128, min(p.va + (uint32_t)(f + 64 * half) * lda, p.ma),
+           dst + (uint32_t)(f * 4096 + half * 2048));
   } else if (c == 12) {
     copy4((wave & 1) ? t.sb + (int64_t)kb * a.N : t.sa + (int64_t)kb * a.M, p.vs,
           stage + 2 * TS * 128 + (wave & 1) * TS);
   } else {
-    const uint32_t j = c < 12 ? c - 8 : c - 9;
-    copy16(t.b + (int64_t)kb * 128, min(p.vb + j * ldb, p.mb), dst + TS * 128 + j * 2048u);
+    const int q = c < 12 ? c - 8 : c - 9, f = q >> 1, half = q & 1;
+    copy16(t.b + (int64_t)kb * 128, min(p.vb + (uint32_t)(f + 64 * half) * ldb, p.mb),
+           dst + TS * 128 + (uint32_t)(f * 4096 + half * 2048));
   }
 }
 
-__device__ __forceinline__ v8i read_frag(const uint8_t* band, int f, int lane) {
-  const int r = f * 16 + (lane & 15), c = (lane >> 4) * 2;
+// Fragment f, tokens 64 kh .. +63: lane l holds position l % 32, tokens
+// 32 (l / 32) .. +31 of those.
+__device__ __forceinline__ v8i read_frag(const uint8_t* band, int f, int kh, int lane) {
+  const int r = f * 32 + (lane & 31), c = kh * 4 + (lane >> 5) * 2;
   const uint4 lo = *reinterpret_cast<const uint4*>(band + r * 128 + swz(r, c) * 16);
   const uint4 hi = *reinterpret_cast<const uint4*>(band + r * 128 + swz(r, c + 1) * 16);
   v8i v;
@@ -477,18 +484,17 @@ __device__ __forceinline__ v8i read_frag(const uint8_t* band, int f, int lane) {
   return v;
 }
 
-// Fragments j of b and i of a; byte j & 3 of the register that holds the
-// exponents of fragments 4 (j / 4) .. +3, and the same for a. (i and j are
-// constants where this is inlined.)
+// Fragments j of b and i of a, whose exponents are bytes j and i of sb and
+// sa. (i and j are constants where this is inlined.)
 template <int FA, int FB>
-__device__ __forceinline__ v4f mfma(const v8i& b, const v8i& a, v4f c, int j, const uint2& sb, int i,
-                                    const uint2& sa) {
-  const int xb = (int)(j < 4 ? sb.x : sb.y), xa = (int)(i < 4 ? sa.x : sa.y);
+__device__ __forceinline__ v16f mfma(const v8i& b, const v8i& a, const v16f& c, int j, uint32_t sb,
+                                     int i, uint32_t sa) {
 #define FP8G_M(J_, I_)                                                                          \
   case J_ * 4 + I_:                                                                             \
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, FB, FA, J_, xb, I_, xa);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, FB, FA, J_, (int)sb, I_,    \
+                                                           (int)sa);
 #define FP8G_M4(J_) FP8G_M(J_, 0) FP8G_M(J_, 1) FP8G_M(J_, 2) FP8G_M(J_, 3)
-  switch ((j & 3) * 4 + (i & 3)) {
+  switch (j * 4 + i) {
     FP8G_M4(0) FP8G_M4(1) FP8G_M4(2) FP8G_M4(3)
   }
 #undef FP8G_M4
@@ -497,6 +503,10 @@ __device__ __forceinline__ v4f mfma(const v8i& b, const v8i& a, v4f c, int j, co
 }
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16_pair(float x, float y) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
+}
 
 template <int FA, int FB>
 __global__ void __launch_bounds__(256, 1)
@@ -572,22 +582,25 @@ wgrad_tile_kernel(WgradArgs a, int mblocks, int nblocks, int xcd_remap) {
     for (int c = 0; c < COPIES; ++c) issue(pl, a, tp, p_kb, base + s * STAGE, wave, c);
     advance();
   }
-  v4f acc[8][8];
-  v8i af[8], bf[8];              // fragments of a and b
-  uint2 sa, sb, sa_n, sb_n;      // their exponent bytes
-  const int r16 = lane & 15, g4 = lane >> 4;
-  const int ea = 2 * TS * 128 + wm * 128 + r16 * 8;
-  const int eb = 2 * TS * 128 + TS + wn * 128 + (r16 & 3) * 32 + (r16 >> 2) * 8;
+  v16f acc[4][4];
+  v8i af[4][2], bf[4][2];        // fragments of a and b, by halves of the 128 tokens
+  uint32_t sa, sb, sa_n, sb_n;   // their exponent bytes
+  const int pos = lane & 31;
+  const int ea = 2 * TS * 128 + wm * 128 + pos * 4;
+  const int eb = 2 * TS * 128 + TS + wn * 128 + col_of(pos) * 4;
   const int oa = wm * 128 * 128, ob = TS * 128 + wn * 128 * 128;
   __builtin_amdgcn_s_waitcnt(vmcnt_only(2 * COPIES - EARLY));
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_barrier" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 8; ++i) af[i] = read_frag(lds + oa, i, lane);
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-  for (int j = 0; j < 4; ++j) bf[j] = read_frag(lds + ob, j, lane);
-  sa = *reinterpret_cast<const uint2*>(lds + ea);
-  sb = *reinterpret_cast<const uint2*>(lds + eb);
+    for (int h = 0; h < 2; ++h) {
+      af[i][h] = read_frag(lds + oa, i, h, lane);
+      if (i < 2) bf[i][h] = read_frag(lds + ob, i, h, lane);
+    }
+  sa = *reinterpret_cast<const uint32_t*>(lds + ea);
+  sb = *reinterpret_cast<const uint32_t*>(lds + eb);
 
   // Two points of a step where everyone waits for copies and meets: after
   // slice 0 for b's late fragments of this step, half way for the early part of
@@ -609,66 +622,98 @@ wgrad_tile_kernel(WgradArgs a, int mblocks, int nblocks, int xcd_remap) {
     Tile tc;
     tile_of(a, ex, slot, mblocks, nblocks, tc);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < 4; ++j) acc[i][j] = v16f{};
     for (int k = 0; k < tc.steps; ++k, ++s) {
       const uint8_t* __restrict__ cur = lds + (s & 1) * STAGE;
       const uint8_t* __restrict__ nxt = lds + ((s & 1) ^ 1) * STAGE;
       const uint32_t stage = base + (s & 1) * STAGE;
-      // first half: fragments 0-3 of b, each against all of a
+      // (between two matrix instructions at most two reads and a copy, which
+      // fit their 64 cycles: a run of them would leave the matrix unit waiting)
+#define FP8G_MFMA(I_, J_, H_)                                                          \
+  do {                                                                                 \
+    acc[I_][J_] = mfma<FA, FB>(bf[J_][H_], af[I_][H_], acc[I_][J_], J_, sb, I_, sa);   \
+    /* (a pure instruction: without this it is moved to where it is used) */           \
+    asm volatile("" : "+a"(acc[I_][J_]));                                              \
+  } while (0)
+      // first half: fragments 0 and 1 of b, each against all of a
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          // (one read or copy between two matrix instructions at most: a
-          // run of them would leave the matrix unit waiting)
-          if ((j == 1 || j == 2) && i % 4 == 0) bf[2 * j + 2 + i / 4] = read_frag(cur + ob, 2 * j + 2 + i / 4, lane);
-          acc[i][j] = mfma<FA, FB>(bf[j], af[i], acc[i][j], j, sb, i, sa);
-          // (a pure instruction: without this it is moved to where it is used)
-          asm volatile("" : "+a"(acc[i][j]));
-          const int m = (j - 1) * 8 + i;
-          if (j > 0 && m % 3 == 2) issue(pl, a, tp, p_kb, stage, wave, m / 3);
-        }
-        if (j == 0) meet(std::integral_constant<int, COPIES>{});
+      for (int m = 0; m < 16; ++m) {
+        const int j = m >> 3, h = (m >> 2) & 1, i = m & 3;
+        if (m == 4) meet(std::integral_constant<int, COPIES>{});
+        if (m >= 4 && m < 8) bf[2 + ((m - 4) >> 1)][m & 1] = read_frag(cur + ob, 2 + ((m - 4) >> 1), m & 1, lane);
+        FP8G_MFMA(i, j, h);
+        if (m >= 4 && (m - 4) % 3 != 2) issue(pl, a, tp, p_kb, stage, wave, (m - 4) - (m - 4) / 3);
       }
       meet(std::integral_constant<int, COPIES - EARLY + EARLY_FIRST>{});
-      // second half: each fragment of a against 4-7 of b, after which the
+      // second half: each fragment of a against 2 and 3 of b, after which the
       // next step's takes its place
-      sa_n = *reinterpret_cast<const uint2*>(nxt + ea);
-      sb_n = *reinterpret_cast<const uint2*>(nxt + eb);
+      sa_n = *reinterpret_cast<const uint32_t*>(nxt + ea);
+      sb_n = *reinterpret_cast<const uint32_t*>(nxt + eb);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (i < 4) bf[i] = read_frag(nxt + ob, i, lane);
-#pragma unroll
-        for (int j = 4; j < 8; ++j) {
-          acc[i][j] = mfma<FA, FB>(bf[j], af[i], acc[i][j], j, sb, i, sa);
-          asm volatile("" : "+a"(acc[i][j]));
-          const int m = i * 4 + j - 4;
-          if (m % 3 == 2 && m / 3 < COPIES - EARLY_FIRST)
-            issue(pl, a, tp, p_kb, stage, wave, EARLY_FIRST + m / 3);
-        }
-        af[i] = read_frag(nxt + oa, i, lane);
+      for (int m = 0; m < 16; ++m) {
+        const int i = m >> 2, h = (m >> 1) & 1, j = 2 + (m & 1);
+        if (m < 4) bf[m >> 1][m & 1] = read_frag(nxt + ob, m >> 1, m & 1, lane);
+        FP8G_MFMA(i, j, h);
+        if (m % 2 == 1) issue(pl, a, tp, p_kb, stage, wave, EARLY_FIRST + m / 2);
+        if (m == 15) issue(pl, a, tp, p_kb, stage, wave, EARLY_FIRST + 8);
+        // (the half of this fragment that is done with)
+        if (m % 2 == 1) af[i][h] = read_frag(nxt + oa, i, h, lane);
       }
+#undef FP8G_MFMA
       advance();
       sa = sa_n;
       sb = sb_n;
     }
     const bool full = tc.mv == TS && tc.nv == TS;
     fresh = full ? 3 : 0;
-    // lane (g4, r16): row 8 r16 + i of the wave's band, columns 32 e + 8 g4 + 0..7
-    uint16_t* const d0 = tc.d + (int64_t)(wm * 128 + r16 * 8) * a.N + wn * 128 + g4 * 8;
+    // A lane holds, of a's position pos, 16 positions of each fragment j of b:
+    // for every t 8 adjacent columns (u = 0) and, 16 further, 8 more (u = 1);
+    // the other half of the wave holds the 8 after each. Exchanging u = 1 of
+    // lanes 0-15 (32-47) with u = 0 of lanes 16-31 (48-63) gives four lanes 64
+    // bytes of a row, and exchanging t + 1 of lanes 0-7 of each 16 with t of
+    // lanes 8-15 gives eight lanes its 128. Whole lines, non-temporal, eight
+    // rows a store, measured fastest (16 rows x 64 bytes and 4 x 256 slower).
+    const int l16 = lane & 15, q16 = lane >> 4;
+    const int cl = wn * 128 + (l16 >> 3) * 32 + (q16 & 1) * 16 + (q16 >> 1) * 8;
+    const int rl = wm * 128 + (l16 & 7) * 4;
+    uint16_t* const d0 = tc.d + (int64_t)rl * a.N + cl;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint16_t* const to = d0 + (int64_t)i * a.N;
-      const bool row = wm * 128 + r16 * 8 + i < tc.mv;
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        Pack<bf16_t, 8> o;
+      for (int t2 = 0; t2 < 2; ++t2) {
+        uint32_t v[2][2][4];                           // [t - 2 t2][u]
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o.v[j] = from_f32<bf16_t>(acc[i][j][e]);
-        if (full || (row && wn * 128 + e * 32 + g4 * 8 < tc.nv))
-          *reinterpret_cast<u32x4*>(to + e * 32) = __builtin_bit_cast(u32x4, o);
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int q = 4 * (2 * t2 + tt) + 2 * u + (w >> 1), j = (w & 1) * 2;
+              v[tt][u][w] = bf16_pair(acc[i][j][q], acc[i][j + 1][q]);
+            }
+            const auto r = __builtin_amdgcn_permlane16_swap(v[tt][0][w], v[tt][1][w], false, false);
+            v[tt][0][w] = r[0];
+            v[tt][1][w] = r[1];
+          }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          u32x4 lo, hi;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int x = (int)v[0][u][w], y = (int)v[1][u][w];
+            lo[w] = (uint32_t)__builtin_amdgcn_update_dpp(x, y, 0x128, 0xF, 0xC, false);
+            hi[w] = (uint32_t)__builtin_amdgcn_update_dpp(y, x, 0x128, 0xF, 0x3, false);
+          }
+          // positions (l16 & 7) + 16 u and 8 more of fragment i
+          const int r0 = 64 * u + i, c = t2 * 64;
+          const bool col = c + cl < tc.nv;
+          if (full || (col && rl + r0 < tc.mv))
+            __builtin_nontemporal_store(lo, reinterpret_cast<u32x4*>(d0 + (int64_t)r0 * a.N + c));
+          if (full || (col && rl + r0 + 32 < tc.mv))
+            __builtin_nontemporal_store(hi, reinterpret_cast<u32x4*>(d0 + (int64_t)(r0 + 32) * a.N + c));
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
