@@ -7,7 +7,9 @@ method happens here, and there is no fallback: if the library cannot be
 loaded, every call raises.
 """
 
+import array
 import ctypes
+import operator
 import os
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -114,10 +116,25 @@ def fp8g_abi_version():
     return load().fp8g_abi_version()
 
 
+_raw_stream = None
+
+
+def _current_stream():
+    """The current device's current stream, as its handle. (torch's own
+    integer form takes 0.1 us, the Stream object 2.9.)"""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.current_stream()                 # (initialises the device)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _raw_stream = ((lambda: raw(torch._C._cuda_getDevice())) if raw is not None
+                       else (lambda: torch.cuda.current_stream().cuda_stream))
+    return _raw_stream()
+
+
 def _stream(stream):
-    import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -395,29 +412,42 @@ def grouped_gemm_fp8_masked(a, sa, b, sb, d, masked_m, expected_m=0, stream=None
     _check(st, "grouped_gemm_fp8_masked")
 
 
-_TYPES = None
+# The training-step calls are short on the GPU, so their checks are written to
+# cost little: one attribute each, messages formed only when one fails.
+_TYPES = {}
 
 
-def _type(t):
-    """FP8G_TYPE_* of a tensor, None for any other element type."""
-    global _TYPES
-    if _TYPES is None:
-        import torch
-        _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    return _TYPES.get(t.dtype)
+def _torch():
+    """torch, with _TYPES (element type -> FP8G_TYPE_*) filled."""
+    import torch
+    if not _TYPES:
+        _TYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    return torch
+
+
+def _fail(msg):
+    raise ValueError(msg)
 
 
 def _rows(t, what):
     """Row stride of a matrix whose rows are contiguous."""
-    _need(t.dim() == 2 and t.is_cuda, f"{what} must be a matrix on the GPU")
-    _need(t.shape[1] <= 1 or t.stride(1) == 1, f"{what}: the elements of a row must be contiguous")
-    # (a single row has any stride, and so have empty ones)
-    return t.stride(0) if t.shape[0] > 1 and t.shape[1] > 0 else t.shape[1]
+    if not t.is_cuda or t.dim() != 2:
+        _fail(f"{what} must be a matrix on the GPU")
+    rows, cols = t.shape
+    if cols <= 1:
+        return t.stride(0) if cols and rows > 1 else cols
+    ld, one = t.stride()
+    if one != 1:
+        _fail(f"{what}: the elements of a row must be contiguous")
+    # (a single row has any stride)
+    return ld if rows > 1 else cols
 
 
 def _out(t, shape, dtype, what):
-    _need(tuple(t.shape) == shape and t.dtype == dtype, f"{what} must be {dtype} {list(shape)}")
-    _need(t.is_cuda and t.is_contiguous(), f"{what} must be contiguous and on the GPU")
+    """The pointer of a contiguous GPU tensor of this shape and type."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _fail(f"{what} must be {dtype} {list(shape)}, contiguous and on the GPU")
+    return t.data_ptr()
 
 
 def _room(workspace):
@@ -447,31 +477,29 @@ def moe_route(logits, top_k, expert_ids, weights, counts, routed, prob_sum, loss
     multiples of align; with max_m > 0 the masked layout's slabs), slots int32
     [T][top_k] (row of each pair in that layout, -1: none). workspace: a device
     tensor of at least moe_route_workspace_size(T, E) bytes."""
-    import torch
+    torch = _torch()
     ld = _rows(logits, "logits")
     T, E = logits.shape
-    top_k = int(top_k)
-    typ = _type(logits)
-    _need(typ is not None, "logits must be float32, bfloat16 or float16")
-    i32, f32 = torch.int32, torch.float32
-    _out(expert_ids, (T, top_k), i32, "expert_ids")
-    _out(weights, (T, top_k), f32, "weights")
-    _out(counts, (E,), i32, "counts")
-    _out(routed, (1,), i32, "routed")
-    _out(prob_sum, (E,), f32, "prob_sum")
-    _out(loss, (1,), f32, "loss")
-    _out(group_offsets, (E + 1,), i32, "group_offsets")
-    _out(slots, (T, top_k), i32, "slots")
+    typ = _TYPES.get(logits.dtype)
+    if typ is None:
+        _fail("logits must be float32, bfloat16 or float16")
+    i32, f32, pairs = torch.int32, torch.float32, (T, top_k)
+    ids = _out(expert_ids, pairs, i32, "expert_ids")
+    wts = _out(weights, pairs, f32, "weights")
+    cnt = _out(counts, (E,), i32, "counts")
+    rtd = _out(routed, (1,), i32, "routed")
+    psm = _out(prob_sum, (E,), f32, "prob_sum")
+    los = _out(loss, (1,), f32, "loss")
+    off = _out(group_offsets, (E + 1,), i32, "group_offsets")
+    slt = _out(slots, pairs, i32, "slots")
+    mask = None
     if token_mask is not None:
-        _need(token_mask.dtype in (torch.bool, torch.uint8) and tuple(token_mask.shape) == (T,),
-              "token_mask must be bool or uint8 [T]")
-        _dev(token_mask)
+        mask = _out(token_mask, (T,), torch.uint8 if token_mask.dtype is torch.uint8 else torch.bool, "token_mask")
     wp, wb = _room(workspace)
-    _check(load().moe_route(_ptr(logits), typ, T, E, ld, _ptr(token_mask), top_k,
-                            1 if renormalise else 0, float(loss_coef), int(align), int(max_m),
-                            _ptr(expert_ids), _ptr(weights), _ptr(counts), _ptr(routed),
-                            _ptr(prob_sum), _ptr(loss), _ptr(group_offsets), _ptr(slots), wp, wb,
-                            _stream(stream)), "moe_route")
+    st = load().moe_route(logits.data_ptr(), typ, T, E, ld, mask, top_k, 1 if renormalise else 0, loss_coef,
+                          align, max_m, ids, wts, cnt, rtd, psm, los, off, slt, wp, wb, _stream(stream))
+    if st:
+        _check(st, "moe_route")
 
 
 def moe_route_backward(logits, expert_ids, d_weights, d_loss, counts, routed, d_logits,
@@ -481,25 +509,22 @@ def moe_route_backward(logits, expert_ids, d_weights, d_loss, counts, routed, d_
     logits, expert_ids, counts, routed, renormalise, loss_coef as given to and
     written by moe_route; d_weights float32 [T][top_k] or None, d_loss float32
     [1] or None; d_logits [T][E] of the logits' type (rows may be strided)."""
-    import torch
+    torch = _torch()
     ld, ldd = _rows(logits, "logits"), _rows(d_logits, "d_logits")
     T, E = logits.shape
-    typ = _type(logits)
-    _need(typ is not None and d_logits.dtype == logits.dtype and d_logits.shape == logits.shape,
-          "logits and d_logits must be float32, bfloat16 or float16, alike in type and shape")
-    _need(expert_ids.dim() == 2 and expert_ids.shape[0] == T, "expert_ids must be int32 [T][top_k]")
-    top_k = expert_ids.shape[1]
-    _out(expert_ids, (T, top_k), torch.int32, "expert_ids")
-    if d_weights is not None:
-        _out(d_weights, (T, top_k), torch.float32, "d_weights")
-    if d_loss is not None:
-        _out(d_loss, (1,), torch.float32, "d_loss")
-    _out(counts, (E,), torch.int32, "counts")
-    _out(routed, (1,), torch.int32, "routed")
-    _check(load().moe_route_backward(_ptr(logits), typ, T, E, ld, _ptr(expert_ids), top_k,
-                                     1 if renormalise else 0, float(loss_coef), _ptr(d_weights),
-                                     _ptr(d_loss), _ptr(counts), _ptr(routed), _ptr(d_logits), ldd,
-                                     _stream(stream)), "moe_route_backward")
+    typ = _TYPES.get(logits.dtype)
+    if typ is None or d_logits.dtype is not logits.dtype or d_logits.shape != logits.shape:
+        _fail("logits and d_logits must be float32, bfloat16 or float16, alike in type and shape")
+    top_k = expert_ids.shape[-1]
+    ids = _out(expert_ids, (T, top_k), torch.int32, "expert_ids")
+    dw = None if d_weights is None else _out(d_weights, (T, top_k), torch.float32, "d_weights")
+    dl = None if d_loss is None else _out(d_loss, (1,), torch.float32, "d_loss")
+    cnt = _out(counts, (E,), torch.int32, "counts")
+    rtd = _out(routed, (1,), torch.int32, "routed")
+    st = load().moe_route_backward(logits.data_ptr(), typ, T, E, ld, ids, top_k, 1 if renormalise else 0,
+                                   loss_coef, dw, dl, cnt, rtd, d_logits.data_ptr(), ldd, _stream(stream))
+    if st:
+        _check(st, "moe_route_backward")
 
 
 def fp8_quantize_transpose(x, fmt, qt, st, stream=None):
@@ -507,18 +532,21 @@ def fp8_quantize_transpose(x, fmt, qt, st, stream=None):
     qt uint8 [cols][R] codes in fmt ('e4m3' or 'e5m2'), R = rows rounded up to
     128, and st uint8 [R/128][cols]: one power-of-two scale per column and 128
     rows, as its exponent + 127."""
-    import torch
+    torch = _torch()
     ldx = _rows(x, "x")
     rows, cols = x.shape
-    typ = _type(x)
-    _need(typ is not None, "x must be float32, bfloat16 or float16")
-    _need(qt.dtype == torch.uint8 and st.dtype == torch.uint8, "qt and st must be uint8")
-    _need(tuple(qt.shape) == (cols, _nb(rows) * 128), "qt must be [cols][rows rounded up to 128]")
-    _need(tuple(st.shape) == (_nb(rows), cols), "st must be [ceil(rows/128)][cols]")
+    nb = _nb(rows)
+    typ = _TYPES.get(x.dtype)
+    if typ is None:
+        _fail("x must be float32, bfloat16 or float16")
+    if qt.dtype is not torch.uint8 or qt.shape != (cols, nb * 128):
+        _fail("qt must be uint8 [cols][rows rounded up to 128]")
     ldq = _rows(qt, "qt")
-    _dev(st)
-    _check(load().fp8_quantize_transpose(_ptr(x), typ, rows, cols, ldx, _fmt(fmt), _ptr(qt), ldq,
-                                         _ptr(st), _stream(stream)), "fp8_quantize_transpose")
+    scales = _out(st, (nb, cols), torch.uint8, "st (ceil(rows/128), cols)")
+    status = load().fp8_quantize_transpose(x.data_ptr(), typ, rows, cols, ldx, _fmt(fmt), qt.data_ptr(), ldq,
+                                           scales, _stream(stream))
+    if status:
+        _check(status, "fp8_quantize_transpose")
 
 
 def grouped_gemm_fp8_wgrad(a, fmt_a, sa, b, fmt_b, sb, d, group_offsets=None, stream=None):
@@ -526,45 +554,57 @@ def grouped_gemm_fp8_wgrad(a, fmt_a, sa, b, fmt_b, sb, d, group_offsets=None, st
     [T/128][M], b [N][T], sb [T/128][N] as fp8_quantize_transpose writes them
     (T a multiple of 128); group_offsets int32 [G+1] (device) or None (G = 1,
     all tokens)."""
-    import torch
+    torch = _torch()
     lda, ldb = _rows(a, "a"), _rows(b, "b")
     M, T = a.shape
     N = b.shape[0]
     fa, fb = _fmt(fmt_a), _fmt(fmt_b)
-    _need(b.shape[1] == T and T % 128 == 0, "a and b must have the same tokens, a multiple of 128")
-    _need(_codes_dtype_ok(a, fmt_a) and _codes_dtype_ok(b, fmt_b),
-          "a and b must be codes of their formats (uint8 or the matching float8 dtype)")
-    _need(tuple(sa.shape) == (T // 128, M) and tuple(sb.shape) == (T // 128, N)
-          and sa.dtype == torch.uint8 and sb.dtype == torch.uint8,
-          "sa and sb must be uint8 [T/128][M] and [T/128][N]")
-    _need(d.dim() == 3 and d.shape[1] == M and d.shape[2] == N
-          and d.dtype in (torch.int16, torch.bfloat16, torch.uint16), "d must be bf16 [G][M][N]")
+    if b.shape[1] != T or T % 128:
+        _fail("a and b must have the same tokens, a multiple of 128")
+    if not (_codes_dtype_ok(a, fmt_a) and _codes_dtype_ok(b, fmt_b)):
+        _fail("a and b must be codes of their formats (uint8 or the matching float8 dtype)")
+    pa = _out(sa, (T // 128, M), torch.uint8, "sa (T/128, M)")
+    pb = _out(sb, (T // 128, N), torch.uint8, "sb (T/128, N)")
+    if d.dim() != 3 or d.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+        _fail("d must be bf16 [G][M][N]")
     G = d.shape[0]
-    if group_offsets is None:
-        _need(G == 1, "group_offsets may be None for one expert only")
+    pd = _out(d, (G, M, N), d.dtype, "d ([G][M][N])")
+    if group_offsets is not None:
+        po = _out(group_offsets, (G + 1,), torch.int32, "group_offsets")
+    elif G == 1:
+        po = None
     else:
-        _out(group_offsets, (G + 1,), torch.int32, "group_offsets")
-    _dev(sa, sb, d)
-    _check(load().grouped_gemm_fp8_wgrad(_ptr(a), fa, lda, _ptr(sa), _ptr(b), fb, ldb, _ptr(sb),
-                                         _ptr(d), _ptr(group_offsets), G, T, M, N, _stream(stream)),
-           "grouped_gemm_fp8_wgrad")
+        _fail("group_offsets may be None for one expert only")
+    st = load().grouped_gemm_fp8_wgrad(a.data_ptr(), fa, lda, pa, b.data_ptr(), fb, ldb, pb, pd, po, G, T, M, N,
+                                       _stream(stream))
+    if st:
+        _check(st, "grouped_gemm_fp8_wgrad")
 
 
 def _grad_list(ts, what):
-    """HOST arrays of the tensors' pointers, sizes and types."""
-    n = len(ts)
-    types = [_type(t) for t in ts]
-    _need(None not in types, f"{what} must be float32, bfloat16 or float16")
-    _need(all(t.is_cuda and t.is_contiguous() for t in ts), f"{what} must be contiguous and on the GPU")
-    return (_c_vp * n)(*[t.data_ptr() for t in ts]), (_c_i64 * n)(*[t.numel() for t in ts]), (_c_int * n)(*types)
+    """HOST arrays of the tensors' pointers, sizes and types. (Hundreds of
+    tensors: every attribute is read in a loop of the interpreter's own.)"""
+    torch = _torch()
+    cls = torch.Tensor
+    types = list(map(_TYPES.get, map(operator.attrgetter("dtype"), ts)))
+    if None in types:
+        _fail(f"{what} must be float32, bfloat16 or float16")
+    if not (all(map(operator.attrgetter("is_cuda"), ts)) and all(map(cls.is_contiguous, ts))):
+        _fail(f"{what} must be contiguous and on the GPU")
+    return (array.array("Q", list(map(cls.data_ptr, ts))), array.array("q", list(map(cls.numel, ts))),
+            array.array("i", types))
+
+
+def _at(a):
+    return a.buffer_info()[0] if len(a) else None
 
 
 def grad_norm_sq_workspace_size(grads):
     """Bytes of workspace grad_norm_sq needs for this list of tensors."""
     out = ctypes.c_size_t(0)
-    n = len(grads)
-    _check(load().grad_norm_sq_workspace_size((_c_i64 * n)(*[t.numel() for t in grads]), n,
-                                              ctypes.byref(out)), "grad_norm_sq_workspace_size")
+    numels = array.array("q", [t.numel() for t in grads])
+    _check(load().grad_norm_sq_workspace_size(_at(numels), len(grads), ctypes.byref(out)),
+           "grad_norm_sq_workspace_size")
     return int(out.value)
 
 
@@ -572,26 +612,29 @@ def grad_norm_sq(grads, sumsq, workspace, stream=None):
     """Sum of squares over a list of contiguous tensors (float32, bfloat16,
     float16, mixed) into sumsq, a float64 device tensor of one element.
     workspace: at least grad_norm_sq_workspace_size(grads) bytes."""
-    import torch
+    torch = _torch()
     ptrs, numels, types = _grad_list(grads, "grads")
-    _out(sumsq, (1,), torch.float64, "sumsq")
+    out = _out(sumsq, (1,), torch.float64, "sumsq")
     wp, wb = _room(workspace)
-    _check(load().grad_norm_sq(ptrs, numels, types, len(grads), _ptr(sumsq), wp, wb, _stream(stream)),
+    _check(load().grad_norm_sq(_at(ptrs), _at(numels), _at(types), len(ptrs), out, wp, wb, _stream(stream)),
            "grad_norm_sq")
 
 
 def grad_clip(grads, outs, sumsq, max_norm, norm, stream=None):
     """outs[i] = grads[i] * min(1, max_norm / (norm + 1e-6)), norm = sqrt(sumsq)
     (float32 device tensor of one element, written). outs[i] may be grads[i]."""
-    import torch
+    torch = _torch()
     ptrs, numels, types = _grad_list(grads, "grads")
-    optrs, onumels, otypes = _grad_list(outs, "outs")
-    _need(len(outs) == len(grads) and onumels[:] == numels[:] and otypes[:] == types[:],
-          "outs must match grads in number, size and type")
-    _out(sumsq, (1,), torch.float64, "sumsq")
-    _out(norm, (1,), torch.float32, "norm")
-    _check(load().grad_clip(ptrs, optrs, numels, types, len(grads), _ptr(sumsq), float(max_norm),
-                            _ptr(norm), _stream(stream)), "grad_clip")
+    if outs is grads:
+        optrs = ptrs
+    else:
+        optrs, onumels, otypes = _grad_list(outs, "outs")
+        if onumels != numels or otypes != types:
+            _fail("outs must match grads in number, size and type")
+    total = _out(sumsq, (1,), torch.float64, "sumsq")
+    nrm = _out(norm, (1,), torch.float32, "norm")
+    _check(load().grad_clip(_at(ptrs), _at(optrs), _at(numels), _at(types), len(ptrs), total, max_norm, nrm,
+                            _stream(stream)), "grad_clip")
 
 
 def fp8g_clock_probe(out, ticks=2000, stream=None):
