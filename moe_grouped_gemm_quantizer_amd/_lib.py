@@ -274,7 +274,8 @@ def gemm_fp8_pertensor(a, scale_a, b, scale_b, d, stream=None):
 
 
 def _fmt(name):
-    _need(name in FORMATS, f"format must be one of {sorted(FORMATS)}")
+    if name not in FORMATS:
+        raise ValueError(f"format must be one of {sorted(FORMATS)}")
     return FORMATS[name]
 
 

@@ -37,7 +37,9 @@ __device__ __forceinline__ float ring16f(float x) {
   return __uint_as_float(ring16<D>(__float_as_uint(x)));
 }
 
-// All-lanes reductions over groups of LPR lanes (16 or 64).
+// All-lanes reductions over groups of LPR lanes (16 or 64). Above 16 lanes
+// gfx950 exchanges whole rows of lanes between two registers: of two copies
+// of x, each lane then holds its own row's value and the other row's.
 template <int LPR, class F>
 __device__ __forceinline__ uint32_t reduce_u32(uint32_t x, F f) {
   x = f(x, ring16<8>(x));
@@ -45,22 +47,18 @@ __device__ __forceinline__ uint32_t reduce_u32(uint32_t x, F f) {
   x = f(x, ring16<2>(x));
   x = f(x, ring16<1>(x));
   if constexpr (LPR == 64) {
-    x = f(x, (uint32_t)__shfl_xor((int)x, 16));
-    x = f(x, (uint32_t)__shfl_xor((int)x, 32));
+    const auto p = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = f(p[0], p[1]);
+    const auto q = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    x = f(q[0], q[1]);
   }
   return x;
 }
 template <int LPR, class F>
 __device__ __forceinline__ float reduce_f32(float x, F f) {
-  x = f(x, ring16f<8>(x));
-  x = f(x, ring16f<4>(x));
-  x = f(x, ring16f<2>(x));
-  x = f(x, ring16f<1>(x));
-  if constexpr (LPR == 64) {
-    x = f(x, __shfl_xor(x, 16));
-    x = f(x, __shfl_xor(x, 32));
-  }
-  return x;
+  return __uint_as_float(reduce_u32<LPR>(__float_as_uint(x), [&](uint32_t a, uint32_t b) {
+    return __float_as_uint(f(__uint_as_float(a), __uint_as_float(b)));
+  }));
 }
 template <int LPR>
 __device__ __forceinline__ float sum_lanes(float x) {
@@ -69,6 +67,32 @@ __device__ __forceinline__ float sum_lanes(float x) {
 template <int LPR>
 __device__ __forceinline__ float max_lanes(float x) {
   return reduce_f32<LPR>(x, [](float a, float b) { return __builtin_fmaxf(a, b); });
+}
+
+// Sum over the wave's 64 lanes, in fp64.
+__device__ __forceinline__ double sum_wave(double x) {
+  const auto other = [](double v, auto get) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)get((uint32_t)u) | (uint64_t)get((uint32_t)(u >> 32)) << 32);
+  };
+  x += other(x, [](uint32_t w) { return ring16<8>(w); });
+  x += other(x, [](uint32_t w) { return ring16<4>(w); });
+  x += other(x, [](uint32_t w) { return ring16<2>(w); });
+  x += other(x, [](uint32_t w) { return ring16<1>(w); });
+  x += other(x, [](uint32_t w) { return (uint32_t)__shfl_xor((int)w, 16); });
+  x += other(x, [](uint32_t w) { return (uint32_t)__shfl_xor((int)w, 32); });
+  return x;
+}
+
+// exp(x) for x <= 0 (or NaN) within 2 ulp: 2^(x log2 e), the product's
+// rounding error put back to first order. Below -150 the result is 0.
+__device__ __forceinline__ float exp_neg(float x) {
+  constexpr float L2E = 0x1.715476p+0f, L2E_LO = 0x1.4ae0cp-26f, LN2 = 0x1.62e43p-1f;
+  x = x < -150.0f ? -150.0f : x;
+  const float t = x * L2E;
+  const float lo = __builtin_fmaf(x, L2E_LO, __builtin_fmaf(x, L2E, -t));
+  const float y = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(y, lo * LN2, y);
 }
 
 }  // namespace elem

@@ -36,7 +36,8 @@ constexpr int MAX_K = 16;
 template <typename T, int LPR, int VPT>
 struct Lay {
   static constexpr int WMAX = 16 / (int)sizeof(T);
-  static constexpr int W = VPT < WMAX ? VPT : WMAX;
+  static constexpr int W = VPT % WMAX == 0 ? WMAX : (VPT % 4 == 0 ? 4 : VPT);
+  static_assert(VPT % W == 0 && W <= WMAX, "whole groups");
   static constexpr int ROWS_AT_ONCE = THREADS / LPR;
   __device__ static __forceinline__ int at(int v, int l) {
     return (v / W) * (W * LPR) + l * W + v % W;
@@ -70,78 +71,121 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t k = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
   return x > -__builtin_inff() ? k : 0u;
 }
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
-}
 
-// The largest remaining logit of each row, and its removal. 16-bit inputs
-// pack the order of their value and the expert's number (lower first) into
-// one word, so that one maximum finds both; 32-bit ones find the value and
-// then the lowest expert that has it.
+// The largest remaining logit of each row, one after the other.
+//
+// A key holds the order of a value in its upper bits and, inverted, the
+// expert's number below, so that one maximum finds the value and the lowest
+// expert that has it, and all keys differ. The next one is the largest key
+// below the last: with d = key - last in wrapping arithmetic, every key below
+// it has a larger d than every key from it on, so it is last + max d, at one
+// subtraction and half a three-way maximum per expert; no key is removed.
+//
+// 16-bit values fit a key whole. Of a 32-bit value BITS low bits give way to
+// the expert's number: exact where they are zero in the whole row (values that
+// were 16-bit ones, for instance); otherwise two neighbours in the order
+// whose kept bits agree are not known to be in order, and the caller looks
+// for such a pair (one place past the k-th too) and falls back to `exact`.
 template <typename T, int LPR, int VPT>
 struct Picker {
   using L = Lay<T, LPR, VPT>;
+  static constexpr bool WHOLE = sizeof(T) == 2;
+  static constexpr int BITS = WHOLE ? 16 : (LPR * VPT <= 256 ? 8 : 10);
+  static constexpr uint32_t LOW = (1u << BITS) - 1u;
   uint32_t key[VPT];
-  static constexpr bool PACKED = sizeof(T) == 2;
+  uint32_t last;
+  uint32_t dropped;      // nonzero: bits of the row's values are not in its keys
 
   // (a 16-bit value's fp32 key: bf16 has its order in the upper half; fp16
   // is widened, so it is brought back to its own 16 bits)
-  __device__ static __forceinline__ uint32_t half_key(float x) {
+  __device__ static __forceinline__ uint32_t upper(float x) {
     if constexpr (std::is_same<T, f16_t>::value) {
       const uint16_t u = __builtin_bit_cast(uint16_t, (f16_t)(x + 0.0f));
       const uint32_t k = (u & 0x8000u) ? (uint16_t)~u : (uint16_t)(u | 0x8000u);
-      return x > -__builtin_inff() ? k : 0u;
+      return x > -__builtin_inff() ? k << 16 : 0u;
     } else {
-      return order_key(x) >> 16;
-    }
-  }
-  __device__ static __forceinline__ float half_value(uint32_t k) {
-    if constexpr (std::is_same<T, f16_t>::value) {
-      const uint16_t u = (uint16_t)((k & 0x8000u) ? (k ^ 0x8000u) : ~k);
-      return (float)__builtin_bit_cast(f16_t, u);
-    } else {
-      // (the lower half of a negative value's key is all ones, cut off above)
-      return key_value((k << 16) | ((k & 0x8000u) ? 0u : 0xFFFFu));
+      return order_key(x) & ~LOW;
     }
   }
 
   __device__ __forceinline__ void start(const float (&x)[VPT], int l) {
+    last = 0u;
+    dropped = 0u;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      if constexpr (PACKED) {
-        const uint32_t h = half_key(x[v]);
-        key[v] = h ? (h << 16) | (0xFFFFu - (uint32_t)L::at(v, l)) : 0u;
-      } else {
-        key[v] = order_key(x[v]);
-      }
+      const uint32_t h = upper(x[v]);
+      key[v] = h ? h | (LOW - (uint32_t)L::at(v, l)) : 0u;
+      if constexpr (!WHOLE) dropped |= __float_as_uint(x[v]);
     }
+    if constexpr (!WHOLE)
+      dropped = reduce_u32<LPR>(dropped & LOW, [](uint32_t a, uint32_t b) { return a | b; });
   }
-  // expert (-1: none is left) and its logit, the same in all the row's lanes
-  __device__ __forceinline__ int next(int l, float& value) {
+  // (the first call: everything lies below 2^32)
+  __device__ __forceinline__ uint32_t next() {
     const auto umax = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+    uint32_t d = key[0] - last;
+#pragma unroll
+    for (int v = 1; v < VPT; ++v) d = umax(d, key[v] - last);
+    d = reduce_u32<LPR>(d, umax);
+    const uint32_t k = last + d;
+    // (none left below: d is one of the keys from `last` on; a key of 0 is
+    // what is never chosen. `last` stays where it is then.)
+    const bool none = k == 0u || (last != 0u && k >= last);
+    last = none ? last : k;
+    return none ? 0u : k;
+  }
+  __device__ static __forceinline__ int expert(uint32_t k) { return k ? (int)(LOW - (k & LOW)) : -1; }
+};
+
+// The k largest of whole 32-bit values: the value, then the lowest expert
+// that has it, which is removed. Lane j gets the j-th.
+template <int LPR, int VPT>
+__device__ __forceinline__ int exact_choice(const float (&x)[VPT], int l, int k) {
+  using L = Lay<float, LPR, VPT>;
+  uint32_t key[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) key[v] = order_key(x[v]);
+  int id = -1;
+  for (int j = 0; j < k; ++j) {
     uint32_t best = key[0];
 #pragma unroll
-    for (int v = 1; v < VPT; ++v) best = umax(best, key[v]);
-    best = reduce_u32<LPR>(best, umax);
-    int e;
-    if constexpr (PACKED) {
-      e = (int)(0xFFFFu - (best & 0xFFFFu));
-      value = half_value(best >> 16);
+    for (int v = 1; v < VPT; ++v) best = best > key[v] ? best : key[v];
+    best = reduce_u32<LPR>(best, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+    uint32_t low = 0xFFFFFFFFu;
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) key[v] = key[v] == best ? 0u : key[v];
-    } else {
-      uint32_t low = 0xFFFFFFFFu;
+    for (int v = VPT - 1; v >= 0; --v) low = key[v] == best ? (uint32_t)L::at(v, l) : low;
+    low = reduce_u32<LPR>(low, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
 #pragma unroll
-      for (int v = VPT - 1; v >= 0; --v) low = key[v] == best ? (uint32_t)L::at(v, l) : low;
-      low = reduce_u32<LPR>(low, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
-      e = (int)low;
-      value = key_value(best);
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) key[v] = (uint32_t)L::at(v, l) == low ? 0u : key[v];
-    }
-    return best ? e : -1;
+    for (int v = 0; v < VPT; ++v) key[v] = (uint32_t)L::at(v, l) == low ? 0u : key[v];
+    if (l == j && best) id = (int)low;
   }
-};
+  return id;
+}
+
+// Lane j gets the row's j-th choice (-1: none).
+template <typename T, int LPR, int VPT>
+__device__ __forceinline__ int choose(const float (&x)[VPT], int l, int k) {
+  using P = Picker<T, LPR, VPT>;
+  P pick;
+  pick.start(x, l);
+  uint32_t mine = 0u, before = 0u;
+  bool close = false;
+  for (int j = 0; j < k; ++j) {
+    const uint32_t key = pick.next();
+    if constexpr (!P::WHOLE) close = close || (key && ((key ^ before) >> P::BITS) == 0u);
+    before = key;
+    if (l == j) mine = key;
+  }
+  int id = P::expert(mine);
+  if constexpr (!P::WHOLE) {
+    if (__ballot(pick.dropped != 0u)) {                // (uniform over the wave)
+      const uint32_t key = pick.next();
+      close = close || (key && ((key ^ before) >> P::BITS) == 0u);
+      if (__ballot(close && pick.dropped != 0u)) id = exact_choice<LPR, VPT>(x, l, k);
+    }
+  }
+  return id;
+}
 
 // exp(x - max) of a row and their sum's reciprocal. A row of -inf alone has
 // p = 0; NaN or +inf in a row make its p NaN.
@@ -155,7 +199,7 @@ __device__ __forceinline__ float row_softmax(const float (&x)[VPT], float& top, 
   float s = 0.0f;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    ex[v] = expf(x[v] - top);
+    ex[v] = exp_neg(x[v] - top);
     s += ex[v];
   }
   s = sum_lanes<LPR>(s);
@@ -194,16 +238,15 @@ __device__ __forceinline__ void offsets_of(const int* __restrict__ counts, int E
   __syncthreads();
 }
 
-// loss = coef sum_e (E c_e / (k n)) (P_e / n), by the first wave.
+// loss = coef sum_e (E c_e / (k n)) (P_e / n), by one wave.
 __device__ __forceinline__ void write_loss(const int* counts, const float* prob_sum, int routed,
                                            int E, int k, float coef, float* loss) {
-  if (threadIdx.x >= 64) return;
+  const int lane = threadIdx.x & 63;
   double s = 0.0;
-  for (int e = threadIdx.x; e < E; e += 64) s += (double)counts[e] * (double)prob_sum[e];
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o);
+  for (int e = lane; e < E; e += 64) s += (double)counts[e] * (double)prob_sum[e];
+  s = sum_wave(s);
   const double n = routed > 0 ? (double)routed : 1.0;
-  if (threadIdx.x == 0) *loss = (float)((double)coef * E / ((double)k * n * n) * s);
+  if (lane == 0) *loss = (float)((double)coef * E / ((double)k * n * n) * s);
 }
 
 struct RouteArgs {
@@ -233,7 +276,7 @@ route_rows_kernel(RouteArgs a) {
   __shared__ uint32_t took[2][MAX_E];                  // tokens of the block that chose e, as bits
   __shared__ short chosen[ROWS][MAX_K];
   __shared__ float psum[THREADS / 64][LPR * VPT];
-  __shared__ int off[MAX_E + 1];
+  __shared__ int count[MAX_E], off[MAX_E + 1];         // (where one block is all)
   __shared__ int wave_sum[THREADS / 64];
   __shared__ int n_routed;
   const int E = a.E, k = a.k;
@@ -256,18 +299,9 @@ route_rows_kernel(RouteArgs a) {
     const float inv = row_softmax<LPR, VPT>(x, top, ex);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) acc[v] += ex[v] * inv;
-    Picker<T, LPR, VPT> pick;
-    pick.start(x, l);
-    int id = -1;                                       // lane j keeps the row's j-th choice
-    float w = 0.0f;
-    for (int j = 0; j < k; ++j) {
-      float value;
-      const int e = pick.next(l, value);
-      if (l == j && e >= 0) {
-        id = e;
-        w = expf(value - top);
-      }
-    }
+    const int id = choose<T, LPR, VPT>(x, l, k);
+    // (the row was just read: its value again is a cache hit)
+    float w = id >= 0 ? exp_neg(to_f32(((const T*)a.logits)[t * a.ld + id]) - top) : 0.0f;
     const float s = a.renorm ? sum_lanes<LPR>(w) : 0.0f;
     // (a NaN row: inv is NaN, and so is every weight)
     w = inv != inv ? inv : (a.renorm ? (s > 0.0f ? w / s : 0.0f) : w * inv);
@@ -299,7 +333,7 @@ route_rows_kernel(RouteArgs a) {
       a.counts[e] = c;
       a.prob_sum[e] = p;
       psum[0][e] = p;
-      off[e] = c;
+      count[e] = c;
     } else {
       a.part_count[(int64_t)blockIdx.x * (E + 1) + e] = c;
       a.part_prob[(int64_t)blockIdx.x * E + e] = p;
@@ -311,14 +345,13 @@ route_rows_kernel(RouteArgs a) {
   }
   if (only) {
     __syncthreads();
-    write_loss(off, psum[0], n_routed, E, k, a.coef, a.loss);
-    __syncthreads();
     if (a.max_m == 0) {
-      offsets_of(off, E, a.align, off, wave_sum);
+      offsets_of(count, E, a.align, off, wave_sum);
       for (int e = threadIdx.x; e <= E; e += THREADS) a.offsets[e] = off[e];
     } else {
       for (int e = threadIdx.x; e <= E; e += THREADS) a.offsets[e] = (int)(e * a.max_m);
     }
+    if (wave == 3) write_loss(count, psum[0], n_routed, E, k, a.coef, a.loss);
   }
   // ranks inside the block (its only block: the slots themselves)
   const int64_t left = a.T - t0;
@@ -349,12 +382,25 @@ route_scan_kernel(RouteArgs a, int nblk) {
   const int E = a.E;
   const int per = (nblk + RUNS - 1) / RUNS;
   const int b0 = run * per, b1 = min(nblk, b0 + per);
+  // (loads in batches: a run is a chain of them otherwise)
+  constexpr int BATCH = 16;
   int s = 0;
   double p = 0.0;
   if (e <= E) {
-    for (int b = b0; b < b1; ++b) {
-      s += a.part_count[(int64_t)b * (E + 1) + e];
-      if (e < E) p += (double)a.part_prob[(int64_t)b * E + e];
+    for (int b = b0; b < b1; b += BATCH) {
+      int c[BATCH];
+      float q[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int64_t at = min(b + i, b1 - 1);
+        c[i] = a.part_count[at * (E + 1) + e];
+        q[i] = e < E ? a.part_prob[at * E + e] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        s += b + i < b1 ? c[i] : 0;
+        p += b + i < b1 ? (double)q[i] : 0.0;
+      }
     }
   }
   cnt[run][l] = s;
@@ -363,11 +409,16 @@ route_scan_kernel(RouteArgs a, int nblk) {
   if (e > E) return;
   int at = 0;
   for (int q = 0; q < run; ++q) at += cnt[q][l];
-  for (int b = b0; b < b1; ++b) {
-    int* c = a.part_count + (int64_t)b * (E + 1) + e;
-    const int v = *c;
-    *c = at;
-    at += v;
+  for (int b = b0; b < b1; b += BATCH) {
+    int c[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) c[i] = a.part_count[(int64_t)min(b + i, b1 - 1) * (E + 1) + e];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      if (b + i < b1) {
+        a.part_count[(int64_t)(b + i) * (E + 1) + e] = at;
+        at += c[i];
+      }
   }
   if (run == RUNS - 1) {
     if (e == E) {
@@ -388,27 +439,30 @@ route_slots_kernel(RouteArgs a) {
   __shared__ int off[MAX_E + 1];
   __shared__ int wave_sum[THREADS / 64];
   const int E = a.E, k = a.k;
-  if (a.max_m == 0) {
-    offsets_of(a.counts, E, a.align, off, wave_sum);
-  } else if (blockIdx.x == 0) {
-    for (int e = threadIdx.x; e <= E; e += THREADS) a.offsets[e] = (int)(e * a.max_m);
-  }
-  if (blockIdx.x == 0) {
-    if (a.max_m == 0)
-      for (int e = threadIdx.x; e <= E; e += THREADS) a.offsets[e] = off[e];
-    write_loss(a.counts, a.prob_sum, a.routed[0], E, k, a.coef, a.loss);
-  }
+  // the pairs' loads first: the offsets are formed while they are on their way
+  constexpr int Q = PAIRS / THREADS;
   const int64_t pairs = a.T * k;
   const int64_t i0 = (int64_t)blockIdx.x * PAIRS + threadIdx.x;
+  int id[Q], rank[Q];
 #pragma unroll
-  for (int q = 0; q < PAIRS / THREADS; ++q) {
+  for (int q = 0; q < Q; ++q) {
     const int64_t i = i0 + q * THREADS;
-    if (i >= pairs) break;
-    const int e = a.ids[i];
-    if (e < 0) continue;                               // (its slot is -1 already)
-    const int64_t blk = i / ((int64_t)ROWS * k);
-    const int rank = a.part_count[blk * (E + 1) + e] + a.slots[i];
-    a.slots[i] = slot_of(a, e, a.max_m == 0 ? off[e] : 0, rank);
+    id[q] = i < pairs ? a.ids[i] : -1;
+    rank[q] = i < pairs ? a.slots[i] : 0;
+  }
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    const int64_t blk = (i0 + q * THREADS) / ((int64_t)ROWS * k);
+    if (id[q] >= 0) rank[q] += a.part_count[blk * (E + 1) + id[q]];
+  }
+  if (a.max_m == 0) offsets_of(a.counts, E, a.align, off, wave_sum);
+#pragma unroll
+  for (int q = 0; q < Q; ++q)                          // (without an expert: the slot is -1 already)
+    if (id[q] >= 0) a.slots[i0 + q * THREADS] = slot_of(a, id[q], a.max_m == 0 ? off[id[q]] : 0, rank[q]);
+  if (blockIdx.x == 0) {
+    for (int e = threadIdx.x; e <= E; e += THREADS)
+      a.offsets[e] = a.max_m == 0 ? off[e] : (int)(e * a.max_m);
+    if (threadIdx.x < 64) write_loss(a.counts, a.prob_sum, a.routed[0], E, k, a.coef, a.loss);
   }
 }
 
@@ -424,6 +478,14 @@ __global__ void route_empty_kernel(RouteArgs a) {
     a.routed[0] = 0;
     a.loss[0] = 0.0f;
   }
+}
+
+// Orders a wave's LDS accesses for the compiler (the LDS itself takes them in
+// order).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 struct RouteBwdArgs {
@@ -442,6 +504,8 @@ template <typename T, int LPR, int VPT>
 __global__ void __launch_bounds__(THREADS)
 route_backward_kernel(RouteBwdArgs a) {
   using L = Lay<T, LPR, VPT>;
+  // the chosen experts' gradients of each row, in the lanes' order of experts
+  __shared__ __attribute__((aligned(16))) float chosen[L::ROWS_AT_ONCE][LPR * VPT];
   const int E = a.E, k = a.k;
   const int l = threadIdx.x & (LPR - 1), group = threadIdx.x / LPR;
   const int n = a.routed[0];
@@ -467,7 +531,7 @@ route_backward_kernel(RouteBwdArgs a) {
     float x[VPT], ex[VPT], top;
     load_row<T, LPR, VPT>(row, E, l, on, a.vec != 0, x);
     const float inv = row_softmax<LPR, VPT>(x, top, ex);
-    const float pj = id >= 0 && on ? expf(to_f32(row[id]) - top) * inv : 0.0f;
+    const float pj = id >= 0 && on ? exp_neg(to_f32(row[id]) - top) * inv : 0.0f;
     float dwj = id >= 0 && a.dw ? a.dw[t * k + l] : 0.0f;
     if (a.renorm) {
       const float s = sum_lanes<LPR>(pj);
@@ -481,15 +545,16 @@ route_backward_kernel(RouteBwdArgs a) {
       dot = __builtin_fmaf(ex[v], f[v], dot);
     }
     dot = sum_lanes<LPR>(dot);
+    // (a row is its wave's own: LDS accesses of a wave stay in order)
     float g[VPT];
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) g[v] = f[v] - dot;
-    for (int j = 0; j < k; ++j) {
-      const int e = __shfl(id, j, LPR);
-      const float d = __shfl(dwj, j, LPR);
+    for (int v = 0; v < VPT; ++v) chosen[group][L::at(v, l)] = 0.0f;
+    wave_sync();
+    if (id >= 0) chosen[group][id] = dwj;
+    wave_sync();
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) g[v] += L::at(v, l) == e ? d : 0.0f;
-    }
+    for (int v = 0; v < VPT; ++v) g[v] = f[v] - dot + chosen[group][L::at(v, l)];
+    wave_sync();
     if (!in) continue;                                 // (whole rows: no lane of a row is left out)
     T* out = (T*)a.d_logits + t * a.ldd;
 #pragma unroll
@@ -513,7 +578,9 @@ route_backward_kernel(RouteBwdArgs a) {
 }
 
 // The kernels for a type and an E: 16 lanes per row up to 256 experts (a DPP
-// row, so that every reduction stays in registers), 64 above.
+// row: reductions take four steps, and four rows share every instruction), 64
+// above; and 64 for the rows of up to four tokens, where a row's latency counts
+// (T 1, E 256, k 8).
 typedef void (*RowsFn)(RouteArgs);
 typedef void (*BwdFn)(RouteBwdArgs);
 struct Pick {
@@ -522,22 +589,26 @@ struct Pick {
   int rows_at_once;
 };
 template <typename T>
-Pick pick_for(int E) {
+Pick pick_for(int E, bool few) {
 #define FP8G_PICK(LPR_, VPT_)                                                     \
   Pick { route_rows_kernel<T, LPR_, VPT_>, route_backward_kernel<T, LPR_, VPT_>,  \
          THREADS / LPR_ }
   if (E <= 16) return FP8G_PICK(16, 1);
   if (E <= 32) return FP8G_PICK(16, 2);
   if (E <= 64) return FP8G_PICK(16, 4);
+  if (few && E <= 256) return FP8G_PICK(64, 4);
   if (E <= 128) return FP8G_PICK(16, 8);
+  if (E <= 192) return FP8G_PICK(16, 12);
   if (E <= 256) return FP8G_PICK(16, 16);
   if (E <= 512) return FP8G_PICK(64, 8);
   return FP8G_PICK(64, 16);
 #undef FP8G_PICK
 }
-Pick pick(int type, int E) {
-  return type == TYPE_F32 ? pick_for<float>(E) : type == TYPE_BF16 ? pick_for<bf16_t>(E)
-                                                                   : pick_for<f16_t>(E);
+Pick pick(int type, int E, int64_t T) {
+  const bool few = T <= 4;
+  return type == TYPE_F32    ? pick_for<float>(E, few)
+         : type == TYPE_BF16 ? pick_for<bf16_t>(E, few)
+                             : pick_for<f16_t>(E, few);
 }
 
 bool vec_ok(const void* p, int64_t ld, int type) {
@@ -585,7 +656,7 @@ hipError_t launch_route(const RouteCall& c, hipStream_t stream) {
     route_empty_kernel<<<dim3(1), dim3(THREADS), 0, stream>>>(a);
     return hipGetLastError();
   }
-  pick(c.type, c.E).rows<<<dim3((unsigned)nblk), dim3(THREADS), 0, stream>>>(a);
+  pick(c.type, c.E, c.T).rows<<<dim3((unsigned)nblk), dim3(THREADS), 0, stream>>>(a);
   if (nblk > 1) {
     route_scan_kernel<<<dim3((unsigned)(c.E / 64 + 1)), dim3(64 * RUNS), 0, stream>>>(a, (int)nblk);
     const int64_t grid = (c.T * c.k + PAIRS - 1) / PAIRS;
@@ -611,7 +682,7 @@ hipError_t launch_route_backward(const RouteBwdCall& c, hipStream_t stream, int 
   a.renorm = c.renorm;
   a.vec = vec_ok(c.logits, c.ld, c.type) && vec_ok(c.d_logits, c.ldd, c.type);
   a.coef = c.coef;
-  const Pick p = pick(c.type, c.E);
+  const Pick p = pick(c.type, c.E, c.T);
   int64_t grid = (c.T + p.rows_at_once - 1) / p.rows_at_once;
   if (grid > (int64_t)cu_count * 8) grid = (int64_t)cu_count * 8;
   p.bwd<<<dim3((unsigned)grid), dim3(THREADS), 0, stream>>>(a);
@@ -620,11 +691,12 @@ hipError_t launch_route_backward(const RouteBwdCall& c, hipStream_t stream, int 
 
 void route_kernels(std::vector<const void*>& out) {
   for (int type : {TYPE_F32, TYPE_BF16, TYPE_F16})
-    for (int E : {16, 32, 64, 128, 256, 512, 1024}) {
-      const Pick p = pick(type, E);
-      out.push_back((const void*)p.rows);
-      out.push_back((const void*)p.bwd);
-    }
+    for (int E : {16, 32, 64, 128, 192, 256, 512, 1024})
+      for (int T : {1, 64}) {
+        const Pick p = pick(type, E, T);
+        out.push_back((const void*)p.rows);
+        out.push_back((const void*)p.bwd);
+      }
   out.push_back((const void*)route_scan_kernel);
   out.push_back((const void*)route_slots_kernel);
   out.push_back((const void*)route_empty_kernel);

@@ -84,6 +84,29 @@ def test_ties_go_to_the_lower_expert(t):
     check(x, 8, run(x, 8))
 
 
+@pytest.mark.parametrize("E", [8, 200, 256, 700])
+def test_neighbours_that_differ_in_their_last_bits_only(E):
+    """fp32 values one or a few ulps apart, equal ones among them, around the
+    k-th place too."""
+    g = np.random.default_rng(E)
+    x = (1.0 + g.integers(0, 40, size=(300, E)) * 2.0 ** -23).astype(np.float32)
+    x[1::4] *= -1
+    x[2::4] = (g.normal(size=x[2::4].shape) * 2.0 ** g.integers(-60, 60, size=(x[2::4].shape[0], 1))).astype(np.float32)
+    x[3::8, : E // 2] = 3.0
+    x = torch.from_numpy(x).to(dev())
+    for k in (1, min(E, 7), min(E, 16)):
+        check(x, k, run(x, k))
+    check(x[:3], min(E, 16), run(x[:3], min(E, 16)))
+
+
+def test_every_expert_is_chosen_when_k_is_all_of_them():
+    for E in (1, 2, 15, 16):
+        x = logits(70, E, "f32", seed=E)
+        check(x, E, run(x, E, renormalise=True), renormalise=True)
+        x = logits(3, E, "bf16", seed=E, steps=1)
+        check(x, E, run(x, E))
+
+
 @pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("T", [50, 500])
 def test_masks_closed_experts_and_empty_rows(T, t):
