@@ -27,7 +27,7 @@ namespace {
 using namespace elem;
 
 constexpr int ROWS = 64;          // tokens of a block
-constexpr int THREADS = 256;
+constexpr int THREADS = 256;       // of a workgroup, where nothing else is said
 constexpr int MAX_E = 1024;
 constexpr int MAX_K = 16;
 
@@ -38,7 +38,6 @@ struct Lay {
   static constexpr int WMAX = 16 / (int)sizeof(T);
   static constexpr int W = VPT % WMAX == 0 ? WMAX : (VPT % 4 == 0 ? 4 : VPT);
   static_assert(VPT % W == 0 && W <= WMAX, "whole groups");
-  static constexpr int ROWS_AT_ONCE = THREADS / LPR;
   __device__ static __forceinline__ int at(int v, int l) {
     return (v / W) * (W * LPR) + l * W + v % W;
   }
@@ -207,14 +206,16 @@ __device__ __forceinline__ float row_softmax(const float (&x)[VPT], float& top, 
 }
 
 // Expert offsets of the contiguous layout: exclusive prefix sums of the
-// counts rounded up to `align`, by the whole workgroup (E <= 4 THREADS).
+// counts rounded up to `align`, by the NT threads of the workgroup.
+template <int NT>
 __device__ __forceinline__ void offsets_of(const int* __restrict__ counts, int E, int align,
                                            int* __restrict__ off, int* __restrict__ wave_sum) {
+  constexpr int PER = MAX_E / NT;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  int c[4], s = 0;
+  int c[PER], s = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = t * 4 + i;
+  for (int i = 0; i < PER; ++i) {
+    const int e = t * PER + i;
     c[i] = e < E ? (counts[e] + align - 1) / align * align : 0;
     s += c[i];
   }
@@ -229,8 +230,8 @@ __device__ __forceinline__ void offsets_of(const int* __restrict__ counts, int E
   int at = inc - s;
   for (int w = 0; w < wave; ++w) at += wave_sum[w];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = t * 4 + i;
+  for (int i = 0; i < PER; ++i) {
+    const int e = t * PER + i;
     if (e < E) off[e] = at;
     at += c[i];
     if (e == E - 1) off[E] = at;
@@ -267,20 +268,25 @@ __device__ __forceinline__ int slot_of(const RouteArgs& a, int e, int first, int
   return rank < a.max_m ? (int)(e * a.max_m) + rank : -1;
 }
 
-// One block of 64 tokens per workgroup; LPR lanes per row.
-template <typename T, int LPR, int VPT>
-__global__ void __launch_bounds__(THREADS)
+// One block of 64 tokens per workgroup; LPR lanes per row. With 1024 threads
+// (16 lanes per row) all rows of a block are worked on at once: its time is
+// that of one row's chain of dependent steps, which four waves that walk the
+// block would go through four times (T 32768, E 256: 27 us).
+template <typename T, int LPR, int VPT, int NT>
+__global__ void __launch_bounds__(NT)
 route_rows_kernel(RouteArgs a) {
   using L = Lay<T, LPR, VPT>;
   constexpr int GROUPS = 64 / LPR;                     // rows of a wave at once
+  constexpr int AT_ONCE = NT / LPR;
+  constexpr int WAVES = NT / 64;
   __shared__ uint32_t took[2][MAX_E];                  // tokens of the block that chose e, as bits
   __shared__ short chosen[ROWS][MAX_K];
-  __shared__ float psum[THREADS / 64][LPR * VPT];
+  __shared__ float psum[WAVES][LPR * VPT];
   __shared__ int count[MAX_E], off[MAX_E + 1];         // (where one block is all)
-  __shared__ int wave_sum[THREADS / 64];
+  __shared__ int wave_sum[WAVES];
   __shared__ int n_routed;
   const int E = a.E, k = a.k;
-  for (int e = threadIdx.x; e < E; e += THREADS) took[0][e] = took[1][e] = 0u;
+  for (int e = threadIdx.x; e < E; e += NT) took[0][e] = took[1][e] = 0u;
   if (threadIdx.x == 0) n_routed = 0;
   __syncthreads();
   const int l = threadIdx.x & (LPR - 1), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -288,7 +294,7 @@ route_rows_kernel(RouteArgs a) {
   float acc[VPT];
 #pragma unroll
   for (int v = 0; v < VPT; ++v) acc[v] = 0.0f;
-  for (int r0 = 0; r0 < ROWS && t0 + r0 < a.T; r0 += L::ROWS_AT_ONCE) {
+  for (int r0 = 0; r0 < ROWS && t0 + r0 < a.T; r0 += AT_ONCE) {
     const int r = r0 + (int)threadIdx.x / LPR;
     const int64_t t = t0 + r;
     const bool in = t < a.T;
@@ -326,9 +332,12 @@ route_rows_kernel(RouteArgs a) {
   }
   __syncthreads();
   const bool only = gridDim.x == 1;
-  for (int e = threadIdx.x; e < E; e += THREADS) {
+  for (int e = threadIdx.x; e < E; e += NT) {
     const int c = __popc(took[0][e]) + __popc(took[1][e]);
-    const float p = (psum[0][e] + psum[1][e]) + (psum[2][e] + psum[3][e]);
+    float p = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; w += 4)
+      p += (psum[w][e] + psum[w + 1][e]) + (psum[w + 2][e] + psum[w + 3][e]);
     if (only) {
       a.counts[e] = c;
       a.prob_sum[e] = p;
@@ -346,17 +355,17 @@ route_rows_kernel(RouteArgs a) {
   if (only) {
     __syncthreads();
     if (a.max_m == 0) {
-      offsets_of(count, E, a.align, off, wave_sum);
-      for (int e = threadIdx.x; e <= E; e += THREADS) a.offsets[e] = off[e];
+      offsets_of<NT>(count, E, a.align, off, wave_sum);
+      for (int e = threadIdx.x; e <= E; e += NT) a.offsets[e] = off[e];
     } else {
-      for (int e = threadIdx.x; e <= E; e += THREADS) a.offsets[e] = (int)(e * a.max_m);
+      for (int e = threadIdx.x; e <= E; e += NT) a.offsets[e] = (int)(e * a.max_m);
     }
-    if (wave == 3) write_loss(count, psum[0], n_routed, E, k, a.coef, a.loss);
+    if (wave == WAVES - 1) write_loss(count, psum[0], n_routed, E, k, a.coef, a.loss);
   }
   // ranks inside the block (its only block: the slots themselves)
   const int64_t left = a.T - t0;
   const int rows = left < ROWS ? (int)left : ROWS;
-  for (int i = threadIdx.x; i < rows * k; i += THREADS) {
+  for (int i = threadIdx.x; i < rows * k; i += NT) {
     const int r = i / k, e = chosen[r][i - r * k];
     int s = -1;
     if (e >= 0) {
@@ -369,21 +378,21 @@ route_rows_kernel(RouteArgs a) {
   }
 }
 
-// Scan over the blocks, 64 experts per workgroup, 16 runs of blocks side by
+// Scan over the blocks, 16 experts per workgroup, 64 runs of blocks side by
 // side: counts become the tokens of earlier blocks (in place), the totals go
 // out. The last column holds the routed tokens.
-constexpr int RUNS = 16;
-__global__ void __launch_bounds__(64 * RUNS)
+constexpr int RUNS = 64, COLS = 16;
+__global__ void __launch_bounds__(COLS * RUNS)
 route_scan_kernel(RouteArgs a, int nblk) {
-  __shared__ int cnt[RUNS][64];
-  __shared__ double prob[RUNS][64];
-  const int l = threadIdx.x & 63, run = threadIdx.x >> 6;
-  const int e = blockIdx.x * 64 + l;
+  __shared__ int cnt[RUNS][COLS];
+  __shared__ double prob[RUNS][COLS];
+  const int l = threadIdx.x % COLS, run = threadIdx.x / COLS;
+  const int e = blockIdx.x * COLS + l;
   const int E = a.E;
   const int per = (nblk + RUNS - 1) / RUNS;
-  const int b0 = run * per, b1 = min(nblk, b0 + per);
+  const int b0 = min(nblk, run * per), b1 = min(nblk, b0 + per);
   // (loads in batches: a run is a chain of them otherwise)
-  constexpr int BATCH = 16;
+  constexpr int BATCH = 8;
   int s = 0;
   double p = 0.0;
   if (e <= E) {
@@ -455,7 +464,7 @@ route_slots_kernel(RouteArgs a) {
     const int64_t blk = (i0 + q * THREADS) / ((int64_t)ROWS * k);
     if (id[q] >= 0) rank[q] += a.part_count[blk * (E + 1) + id[q]];
   }
-  if (a.max_m == 0) offsets_of(a.counts, E, a.align, off, wave_sum);
+  if (a.max_m == 0) offsets_of<THREADS>(a.counts, E, a.align, off, wave_sum);
 #pragma unroll
   for (int q = 0; q < Q; ++q)                          // (without an expert: the slot is -1 already)
     if (id[q] >= 0) a.slots[i0 + q * THREADS] = slot_of(a, id[q], a.max_m == 0 ? off[id[q]] : 0, rank[q]);
@@ -463,6 +472,66 @@ route_slots_kernel(RouteArgs a) {
     for (int e = threadIdx.x; e <= E; e += THREADS)
       a.offsets[e] = a.max_m == 0 ? off[e] : (int)(e * a.max_m);
     if (threadIdx.x < 64) write_loss(a.counts, a.prob_sum, a.routed[0], E, k, a.coef, a.loss);
+  }
+}
+
+// Scan and slots in one launch, for tables of counts so small that every
+// workgroup may read all of it: one workgroup per block of tokens, EP threads
+// (a power of two over E) side by side in a row of the table.
+constexpr int JOIN_MAX = 8192;                         // entries of the table
+__global__ void __launch_bounds__(THREADS)
+route_join_kernel(RouteArgs a, int nblk, int EP) {
+  __shared__ int before[THREADS], total[THREADS];
+  __shared__ int off[MAX_E + 1];
+  __shared__ int wave_sum[THREADS / 64];
+  __shared__ double prob[THREADS];
+  __shared__ float psum[THREADS];
+  const int E = a.E, k = a.k, blk = blockIdx.x;
+  const int t = threadIdx.x, e = t & (EP - 1), run = t / EP, runs = THREADS / EP;
+  const int64_t t0 = (int64_t)blk * ROWS;
+  const int pairs = (int)(min((int64_t)ROWS, a.T - t0) * k);
+  constexpr int Q = ROWS * MAX_K / THREADS;
+  int id[Q], rank[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    const int i = t + q * THREADS;
+    id[q] = i < pairs ? a.ids[t0 * k + i] : -1;
+    rank[q] = i < pairs ? a.slots[t0 * k + i] : 0;
+  }
+  before[t] = total[t] = 0;
+  __syncthreads();
+  int all = 0, early = 0;
+  double p = 0.0;
+  if (e <= E) {
+#pragma unroll 4
+    for (int b = run; b < nblk; b += runs) {
+      const int c = a.part_count[(int64_t)b * (E + 1) + e];
+      all += c;
+      early += b < blk ? c : 0;
+      if (blk == 0 && e < E) p += (double)a.part_prob[(int64_t)b * E + e];
+    }
+    atomicAdd(&total[e], all);
+    atomicAdd(&before[e], early);
+  }
+  prob[t] = p;
+  __syncthreads();
+  if (a.max_m == 0) offsets_of<THREADS>(total, E, a.align, off, wave_sum);
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    if (id[q] >= 0)
+      a.slots[t0 * k + t + q * THREADS] =
+          slot_of(a, id[q], a.max_m == 0 ? off[id[q]] : 0, before[id[q]] + rank[q]);
+  if (blk == 0) {
+    if (t <= E) a.offsets[t] = a.max_m == 0 ? off[t] : (int)(t * a.max_m);
+    if (t < E) {
+      double s = 0.0;
+      for (int r = 0; r < runs; ++r) s += prob[r * EP + t];
+      a.counts[t] = total[t];
+      a.prob_sum[t] = psum[t] = (float)s;
+    }
+    if (t == 0) a.routed[0] = total[E];
+    __syncthreads();
+    if (t < 64) write_loss(total, psum, total[E], E, k, a.coef, a.loss);
   }
 }
 
@@ -505,7 +574,8 @@ __global__ void __launch_bounds__(THREADS)
 route_backward_kernel(RouteBwdArgs a) {
   using L = Lay<T, LPR, VPT>;
   // the chosen experts' gradients of each row, in the lanes' order of experts
-  __shared__ __attribute__((aligned(16))) float chosen[L::ROWS_AT_ONCE][LPR * VPT];
+  constexpr int AT_ONCE = THREADS / LPR;
+  __shared__ __attribute__((aligned(16))) float chosen[AT_ONCE][LPR * VPT];
   const int E = a.E, k = a.k;
   const int l = threadIdx.x & (LPR - 1), group = threadIdx.x / LPR;
   const int n = a.routed[0];
@@ -519,20 +589,22 @@ route_backward_kernel(RouteBwdArgs a) {
     const int e = L::at(v, l);
     f[v] = e < E ? fac * (float)a.counts[e] : 0.0f;
   }
-  for (int64_t t0 = (int64_t)blockIdx.x * L::ROWS_AT_ONCE; t0 < a.T;
-       t0 += (int64_t)gridDim.x * L::ROWS_AT_ONCE) {
+  for (int64_t t0 = (int64_t)blockIdx.x * AT_ONCE; t0 < a.T;
+       t0 += (int64_t)gridDim.x * AT_ONCE) {
     const int64_t t = t0 + group;
     const bool in = t < a.T;
     const T* row = (const T*)a.logits + (in ? t : 0) * a.ld;
-    int id = -1;
-    if (in && l < k) id = a.ids[t * k + l];
-    if (id >= E || id < 0) id = -1;
-    const bool on = __shfl(id, 0, LPR) >= 0;
+    // (all loads at once; what a row that takes no part holds does not matter)
+    int id = in && l < k ? a.ids[t * k + l] : -1;
+    float dwj = in && l < k && a.dw ? a.dw[t * k + l] : 0.0f;
     float x[VPT], ex[VPT], top;
-    load_row<T, LPR, VPT>(row, E, l, on, a.vec != 0, x);
+    load_row<T, LPR, VPT>(row, E, l, in, a.vec != 0, x);
+    if (id >= E || id < 0) id = -1;
+    const float xj = id >= 0 ? to_f32(row[id]) : 0.0f;
+    const bool on = __shfl(id, 0, LPR) >= 0;
     const float inv = row_softmax<LPR, VPT>(x, top, ex);
-    const float pj = id >= 0 && on ? exp_neg(to_f32(row[id]) - top) * inv : 0.0f;
-    float dwj = id >= 0 && a.dw ? a.dw[t * k + l] : 0.0f;
+    const float pj = id >= 0 ? exp_neg(xj - top) * inv : 0.0f;
+    if (id < 0) dwj = 0.0f;
     if (a.renorm) {
       const float s = sum_lanes<LPR>(pj);
       const float c = sum_lanes<LPR>(id >= 0 ? dwj * pj : 0.0f);
@@ -585,13 +657,15 @@ typedef void (*RowsFn)(RouteArgs);
 typedef void (*BwdFn)(RouteBwdArgs);
 struct Pick {
   RowsFn rows;
+  int rows_threads;
   BwdFn bwd;
   int rows_at_once;
 };
-template <typename T>
-Pick pick_for(int E, bool few) {
+template <typename T, int NT>
+Pick pick_for(int E) {
+  constexpr bool few = NT == THREADS;
 #define FP8G_PICK(LPR_, VPT_)                                                     \
-  Pick { route_rows_kernel<T, LPR_, VPT_>, route_backward_kernel<T, LPR_, VPT_>,  \
+  Pick { route_rows_kernel<T, LPR_, VPT_, NT>, NT, route_backward_kernel<T, LPR_, VPT_>, \
          THREADS / LPR_ }
   if (E <= 16) return FP8G_PICK(16, 1);
   if (E <= 32) return FP8G_PICK(16, 2);
@@ -604,11 +678,14 @@ Pick pick_for(int E, bool few) {
   return FP8G_PICK(64, 16);
 #undef FP8G_PICK
 }
+template <typename T>
+Pick pick_of(int E, int64_t tokens) {
+  return tokens <= 4 ? pick_for<T, THREADS>(E) : pick_for<T, 1024>(E);
+}
 Pick pick(int type, int E, int64_t T) {
-  const bool few = T <= 4;
-  return type == TYPE_F32    ? pick_for<float>(E, few)
-         : type == TYPE_BF16 ? pick_for<bf16_t>(E, few)
-                             : pick_for<f16_t>(E, few);
+  return type == TYPE_F32    ? pick_of<float>(E, T)
+         : type == TYPE_BF16 ? pick_of<bf16_t>(E, T)
+                             : pick_of<f16_t>(E, T);
 }
 
 bool vec_ok(const void* p, int64_t ld, int type) {
@@ -656,9 +733,14 @@ hipError_t launch_route(const RouteCall& c, hipStream_t stream) {
     route_empty_kernel<<<dim3(1), dim3(THREADS), 0, stream>>>(a);
     return hipGetLastError();
   }
-  pick(c.type, c.E, c.T).rows<<<dim3((unsigned)nblk), dim3(THREADS), 0, stream>>>(a);
-  if (nblk > 1) {
-    route_scan_kernel<<<dim3((unsigned)(c.E / 64 + 1)), dim3(64 * RUNS), 0, stream>>>(a, (int)nblk);
+  const Pick p = pick(c.type, c.E, c.T);
+  p.rows<<<dim3((unsigned)nblk), dim3((unsigned)p.rows_threads), 0, stream>>>(a);
+  if (nblk > 1 && c.E < THREADS && nblk * (c.E + 1) <= JOIN_MAX) {
+    int ep = 1;
+    while (ep <= c.E) ep *= 2;
+    route_join_kernel<<<dim3((unsigned)nblk), dim3(THREADS), 0, stream>>>(a, (int)nblk, ep);
+  } else if (nblk > 1) {
+    route_scan_kernel<<<dim3((unsigned)(c.E / COLS + 1)), dim3(COLS * RUNS), 0, stream>>>(a, (int)nblk);
     const int64_t grid = (c.T * c.k + PAIRS - 1) / PAIRS;
     route_slots_kernel<<<dim3((unsigned)grid), dim3(THREADS), 0, stream>>>(a);
   }
@@ -699,6 +781,7 @@ void route_kernels(std::vector<const void*>& out) {
       }
   out.push_back((const void*)route_scan_kernel);
   out.push_back((const void*)route_slots_kernel);
+  out.push_back((const void*)route_join_kernel);
   out.push_back((const void*)route_empty_kernel);
 }
 
