@@ -146,7 +146,9 @@ clip_kernel(Table t, const double* __restrict__ sumsq, float max_norm, float* __
   const double q = (double)max_norm / (nrm + 1e-6);
   const float f = q >= 1.0 ? 1.0f : (float)q;          // (NaN stays NaN)
   const int chunks = t.n ? t.end[t.n - 1] : 0;
-  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+  // (last chunks first: of what the norm's pass read, the end is what the
+  // caches still hold)
+  for (int c = chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
     int64_t at;
     const int i = find(t, c, at);
     if (t.x[i] == t.y[i] && f == 1.0f) continue;

@@ -84,15 +84,11 @@ __device__ __forceinline__ double sum_wave(double x) {
   return x;
 }
 
-// exp(x) for x <= 0 (or NaN) within 2 ulp: 2^(x log2 e), the product's
-// rounding error put back to first order. Below -150 the result is 0.
+// exp(x) for x <= 0 (or NaN) as 2^(x log2 e): the product's rounding makes its
+// relative error |x| 2^-24 at most (as much as a difference x = a - b of that
+// size carries already), and -inf gives 0 without a test.
 __device__ __forceinline__ float exp_neg(float x) {
-  constexpr float L2E = 0x1.715476p+0f, L2E_LO = 0x1.4ae0cp-26f, LN2 = 0x1.62e43p-1f;
-  x = x < -150.0f ? -150.0f : x;
-  const float t = x * L2E;
-  const float lo = __builtin_fmaf(x, L2E_LO, __builtin_fmaf(x, L2E, -t));
-  const float y = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(y, lo * LN2, y);
+  return __builtin_amdgcn_exp2f(x * 0x1.715476p+0f);
 }
 
 }  // namespace elem

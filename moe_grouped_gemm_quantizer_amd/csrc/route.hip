@@ -325,8 +325,11 @@ route_rows_kernel(RouteArgs a) {
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     if constexpr (GROUPS > 1) {
-      acc[v] += __shfl_xor(acc[v], 16);
-      acc[v] += __shfl_xor(acc[v], 32);
+      const uint32_t u = __float_as_uint(acc[v]);
+      const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+      const uint32_t w = __float_as_uint(__uint_as_float(p[0]) + __uint_as_float(p[1]));
+      const auto q = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+      acc[v] = __uint_as_float(q[0]) + __uint_as_float(q[1]);
     }
     if (lane < LPR) psum[wave][L::at(v, l)] = acc[v];
   }
