@@ -23,6 +23,7 @@ constexpr int THREADS = 256;
 constexpr int MAX_T = 112;                             // tensors of a launch
 constexpr int64_t CHUNK = 32768;                       // elements of a chunk
 constexpr int64_t MAX_GRID = 2048;                     // eight workgroups per CU
+constexpr int64_t STREAM_BYTES = 192 << 20;            // lists from here on outgrow the caches
 
 struct Table {
   const void* x[MAX_T];
@@ -119,7 +120,14 @@ __device__ __forceinline__ T scaled(T x, float f) {
   return from_f32<T>(p);
 }
 
-template <typename T>
+// Stores are non-temporal: the next reader is another kernel, and the list's
+// own values are what should stay in the caches (8 x 29M bf16, norm and
+// clipping: 278 -> 246 us; 8 x 2M: 22.6 -> 22.4). STREAM: so are the loads,
+// for a list larger than the caches, where they would push out what the
+// norm's pass left there (8 x 29M: 246 -> 233 us, 8 x 16M: 135 -> 131; but
+// 8 x 8M 66.5 -> 69, 8 x 2M 22.4 -> 29).
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <bool STREAM, typename T>
 __device__ __forceinline__ void chunk_scale(const T* x, T* y, int n, float f) {
   constexpr int W = 16 / (int)sizeof(T);
   int done = 0;
@@ -128,16 +136,18 @@ __device__ __forceinline__ void chunk_scale(const T* x, T* y, int n, float f) {
     done = packs * W;
 #pragma unroll 4
     for (int i = threadIdx.x; i < packs; i += THREADS) {
-      Pack<T, W> p = reinterpret_cast<const Pack<T, W>*>(x)[i];
+      const u32x4* const at = reinterpret_cast<const u32x4*>(x) + i;
+      Pack<T, W> p = __builtin_bit_cast(Pack<T, W>, STREAM ? __builtin_nontemporal_load(at) : *at);
 #pragma unroll
       for (int w = 0; w < W; ++w) p.v[w] = scaled(p.v[w], f);
-      reinterpret_cast<Pack<T, W>*>(y)[i] = p;
+      __builtin_nontemporal_store(__builtin_bit_cast(u32x4, p), reinterpret_cast<u32x4*>(y) + i);
     }
   }
   for (int i = done + threadIdx.x; i < n; i += THREADS) y[i] = scaled(x[i], f);
 }
 
 // (n == 0: one workgroup writes the norm)
+template <bool STREAM>
 __global__ void __launch_bounds__(THREADS)
 clip_kernel(Table t, const double* __restrict__ sumsq, float max_norm, float* __restrict__ norm,
             int write_norm) {
@@ -155,11 +165,11 @@ clip_kernel(Table t, const double* __restrict__ sumsq, float max_norm, float* __
     const int64_t left = t.numel[i] - at;
     const int n = (int)(left < CHUNK ? left : CHUNK);
     if (t.type[i] == TYPE_F32)
-      chunk_scale((const float*)t.x[i] + at, (float*)t.y[i] + at, n, f);
+      chunk_scale<STREAM>((const float*)t.x[i] + at, (float*)t.y[i] + at, n, f);
     else if (t.type[i] == TYPE_BF16)
-      chunk_scale((const bf16_t*)t.x[i] + at, (bf16_t*)t.y[i] + at, n, f);
+      chunk_scale<STREAM>((const bf16_t*)t.x[i] + at, (bf16_t*)t.y[i] + at, n, f);
     else
-      chunk_scale((const f16_t*)t.x[i] + at, (f16_t*)t.y[i] + at, n, f);
+      chunk_scale<STREAM>((const f16_t*)t.x[i] + at, (f16_t*)t.y[i] + at, n, f);
   }
 }
 
@@ -225,12 +235,15 @@ hipError_t launch_grad_clip(const void* const* grads, void* const* outs, const i
                             const int* types, int n, const double* sumsq, float max_norm,
                             float* norm, hipStream_t stream) {
   Table t;
+  int64_t bytes = 0;
+  for (int j = 0; j < n && bytes < STREAM_BYTES; ++j) bytes += numels[j] * (types[j] == TYPE_F32 ? 4 : 2);
+  const auto kernel = bytes >= STREAM_BYTES ? clip_kernel<true> : clip_kernel<false>;
   int i = 0, first = 1;
   for (;;) {
     const int64_t grid = fill(t, i, grads, outs, numels, types, n);
     if (grid == 0 && !first) break;
-    clip_kernel<<<dim3((unsigned)(grid ? grid : 1)), dim3(THREADS), 0, stream>>>(
-        t, sumsq, max_norm, norm, first);
+    kernel<<<dim3((unsigned)(grid ? grid : 1)), dim3(THREADS), 0, stream>>>(t, sumsq, max_norm, norm,
+                                                                            first);
     first = 0;
     if (grid == 0) break;
   }
@@ -240,7 +253,8 @@ hipError_t launch_grad_clip(const void* const* grads, void* const* outs, const i
 void clip_kernels(std::vector<const void*>& out) {
   out.push_back((const void*)norm_partial_kernel);
   out.push_back((const void*)norm_finish_kernel);
-  out.push_back((const void*)clip_kernel);
+  out.push_back((const void*)clip_kernel<false>);
+  out.push_back((const void*)clip_kernel<true>);
 }
 
 }  // namespace fp8g

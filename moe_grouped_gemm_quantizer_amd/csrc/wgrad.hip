@@ -18,7 +18,6 @@ namespace {
 using namespace elem;
 
 typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 // ---------------------------------------------------------------------------
@@ -244,19 +243,68 @@ quant_transpose_kernel(const T* __restrict__ x, int64_t rows, int64_t cols, int6
 }
 
 // ---------------------------------------------------------------------------
-// The product. 128x128 tiles, four waves of 64x64; each K step (128 tokens)
-// goes through registers into LDS.
+// The product. Two kernels: 256x256 tiles where there are enough of them to
+// fill the chip, 128x128 tiles below. In both, codes go from global memory
+// straight into LDS; each 128-byte LDS row holds one row's 128 tokens, its
+// 16-byte chunks swizzled (swz).
 
-constexpr int BT = 128;
-constexpr int ROWB = 128 + 16;                         // LDS row: 128 codes, padded
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr_t)p);
+}
+// Direct global -> LDS copies, through inline assembly so that the compiler
+// does not wait for all of them before the next LDS read; the waits are
+// explicit, before the barrier that publishes a stage.
+__device__ __forceinline__ void copy16(const void* base, uint32_t voff, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "{m0}"(lds)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(const void* base, uint32_t voff, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "{m0}"(lds)
+               : "memory");
+}
+constexpr int vmcnt_only(int n) { return (n & 0xF) | (0x7 << 4) | (0xF << 8) | (((n >> 4) & 3) << 14); }
 
-__device__ __forceinline__ v8i frag(const uint8_t* p) {
-  const uint4 lo = *reinterpret_cast<const uint4*>(p);
-  const uint4 hi = *reinterpret_cast<const uint4*>(p + 16);
-  v8i f;
-  f[0] = (int)lo.x; f[1] = (int)lo.y; f[2] = (int)lo.z; f[3] = (int)lo.w;
-  f[4] = (int)hi.x; f[5] = (int)hi.y; f[6] = (int)hi.z; f[7] = (int)hi.w;
-  return f;
+// Chunk swizzle of an LDS row of 128 bytes (16-byte chunks): fragment reads
+// of 8 or 16 consecutive rows meet every bank group equally.
+__device__ __forceinline__ int swz(int row, int chunk) {
+  return chunk ^ (row & 7) ^ ((row >> 3) & 1);
+}
+
+// Fragment f of a band of rows, tokens 64 kh .. +63: lane l holds position
+// l % 32, tokens 32 (l / 32) .. +31 of those.
+__device__ __forceinline__ v8i read_frag(const uint8_t* band, int f, int kh, int lane) {
+  const int r = f * 32 + (lane & 31), c = kh * 4 + (lane >> 5) * 2;
+  const uint4 lo = *reinterpret_cast<const uint4*>(band + r * 128 + swz(r, c) * 16);
+  const uint4 hi = *reinterpret_cast<const uint4*>(band + r * 128 + swz(r, c + 1) * 16);
+  v8i v;
+  v[0] = (int)lo.x; v[1] = (int)lo.y; v[2] = (int)lo.z; v[3] = (int)lo.w;
+  v[4] = (int)hi.x; v[5] = (int)hi.y; v[6] = (int)hi.z; v[7] = (int)hi.w;
+  return v;
+}
+
+// Fragments j of b and i of a, whose exponents are bytes j and i of sb and
+// sa. (i and j are constants where this is inlined.)
+template <int FA, int FB>
+__device__ __forceinline__ v16f mfma(const v8i& b, const v8i& a, const v16f& c, int j, uint32_t sb,
+                                     int i, uint32_t sa) {
+#define FP8G_M(J_, I_)                                                                          \
+  case J_ * 4 + I_:                                                                             \
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, FB, FA, J_, (int)sb, I_,    \
+                                                           (int)sa);
+#define FP8G_M4(J_) FP8G_M(J_, 0) FP8G_M(J_, 1) FP8G_M(J_, 2) FP8G_M(J_, 3)
+  switch (j * 4 + i) {
+    FP8G_M4(0) FP8G_M4(1) FP8G_M4(2) FP8G_M4(3)
+  }
+#undef FP8G_M4
+#undef FP8G_M
+  return c;
+}
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16_pair(float x, float y) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
 }
 
 // The blocks of 128 tokens of expert g.
@@ -272,67 +320,108 @@ __device__ __forceinline__ void token_blocks(const WgradArgs& a, int g, int& kb0
   kb1 = hi < 0 ? 0 : min(hi / 128, last);
 }
 
+// 128x128 tiles, four waves of 64x64, four LDS stages: the copies of three
+// steps are on their way while one is multiplied, since with few workgroups
+// a step's time is what its copies take to arrive. One barrier a step: it
+// publishes the stage that has landed and frees the one read before. Position r
+// of fragment i of a wave's 64 rows is row 2 r + i, so that a lane's exponents
+// are two adjacent bytes and its results runs of 8 columns.
+constexpr int BT = 128;
+constexpr int RING = 4;
+constexpr int RSTAGE = 2 * BT * 128 + 2 * BT;
+constexpr int RCOPIES = 9;                             // a wave's copies of a stage
+
 template <int FA, int FB>
-__global__ void __launch_bounds__(256)
-wgrad_kernel(WgradArgs a, int mblocks, int nblocks) {
-  __shared__ __attribute__((aligned(16))) uint8_t la[BT * ROWB], lb[BT * ROWB];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-  const int64_t tile = blockIdx.x;
-  const int g = (int)(tile / ((int64_t)mblocks * nblocks));
-  const int in_g = (int)(tile - (int64_t)g * mblocks * nblocks);
+__global__ void __launch_bounds__(256, 1)
+wgrad_ring_kernel(WgradArgs a, int mblocks, int nblocks) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[RING * RSTAGE];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int per = mblocks * nblocks;
+  const int g = (int)blockIdx.x / per, in_g = (int)blockIdx.x - g * per;
   const int64_t m0 = (int64_t)(in_g % mblocks) * BT, n0 = (int64_t)(in_g / mblocks) * BT;
+  const int mv = (int)min((int64_t)BT, a.M - m0), nv = (int)min((int64_t)BT, a.N - n0);
   int kb0, kb1;
   token_blocks(a, g, kb0, kb1);
-  v4f acc[4][4];
+  const int steps = __builtin_amdgcn_readfirstlane(kb1 - kb0);
+  // copies: waves 0 and 1 take a's two bands of 64 rows, 2 and 3 b's; copy c
+  // is fragment c / 4, positions 8 (c % 4) .. +7; then 128 exponents (0 and 2 a's,
+  // 1 and 3 b's)
+  const uint8_t* const src = wave < 2 ? a.a + m0 * a.lda : a.b + n0 * a.ldb;
+  const uint32_t ld = (uint32_t)(wave < 2 ? a.lda : a.ldb);
+  const int last = (wave < 2 ? mv : nv) - 1, band = (wave & 1) * 64;
+  const uint8_t* const esrc = (wave & 1) ? a.sb + n0 : a.sa + m0;
+  const int64_t estep = (wave & 1) ? a.N : a.M;
+  const uint32_t eoff = (uint32_t)min((lane & 31) * 4, ((wave & 1) ? nv : mv) - 4);
+  uint32_t voff[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int kb = kb0; kb < kb1; ++kb) {
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int i = q * 256 + (int)threadIdx.x, r = i >> 3, c = (i & 7) * 16;
-      const int64_t ra = min(m0 + r, a.M - 1), rb = min(n0 + r, a.N - 1);
-      *reinterpret_cast<uint4*>(la + r * ROWB + c) =
-          *reinterpret_cast<const uint4*>(a.a + ra * a.lda + (int64_t)kb * 128 + c);
-      *reinterpret_cast<uint4*>(lb + r * ROWB + c) =
-          *reinterpret_cast<const uint4*>(a.b + rb * a.ldb + (int64_t)kb * 128 + c);
-    }
-    int sa[4], sb[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sa[i] = a.sa[(int64_t)kb * a.M + min(m0 + wm + i * 16 + (lane & 15), a.M - 1)];
-      sb[i] = a.sb[(int64_t)kb * a.N + min(n0 + wn + i * 16 + (lane & 15), a.N - 1)];
-    }
-    __syncthreads();
-    v8i fa[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      fa[i] = frag(la + (wm + i * 16 + (lane & 15)) * ROWB + (lane >> 4) * 32);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const v8i fb = frag(lb + (wn + j * 16 + (lane & 15)) * ROWB + (lane >> 4) * 32);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa[i], acc[i][j], FB, FA, 0,
-                                                                     sb[j], 0, sa[i]);
-    }
+  for (int c = 0; c < 8; ++c) {
+    const int row = band + ((c & 3) * 8 + (lane >> 3)) * 2 + (c >> 2);
+    voff[c] = (uint32_t)min(row, last) * ld + (uint32_t)((lane & 7) ^ (lane >> 3) ^ (c & 1)) * 16u;
   }
-  // (b first: lane l holds row l & 15 of the tile, columns 4 (l >> 4) .. +3)
+  const uint32_t base = lds_addr(lds);
+  auto issue_stage = [&](int s) __attribute__((always_inline)) {
+    // (past the end the last step again, for nothing: every wait counts alike)
+    const int64_t kb = kb0 + min(s, steps - 1);
+    const uint32_t st = base + (uint32_t)(s % RING) * RSTAGE;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + wm + i * 16 + (lane & 15);
+    for (int c = 0; c < 8; ++c)
+      copy16(src + kb * 128, voff[c], st + (uint32_t)((wave >> 1) * BT + band + c * 8) * 128u);
+    if (lane < 32) copy4(esrc + kb * estep, eoff, st + 2 * BT * 128 + (wave & 1) * BT);
+  };
+  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+  v16f acc[2][2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t n = n0 + wn + j * 16 + (lane >> 4) * 4;
-      if (m < a.M && n < a.N) {
-        Pack<bf16_t, 4> o;
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o.v[e] = from_f32<bf16_t>(acc[i][j][e]);
-        *reinterpret_cast<Pack<bf16_t, 4>*>(a.d + ((int64_t)g * a.M + m) * a.N + n) = o;
+    for (int j = 0; j < 2; ++j) acc[i][j] = v16f{};
+  if (steps > 0) {
+#pragma unroll
+    for (int s = 0; s < RING - 1; ++s) issue_stage(s);
+    for (int s = 0; s < steps; ++s) {
+      // (own reads of the stage before have fed matrix instructions)
+      __builtin_amdgcn_s_waitcnt(vmcnt_only((RING - 2) * RCOPIES));
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("s_barrier" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      issue_stage(s + RING - 1);
+      const uint8_t* const st = lds + (s % RING) * RSTAGE;
+      const uint32_t sa = *reinterpret_cast<const uint16_t*>(st + 2 * BT * 128 + wm + (lane & 31) * 2);
+      const uint32_t sb =
+          *reinterpret_cast<const uint16_t*>(st + 2 * BT * 128 + BT + wn + (lane & 31) * 2);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        v8i fa[2], fb[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          fa[i] = read_frag(st + wm * 128, i, h, lane);
+          fb[i] = read_frag(st + BT * 128 + wn * 128, i, h, lane);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[i][j] = mfma<FA, FB>(fb[j], fa[i], acc[i][j], j, sb, i, sa);
       }
+      // (every LDS read of this stage has arrived before the next barrier)
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+    }
+    // (no copy may arrive after the workgroup's LDS is someone else's)
+    __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+  }
+  // b is the first operand: lane l holds position l % 32 of fragment i of a,
+  // and of fragment j of b positions 8 t + 4 (l / 32) + e; column 2 position + j
+  uint16_t* const d = a.d + ((int64_t)g * a.M + m0) * a.N + n0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = wm + (lane & 31) * 2 + i;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int col = wn + t * 16 + (lane >> 5) * 8;
+      u32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = bf16_pair(acc[i][0][4 * t + e], acc[i][1][4 * t + e]);
+      if (row < mv && col < nv) *reinterpret_cast<u32x4*>(d + (int64_t)row * a.N + col) = v;
     }
   }
 }
@@ -372,23 +461,6 @@ constexpr int EARLY_FIRST = 8;                         // of these, issued in a 
 constexpr int STORES = 32;                             // a wave's stores of a full tile
 constexpr int MAX_G = 1024;
 
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr_t)p);
-}
-// Direct global -> LDS copies, through inline assembly so that the compiler
-// does not wait for all of them before the next LDS read; the waits are
-// explicit (the barrier of slice 4).
-__device__ __forceinline__ void copy16(const void* base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "{m0}"(lds)
-               : "memory");
-}
-__device__ __forceinline__ void copy4(const void* base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "{m0}"(lds)
-               : "memory");
-}
-constexpr int vmcnt_only(int n) { return (n & 0xF) | (0x7 << 4) | (0xF << 8) | (((n >> 4) & 3) << 14); }
-
 // The experts that have tokens, in order, and those that have none.
 struct Experts {
   int full[MAX_G], kb0[MAX_G], steps[MAX_G];
@@ -401,12 +473,6 @@ struct Tile {
   uint16_t* d;
   int mv, nv, steps;                                   // rows and columns that exist
 };
-
-// Chunk swizzle of an LDS row of 128 bytes (16-byte chunks): fragment reads
-// of 16 consecutive rows meet every bank group equally.
-__device__ __forceinline__ int swz(int row, int chunk) {
-  return chunk ^ (row & 7) ^ ((row >> 3) & 1);
-}
 
 __device__ __forceinline__ void tile_of(const WgradArgs& a, const Experts& ex, int slot, int mblocks,
                                         int nblocks, Tile& t) {
@@ -470,42 +536,6 @@ __device__ __forceinline__ void issue(const Plan& p, const WgradArgs& a, const T
     copy16(t.b + (int64_t)kb * 128, min(p.vb + (uint32_t)(f + 64 * half) * ldb, p.mb),
            dst + TS * 128 + (uint32_t)(f * 4096 + half * 2048));
   }
-}
-
-// Fragment f, tokens 64 kh .. +63: lane l holds position l % 32, tokens
-// 32 (l / 32) .. +31 of those.
-__device__ __forceinline__ v8i read_frag(const uint8_t* band, int f, int kh, int lane) {
-  const int r = f * 32 + (lane & 31), c = kh * 4 + (lane >> 5) * 2;
-  const uint4 lo = *reinterpret_cast<const uint4*>(band + r * 128 + swz(r, c) * 16);
-  const uint4 hi = *reinterpret_cast<const uint4*>(band + r * 128 + swz(r, c + 1) * 16);
-  v8i v;
-  v[0] = (int)lo.x; v[1] = (int)lo.y; v[2] = (int)lo.z; v[3] = (int)lo.w;
-  v[4] = (int)hi.x; v[5] = (int)hi.y; v[6] = (int)hi.z; v[7] = (int)hi.w;
-  return v;
-}
-
-// Fragments j of b and i of a, whose exponents are bytes j and i of sb and
-// sa. (i and j are constants where this is inlined.)
-template <int FA, int FB>
-__device__ __forceinline__ v16f mfma(const v8i& b, const v8i& a, const v16f& c, int j, uint32_t sb,
-                                     int i, uint32_t sa) {
-#define FP8G_M(J_, I_)                                                                          \
-  case J_ * 4 + I_:                                                                             \
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, FB, FA, J_, (int)sb, I_,    \
-                                                           (int)sa);
-#define FP8G_M4(J_) FP8G_M(J_, 0) FP8G_M(J_, 1) FP8G_M(J_, 2) FP8G_M(J_, 3)
-  switch (j * 4 + i) {
-    FP8G_M4(0) FP8G_M4(1) FP8G_M4(2) FP8G_M4(3)
-  }
-#undef FP8G_M4
-#undef FP8G_M
-  return c;
-}
-
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t bf16_pair(float x, float y) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
 }
 
 template <int FA, int FB>
@@ -744,10 +774,10 @@ TileFn tile_pick(int fa, int fb) {
   if (fa == FMT_E4M3) return fb == FMT_E4M3 ? wgrad_tile_kernel<0, 0> : wgrad_tile_kernel<0, 1>;
   return fb == FMT_E4M3 ? wgrad_tile_kernel<1, 0> : wgrad_tile_kernel<1, 1>;
 }
-typedef void (*WgradFn)(WgradArgs, int, int);
-WgradFn wgrad_pick(int fa, int fb) {
-  if (fa == FMT_E4M3) return fb == FMT_E4M3 ? wgrad_kernel<0, 0> : wgrad_kernel<0, 1>;
-  return fb == FMT_E4M3 ? wgrad_kernel<1, 0> : wgrad_kernel<1, 1>;
+typedef void (*RingFn)(WgradArgs, int, int);
+RingFn ring_pick(int fa, int fb) {
+  if (fa == FMT_E4M3) return fb == FMT_E4M3 ? wgrad_ring_kernel<0, 0> : wgrad_ring_kernel<0, 1>;
+  return fb == FMT_E4M3 ? wgrad_ring_kernel<1, 0> : wgrad_ring_kernel<1, 1>;
 }
 
 }  // namespace
@@ -763,6 +793,10 @@ hipError_t launch_quantize_transpose(const void* x, int type, int64_t rows, int6
 hipError_t launch_wgrad(const WgradArgs& args, int fmt_a, int fmt_b, const DeviceInfo& dev,
                         hipStream_t stream) {
   const int64_t mb = (args.M + TS - 1) / TS, nb = (args.N + TS - 1) / TS, all = mb * nb * args.G;
+  // 256x256 tiles from half the CUs on: below that, at most two rounds of 128x128
+  // tiles, whose copies are further ahead (dense, T 4096: 64 tiles 24.7
+  // against 41.3 us, 112 tiles 43.4 / 41.5, 140 tiles 62.5 / 41.6, 256 tiles 81.7
+  // / 49.4; T 1024: 45 tiles 8.5 / 17.1, 112 tiles 16.8 / 17.2, 140 tiles 23.7 / 16.9)
   if (all >= dev.cu_count / 2 && args.T > 0) {
     const int64_t grid = all < dev.cu_count ? all : dev.cu_count;
     tile_pick(fmt_a, fmt_b)<<<dim3((unsigned)grid), dim3(256), 0, stream>>>(
@@ -770,7 +804,7 @@ hipError_t launch_wgrad(const WgradArgs& args, int fmt_a, int fmt_b, const Devic
     return hipGetLastError();
   }
   const int64_t mblocks = (args.M + BT - 1) / BT, nblocks = (args.N + BT - 1) / BT;
-  wgrad_pick(fmt_a, fmt_b)<<<dim3((unsigned)(mblocks * nblocks * args.G)), dim3(256), 0, stream>>>(
+  ring_pick(fmt_a, fmt_b)<<<dim3((unsigned)(mblocks * nblocks * args.G)), dim3(256), 0, stream>>>(
       args, (int)mblocks, (int)nblocks);
   return hipGetLastError();
 }
@@ -781,7 +815,7 @@ void wgrad_kernels(std::vector<const void*>& out) {
     out.push_back((const void*)quant_kernel<bf16_t>(fmt));
     out.push_back((const void*)quant_kernel<f16_t>(fmt));
     for (int fb : {FMT_E4M3, FMT_E5M2}) {
-      out.push_back((const void*)wgrad_pick(fmt, fb));
+      out.push_back((const void*)ring_pick(fmt, fb));
       out.push_back((const void*)tile_pick(fmt, fb));
     }
   }
