@@ -431,17 +431,16 @@ def _fail(msg):
 
 
 def _rows(t, what):
-    """Row stride of a matrix whose rows are contiguous."""
+    """Pointer, rows, columns and row stride of a GPU matrix whose rows are
+    contiguous."""
     if not t.is_cuda or t.dim() != 2:
         _fail(f"{what} must be a matrix on the GPU")
     rows, cols = t.shape
-    if cols <= 1:
-        return t.stride(0) if cols and rows > 1 else cols
     ld, one = t.stride()
-    if one != 1:
+    if one != 1 and cols > 1:
         _fail(f"{what}: the elements of a row must be contiguous")
-    # (a single row has any stride)
-    return ld if rows > 1 else cols
+    # (a single row has any stride, and so have empty ones)
+    return t.data_ptr(), rows, cols, ld if rows > 1 and cols > 0 else cols
 
 
 def _out(t, shape, dtype, what):
@@ -479,8 +478,7 @@ def moe_route(logits, top_k, expert_ids, weights, counts, routed, prob_sum, loss
     [T][top_k] (row of each pair in that layout, -1: none). workspace: a device
     tensor of at least moe_route_workspace_size(T, E) bytes."""
     torch = _torch()
-    ld = _rows(logits, "logits")
-    T, E = logits.shape
+    ptr, T, E, ld = _rows(logits, "logits")
     typ = _TYPES.get(logits.dtype)
     if typ is None:
         _fail("logits must be float32, bfloat16 or float16")
@@ -497,7 +495,7 @@ def moe_route(logits, top_k, expert_ids, weights, counts, routed, prob_sum, loss
     if token_mask is not None:
         mask = _out(token_mask, (T,), torch.uint8 if token_mask.dtype is torch.uint8 else torch.bool, "token_mask")
     wp, wb = _room(workspace)
-    st = load().moe_route(logits.data_ptr(), typ, T, E, ld, mask, top_k, 1 if renormalise else 0, loss_coef,
+    st = load().moe_route(ptr, typ, T, E, ld, mask, top_k, 1 if renormalise else 0, loss_coef,
                           align, max_m, ids, wts, cnt, rtd, psm, los, off, slt, wp, wb, _stream(stream))
     if st:
         _check(st, "moe_route")
@@ -511,10 +509,10 @@ def moe_route_backward(logits, expert_ids, d_weights, d_loss, counts, routed, d_
     written by moe_route; d_weights float32 [T][top_k] or None, d_loss float32
     [1] or None; d_logits [T][E] of the logits' type (rows may be strided)."""
     torch = _torch()
-    ld, ldd = _rows(logits, "logits"), _rows(d_logits, "d_logits")
-    T, E = logits.shape
+    ptr, T, E, ld = _rows(logits, "logits")
+    dptr, dT, dE, ldd = _rows(d_logits, "d_logits")
     typ = _TYPES.get(logits.dtype)
-    if typ is None or d_logits.dtype is not logits.dtype or d_logits.shape != logits.shape:
+    if typ is None or d_logits.dtype is not logits.dtype or dT != T or dE != E:
         _fail("logits and d_logits must be float32, bfloat16 or float16, alike in type and shape")
     top_k = expert_ids.shape[-1]
     ids = _out(expert_ids, (T, top_k), torch.int32, "expert_ids")
@@ -522,8 +520,8 @@ def moe_route_backward(logits, expert_ids, d_weights, d_loss, counts, routed, d_
     dl = None if d_loss is None else _out(d_loss, (1,), torch.float32, "d_loss")
     cnt = _out(counts, (E,), torch.int32, "counts")
     rtd = _out(routed, (1,), torch.int32, "routed")
-    st = load().moe_route_backward(logits.data_ptr(), typ, T, E, ld, ids, top_k, 1 if renormalise else 0,
-                                   loss_coef, dw, dl, cnt, rtd, d_logits.data_ptr(), ldd, _stream(stream))
+    st = load().moe_route_backward(ptr, typ, T, E, ld, ids, top_k, 1 if renormalise else 0,
+                                   loss_coef, dw, dl, cnt, rtd, dptr, ldd, _stream(stream))
     if st:
         _check(st, "moe_route_backward")
 
@@ -534,18 +532,17 @@ def fp8_quantize_transpose(x, fmt, qt, st, stream=None):
     128, and st uint8 [R/128][cols]: one power-of-two scale per column and 128
     rows, as its exponent + 127."""
     torch = _torch()
-    ldx = _rows(x, "x")
-    rows, cols = x.shape
-    nb = _nb(rows)
+    xp, rows, cols, ldx = _rows(x, "x")
+    nb = (rows + 127) // 128
     typ = _TYPES.get(x.dtype)
     if typ is None:
         _fail("x must be float32, bfloat16 or float16")
-    if qt.dtype is not torch.uint8 or qt.shape != (cols, nb * 128):
+    qp, qrows, qcols, ldq = _rows(qt, "qt")
+    if qt.dtype is not torch.uint8 or qrows != cols or qcols != nb * 128:
         _fail("qt must be uint8 [cols][rows rounded up to 128]")
-    ldq = _rows(qt, "qt")
     scales = _out(st, (nb, cols), torch.uint8, "st (ceil(rows/128), cols)")
-    status = load().fp8_quantize_transpose(x.data_ptr(), typ, rows, cols, ldx, _fmt(fmt), qt.data_ptr(), ldq,
-                                           scales, _stream(stream))
+    status = load().fp8_quantize_transpose(xp, typ, rows, cols, ldx, _fmt(fmt), qp, ldq, scales,
+                                           _stream(stream))
     if status:
         _check(status, "fp8_quantize_transpose")
 
@@ -556,28 +553,28 @@ def grouped_gemm_fp8_wgrad(a, fmt_a, sa, b, fmt_b, sb, d, group_offsets=None, st
     (T a multiple of 128); group_offsets int32 [G+1] (device) or None (G = 1,
     all tokens)."""
     torch = _torch()
-    lda, ldb = _rows(a, "a"), _rows(b, "b")
-    M, T = a.shape
-    N = b.shape[0]
+    ap, M, T, lda = _rows(a, "a")
+    bp, N, Tb, ldb = _rows(b, "b")
     fa, fb = _fmt(fmt_a), _fmt(fmt_b)
-    if b.shape[1] != T or T % 128:
+    if Tb != T or T % 128:
         _fail("a and b must have the same tokens, a multiple of 128")
-    if not (_codes_dtype_ok(a, fmt_a) and _codes_dtype_ok(b, fmt_b)):
+    u8 = torch.uint8
+    if not ((a.dtype is u8 or _codes_dtype_ok(a, fmt_a)) and (b.dtype is u8 or _codes_dtype_ok(b, fmt_b))):
         _fail("a and b must be codes of their formats (uint8 or the matching float8 dtype)")
-    pa = _out(sa, (T // 128, M), torch.uint8, "sa (T/128, M)")
-    pb = _out(sb, (T // 128, N), torch.uint8, "sb (T/128, N)")
-    if d.dim() != 3 or d.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+    pa = _out(sa, (T // 128, M), u8, "sa (T/128, M)")
+    pb = _out(sb, (T // 128, N), u8, "sb (T/128, N)")
+    dt = d.dtype
+    if d.dim() != 3 or (dt is not torch.bfloat16 and dt is not torch.int16 and dt is not torch.uint16):
         _fail("d must be bf16 [G][M][N]")
-    G = d.shape[0]
-    pd = _out(d, (G, M, N), d.dtype, "d ([G][M][N])")
+    G = len(d)
+    pd = _out(d, (G, M, N), dt, "d ([G][M][N])")
     if group_offsets is not None:
         po = _out(group_offsets, (G + 1,), torch.int32, "group_offsets")
     elif G == 1:
         po = None
     else:
         _fail("group_offsets may be None for one expert only")
-    st = load().grouped_gemm_fp8_wgrad(a.data_ptr(), fa, lda, pa, b.data_ptr(), fb, ldb, pb, pd, po, G, T, M, N,
-                                       _stream(stream))
+    st = load().grouped_gemm_fp8_wgrad(ap, fa, lda, pa, bp, fb, ldb, pb, pd, po, G, T, M, N, _stream(stream))
     if st:
         _check(st, "grouped_gemm_fp8_wgrad")
 
