@@ -82,9 +82,8 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 //
 // 16-bit values fit a key whole. Of a 32-bit value BITS low bits give way to
 // the expert's number: exact where they are zero in the whole row (values that
-// were 16-bit ones, for instance); otherwise two neighbours in the order
-// whose kept bits agree are not known to be in order, and the caller looks
-// for such a pair (one place past the k-th too) and falls back to `exact`.
+// were 16-bit ones, for instance); otherwise neighbours whose kept bits agree
+// are not known to be in order, and `choose` puts them in order.
 template <typename T, int LPR, int VPT>
 struct Picker {
   using L = Lay<T, LPR, VPT>;
@@ -161,9 +160,11 @@ __device__ __forceinline__ int exact_choice(const float (&x)[VPT], int l, int k)
   return id;
 }
 
-// Lane j gets the row's j-th choice (-1: none).
+// Lane j gets the row's j-th choice (-1: none) and its logit, of which `row` is
+// the first.
 template <typename T, int LPR, int VPT>
-__device__ __forceinline__ int choose(const float (&x)[VPT], int l, int k) {
+__device__ __forceinline__ int choose(const float (&x)[VPT], const T* __restrict__ row, int l, int k,
+                                      float& value) {
   using P = Picker<T, LPR, VPT>;
   P pick;
   pick.start(x, l);
@@ -176,11 +177,41 @@ __device__ __forceinline__ int choose(const float (&x)[VPT], int l, int k) {
     if (l == j) mine = key;
   }
   int id = P::expert(mine);
+  // (the row was just read: its value again is a cache hit)
+  value = id >= 0 ? to_f32(row[id]) : 0.0f;
   if constexpr (!P::WHOLE) {
-    if (__ballot(pick.dropped != 0u)) {                // (uniform over the wave)
+    if (__ballot(pick.dropped != 0u)) {                // (uniform over the wave, as all of these)
       const uint32_t key = pick.next();
-      close = close || (key && ((key ^ before) >> P::BITS) == 0u);
-      if (__ballot(close && pick.dropped != 0u)) id = exact_choice<LPR, VPT>(x, l, k);
+      const bool edge = key && ((key ^ before) >> P::BITS) == 0u;
+      if (__ballot(edge && pick.dropped != 0u)) {
+        // the k-th and the next one: which of them is larger, or a third
+        id = exact_choice<LPR, VPT>(x, l, k);
+        value = id >= 0 ? to_f32(row[id]) : 0.0f;
+      } else if (__ballot(close && pick.dropped != 0u)) {
+        // neighbours among the chosen: exchanged until whole values are in
+        // order (most often two of them, once)
+        uint32_t full = id >= 0 ? order_key(value) : 0u;
+        bool moved;
+        do {
+          moved = false;
+#pragma unroll
+          for (int odd = 0; odd < 2; ++odd) {
+            const int with = ((l + odd) ^ 1) - odd;
+            const bool first = with > l, pair = l < MAX_K && with >= 0 && with < MAX_K;
+            const uint32_t f = (uint32_t)__shfl((int)full, with & (LPR - 1), LPR);
+            const int i = __shfl(id, with & (LPR - 1), LPR);
+            const float v = __shfl(value, with & (LPR - 1), LPR);
+            // (0: no choice; two of those stay where they are)
+            const bool ahead = f > full || (f == full && i < id);    // the other one is
+            if (pair && (f | full) != 0u && ahead == first) {
+              full = f;
+              id = i;
+              value = v;
+              moved = true;
+            }
+          }
+        } while (__ballot(moved));
+      }
     }
   }
   return id;
@@ -271,7 +302,9 @@ __device__ __forceinline__ int slot_of(const RouteArgs& a, int e, int first, int
 // One block of 64 tokens per workgroup; LPR lanes per row. With 1024 threads
 // (16 lanes per row) all rows of a block are worked on at once: its time is
 // that of one row's chain of dependent steps, which four waves that walk the
-// block would go through four times (T 32768, E 256: 27 us).
+// block go through four times (T 4096, E 8: 6.4 -> 4.5 us; T 32768, E 256: 27
+// -> 26). Bound by the vector unit at many experts: about 850 instructions for
+// four rows of 256.
 template <typename T, int LPR, int VPT, int NT>
 __global__ void __launch_bounds__(NT)
 route_rows_kernel(RouteArgs a) {
@@ -305,9 +338,9 @@ route_rows_kernel(RouteArgs a) {
     const float inv = row_softmax<LPR, VPT>(x, top, ex);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) acc[v] += ex[v] * inv;
-    const int id = choose<T, LPR, VPT>(x, l, k);
-    // (the row was just read: its value again is a cache hit)
-    float w = id >= 0 ? exp_neg(to_f32(((const T*)a.logits)[t * a.ld + id]) - top) : 0.0f;
+    float xj;
+    const int id = choose<T, LPR, VPT>(x, (const T*)a.logits + (in ? t : 0) * a.ld, l, k, xj);
+    float w = id >= 0 ? exp_neg(xj - top) : 0.0f;
     const float s = a.renorm ? sum_lanes<LPR>(w) : 0.0f;
     // (a NaN row: inv is NaN, and so is every weight)
     w = inv != inv ? inv : (a.renorm ? (s > 0.0f ? w / s : 0.0f) : w * inv);
@@ -560,6 +593,10 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// workgroups per CU of the backward pass (T 30011, E 160: 8: 15.3 us, 6: 12.5, 4: 12.4,
+// 2: 13.1; with 8 every workgroup has one set of rows and nothing to load ahead)
+constexpr int BWD_PER_CU = 4;
+
 struct RouteBwdArgs {
   const void* logits;
   void* d_logits;
@@ -592,16 +629,28 @@ route_backward_kernel(RouteBwdArgs a) {
     const int e = L::at(v, l);
     f[v] = e < E ? fac * (float)a.counts[e] : 0.0f;
   }
-  for (int64_t t0 = (int64_t)blockIdx.x * AT_ONCE; t0 < a.T;
-       t0 += (int64_t)gridDim.x * AT_ONCE) {
+  // (a row's loads are issued while the one before it is worked on; what a row
+  // that takes no part holds does not matter)
+  const int64_t stride = (int64_t)gridDim.x * AT_ONCE;
+  int id_n;
+  float dw_n, x_n[VPT];
+  const auto fetch = [&](int64_t t) __attribute__((always_inline)) {
+    const bool in = t < a.T;
+    id_n = in && l < k ? a.ids[t * k + l] : -1;
+    dw_n = in && l < k && a.dw ? a.dw[t * k + l] : 0.0f;
+    load_row<T, LPR, VPT>((const T*)a.logits + (in ? t : 0) * a.ld, E, l, in, a.vec != 0, x_n);
+  };
+  fetch((int64_t)blockIdx.x * AT_ONCE + group);
+  for (int64_t t0 = (int64_t)blockIdx.x * AT_ONCE; t0 < a.T; t0 += stride) {
     const int64_t t = t0 + group;
     const bool in = t < a.T;
     const T* row = (const T*)a.logits + (in ? t : 0) * a.ld;
-    // (all loads at once; what a row that takes no part holds does not matter)
-    int id = in && l < k ? a.ids[t * k + l] : -1;
-    float dwj = in && l < k && a.dw ? a.dw[t * k + l] : 0.0f;
+    int id = id_n;
+    float dwj = dw_n;
     float x[VPT], ex[VPT], top;
-    load_row<T, LPR, VPT>(row, E, l, in, a.vec != 0, x);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) x[v] = x_n[v];
+    if (t0 + stride < a.T) fetch(t + stride);
     if (id >= E || id < 0) id = -1;
     const float xj = id >= 0 ? to_f32(row[id]) : 0.0f;
     const bool on = __shfl(id, 0, LPR) >= 0;
@@ -667,8 +716,12 @@ struct Pick {
 template <typename T, int NT>
 Pick pick_for(int E) {
   constexpr bool few = NT == THREADS;
-#define FP8G_PICK(LPR_, VPT_)                                                     \
-  Pick { route_rows_kernel<T, LPR_, VPT_, NT>, NT, route_backward_kernel<T, LPR_, VPT_>, \
+  // (from 12 values a lane on, two workgroups of 512 threads fit a CU's registers
+  // and one of 1024 alone: T 32768, E 256 33.7 -> 32.1 us; E 64 19.7 -> 20.3)
+  constexpr int WIDE = NT > 512 ? 512 : NT;
+#define FP8G_PICK(LPR_, VPT_)                                                             \
+  Pick { route_rows_kernel<T, LPR_, VPT_, LPR_ == 16 && VPT_ >= 12 ? WIDE : NT>,          \
+         LPR_ == 16 && VPT_ >= 12 ? WIDE : NT, route_backward_kernel<T, LPR_, VPT_>,      \
          THREADS / LPR_ }
   if (E <= 16) return FP8G_PICK(16, 1);
   if (E <= 32) return FP8G_PICK(16, 2);
@@ -769,7 +822,7 @@ hipError_t launch_route_backward(const RouteBwdCall& c, hipStream_t stream, int 
   a.coef = c.coef;
   const Pick p = pick(c.type, c.E, c.T);
   int64_t grid = (c.T + p.rows_at_once - 1) / p.rows_at_once;
-  if (grid > (int64_t)cu_count * 8) grid = (int64_t)cu_count * 8;
+  if (grid > (int64_t)cu_count * BWD_PER_CU) grid = (int64_t)cu_count * BWD_PER_CU;
   p.bwd<<<dim3((unsigned)grid), dim3(THREADS), 0, stream>>>(a);
   return hipGetLastError();
 }
