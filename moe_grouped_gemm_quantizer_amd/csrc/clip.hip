@@ -21,7 +21,9 @@ using namespace elem;
 
 constexpr int THREADS = 256;
 constexpr int MAX_T = 112;                             // tensors of a launch
-constexpr int64_t CHUNK = 32768;                       // elements of a chunk
+// Elements of a chunk: small ones where the list would otherwise leave CUs without
+// work, large ones where there is plenty (each chunk costs a search in the table).
+constexpr int64_t CHUNK_MIN = 8192, CHUNK_MAX = 32768;
 constexpr int64_t MAX_GRID = 2048;                     // eight workgroups per CU
 constexpr int64_t STREAM_BYTES = 192 << 20;            // lists from here on outgrow the caches
 
@@ -31,10 +33,17 @@ struct Table {
   int64_t numel[MAX_T];
   int end[MAX_T];                                      // chunks of this tensor and those before it
   uint8_t type[MAX_T];
-  int n;
+  int n, chunk;
 };
 
-int64_t chunks_of(int64_t numel) { return (numel + CHUNK - 1) / CHUNK; }
+int64_t chunks_of(int64_t numel, int64_t chunk) { return (numel + chunk - 1) / chunk; }
+
+// A list's chunk: the large one from twice a full grid of them on.
+int64_t chunk_for(const int64_t* numels, int n) {
+  int64_t total = 0;
+  for (int i = 0; i < n && total < 2 * MAX_GRID * CHUNK_MAX; ++i) total += numels[i];
+  return total < 2 * MAX_GRID * CHUNK_MAX ? CHUNK_MIN : CHUNK_MAX;
+}
 
 // The tensor of chunk c and the chunk's place in it.
 __device__ __forceinline__ int find(const Table& t, int c, int64_t& at) {
@@ -44,7 +53,7 @@ __device__ __forceinline__ int find(const Table& t, int c, int64_t& at) {
     if (c < t.end[mid]) hi = mid;
     else lo = mid + 1;
   }
-  at = (int64_t)(c - (lo ? t.end[lo - 1] : 0)) * CHUNK;
+  at = (int64_t)(c - (lo ? t.end[lo - 1] : 0)) * t.chunk;
   return lo;
 }
 
@@ -92,7 +101,7 @@ norm_partial_kernel(Table t, double* __restrict__ part) {
     int64_t at;
     const int i = find(t, c, at);
     const int64_t left = t.numel[i] - at;
-    const int n = (int)(left < CHUNK ? left : CHUNK);
+    const int n = (int)(left < t.chunk ? left : t.chunk);
     if (t.type[i] == TYPE_F32) s += chunk_sum((const float*)t.x[i] + at, n);
     else if (t.type[i] == TYPE_BF16) s += chunk_sum((const bf16_t*)t.x[i] + at, n);
     else s += chunk_sum((const f16_t*)t.x[i] + at, n);
@@ -105,6 +114,7 @@ __global__ void __launch_bounds__(THREADS)
 norm_finish_kernel(const double* __restrict__ part, int n, double* __restrict__ sumsq) {
   __shared__ double lds[THREADS / 64];
   double s = 0.0;
+#pragma unroll 8
   for (int i = threadIdx.x; i < n; i += THREADS) s += part[i];
   s = group_sum(s, lds);
   if (threadIdx.x == 0) *sumsq = s;
@@ -163,7 +173,7 @@ clip_kernel(Table t, const double* __restrict__ sumsq, float max_norm, float* __
     const int i = find(t, c, at);
     if (t.x[i] == t.y[i] && f == 1.0f) continue;
     const int64_t left = t.numel[i] - at;
-    const int n = (int)(left < CHUNK ? left : CHUNK);
+    const int n = (int)(left < t.chunk ? left : t.chunk);
     if (t.type[i] == TYPE_F32)
       chunk_scale<STREAM>((const float*)t.x[i] + at, (float*)t.y[i] + at, n, f);
     else if (t.type[i] == TYPE_BF16)
@@ -181,7 +191,7 @@ int64_t fill(Table& t, int& i, const void* const* xs, void* const* ys, const int
   int64_t chunks = 0;
   for (; i < n && t.n < MAX_T; ++i) {
     if (numels[i] == 0) continue;
-    const int64_t c = chunks_of(numels[i]);
+    const int64_t c = chunks_of(numels[i], t.chunk);
     if (chunks + c > 0x7FFFFFFF) break;                // (each tensor fits by itself: checked before)
     chunks += c;
     t.x[t.n] = xs[i];
@@ -199,11 +209,12 @@ int64_t fill(Table& t, int& i, const void* const* xs, void* const* ys, const int
 // One fp64 partial sum per workgroup of every launch: a launch has at most
 // MAX_GRID of them, and at most one per chunk.
 size_t grad_norm_workspace_bytes(const int64_t* numels, int n) {
+  const int64_t chunk = chunk_for(numels, n);
   int64_t parts = 0, chunks = 0;
   int tensors = 0;
   for (int i = 0; i < n; ++i) {
     if (numels[i] == 0) continue;
-    const int64_t c = chunks_of(numels[i]);
+    const int64_t c = chunks_of(numels[i], chunk);
     if (tensors == MAX_T || chunks + c > 0x7FFFFFFF) {
       parts += chunks < MAX_GRID ? chunks : MAX_GRID;
       chunks = 0;
@@ -219,6 +230,7 @@ size_t grad_norm_workspace_bytes(const int64_t* numels, int n) {
 hipError_t launch_grad_norm_sq(const void* const* grads, const int64_t* numels, const int* types,
                                int n, double* sumsq, void* workspace, hipStream_t stream) {
   Table t;
+  t.chunk = (int)chunk_for(numels, n);
   double* part = (double*)workspace;
   int parts = 0, i = 0;
   for (;;) {
@@ -235,6 +247,7 @@ hipError_t launch_grad_clip(const void* const* grads, void* const* outs, const i
                             const int* types, int n, const double* sumsq, float max_norm,
                             float* norm, hipStream_t stream) {
   Table t;
+  t.chunk = (int)chunk_for(numels, n);
   int64_t bytes = 0;
   for (int j = 0; j < n && bytes < STREAM_BYTES; ++j) bytes += numels[j] * (types[j] == TYPE_F32 ? 4 : 2);
   const auto kernel = bytes >= STREAM_BYTES ? clip_kernel<true> : clip_kernel<false>;
