@@ -6,6 +6,11 @@
 // vanishes below 1e-23, and the vector unit's fp64 rate (one fma per lane
 // and cycle as in fp32) is far above what HBM feeds it.
 //
+// Measured: 8 x 29.4M bf16 (470 MB read, then read and written): norm 77-81 us
+// (6 TB/s), clipping 141-148 us (6.4 TB/s); 300 tensors of 50M values, half of
+// them fp32: 43 + 68 us in three launches each, less than the host takes to
+// list them; 12 tensors of 40,000 values 4.3 + 1.6 + 4.9 us.
+//
 // The list travels in the kernel's arguments, up to 112 tensors a launch
 // (4 KB of arguments): nothing of it stays on the device or in the library.
 

@@ -27,7 +27,10 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 // bytes of columns and the 64 / CV consecutive tokens from rg 64 / CV on, so that
 // its codes of one column are consecutive bytes of the transposed row. The
 // codes cross the workgroup through LDS and leave as whole 128-byte rows.
-// HBM-bound: sizeof(T) bytes in and one out per element.
+// HBM-bound: sizeof(T) bytes in and one out per element. 4096x8192 bf16 23.2 us
+// (4.3 TB/s), 4864x4096 12.3 us (4.9), 4096x8192 fp32 35.8 us (4.7). With the values
+// widened to fp32 in registers, and each code compared and packed on its own, 30.3
+// us (bf16); 256 tokens x 64 columns per workgroup were slower than 128 x 128.
 
 constexpr int QTHREADS = 256;
 constexpr int QCOLS = 128;
@@ -325,7 +328,9 @@ __device__ __forceinline__ void token_blocks(const WgradArgs& a, int g, int& kb0
 // a step's time is what its copies take to arrive. One barrier a step: it
 // publishes the stage that has landed and frees the one read before. Position r
 // of fragment i of a wave's 64 rows is row 2 r + i, so that a lane's exponents
-// are two adjacent bytes and its results runs of 8 columns.
+// are two adjacent bytes and its results runs of 8 columns. Bound by latency: T
+// 128 4 us, T 1024 8 to 10 us, T 4096 21 us (0.6 us a step) up to one workgroup
+// per CU; through registers and one LDS stage it was 13.4 us at T 1024.
 constexpr int BT = 128;
 constexpr int RING = 4;
 constexpr int RSTAGE = 2 * BT * 128 + 2 * BT;
@@ -430,21 +435,36 @@ wgrad_ring_kernel(WgradArgs a, int mblocks, int nblocks) {
 // 256x256 tiles: four waves of 128x128, one per SIMD, the 256 accumulators
 // of a lane in the accumulation registers (nothing but the matrix unit
 // touches them until the end, since the scales go into the instruction). Per
-// 128 tokens a wave reads (128 + 128) x 128 bytes of LDS for 64 matrix
-// instructions of 32 cycles: 64 bytes a cycle and CU, with the 32 of the
+// 128 tokens a wave reads (128 + 128) x 128 bytes of LDS for 32 matrix
+// instructions of 64 cycles: 64 bytes a cycle and CU, with the 32 of the
 // copies into LDS three quarters of what the LDS moves; eight waves of
 // 64x128 would need all of it.
 //
 // A workgroup walks tiles (expert, row block, column block); the 128-token
-// steps of all its tiles form one sequence with two LDS stages. A step, by
-// its eight slices of eight matrix instructions (one 16-row fragment of b
-// against all eight of a):
-//   slices 0-2  read the rest of the step's b fragments
-//   slice 4     wait for the next step's copies, barrier (everyone is done
-//               with this stage), then issue the copies of the step after next
-//               into it, and up to slice 7 read the next step's a fragments
-//               and first b fragments
-// so that every read has about a slice, and every copy a step, to arrive.
+// steps of all its tiles form one sequence with two LDS stages. A step's 32
+// matrix instructions:
+//   0-15   fragments 0 and 1 of b against all of a. After the first four
+//          everyone meets: a's part of this stage and b's first half have been read
+//          by all (a step ahead), so that the copies of the step after next may
+//          go there, and b's second half has landed and is read.
+//   16-31  everyone meets again: this stage is read altogether, and the next
+//          one's a and b first half have landed. Each fragment of a against 2
+//          and 3 of b, after which the next step's fragment takes its place.
+// At most one copy and two LDS reads stand between two matrix instructions: a
+// copy holds its wave for about 58 cycles (the four waves of a CU share the
+// path), which the 64 of a 32x32x64 instruction cover and the 32 of a
+// 16x16x128 do not; copies in bursts leave the matrix unit waiting.
+//
+// Measured (T 4096, 8192x8192: 550 GFLOP; T 4096, 8 experts, 4096x7168: 470 MB of
+// results): first version, one barrier and three bursts of copies a step 215 and 209
+// us; two meets, spread copies 205 and 205; 32x32x64, whole-line stores 197 (2.8
+// PFLOP/s; the library's 8-bit product of 8192^3 reaches 3.06 here) and 166.
+// Without copies 168 and 149, without stores 175 and 97, with neither 147 and
+// 85: the large layer is bound by the copies' issue, the experts by writing 128
+// KB per tile after 2 to 15 steps, during which the matrix unit is idle (5 us a
+// tile: half conversion, half stores). Prefetching into L2, operands laid out in tiles,
+// fewer or more rows per XCD group and shifting the experts' order per XCD or
+// CU changed nothing.
 //
 // Which global row lies in which LDS row is free, as each lane of a copy has
 // its own address. The rows of a 128-row band are dealt so that
@@ -632,10 +652,11 @@ wgrad_tile_kernel(WgradArgs a, int mblocks, int nblocks, int xcd_remap) {
   sa = *reinterpret_cast<const uint32_t*>(lds + ea);
   sb = *reinterpret_cast<const uint32_t*>(lds + eb);
 
-  // Two points of a step where everyone waits for copies and meets: after
-  // slice 0 for b's late fragments of this step, half way for the early part of
-  // the next. N copies have been issued since those; for three points after
-  // a full tile its stores are newer too.
+  // Two points of a step where everyone waits for copies and meets: for b's
+  // late fragments of this step, and half way for the early part of the next.
+  // N copies have been issued since those; for three points after a full tile
+  // its stores are newer too. (Waits may be longer than needed, never shorter:
+  // where a ragged tile stores less, its stores are waited for.)
   int fresh = 0;
   auto meet = [&](auto n) __attribute__((always_inline)) {
     constexpr int N = decltype(n)::value;
