@@ -9,7 +9,7 @@
 // Measured: 8 x 29.4M bf16 (470 MB read, then read and written): norm 77-81 us
 // (6 TB/s), clipping 141-148 us (6.4 TB/s); 300 tensors of 50M values, half of
 // them fp32: 43 + 68 us in three launches each, less than the host takes to
-// list them; 12 tensors of 40,000 values 4.3 + 1.6 + 4.9 us.
+// list them; 12 tensors of 40,000 values 5.1 + 4.5 us.
 //
 // The list travels in the kernel's arguments, up to 112 tensors a launch
 // (4 KB of arguments): nothing of it stays on the device or in the library.
@@ -29,6 +29,10 @@ constexpr int MAX_T = 112;                             // tensors of a launch
 // Elements of a chunk: small ones where the list would otherwise leave CUs without
 // work, large ones where there is plenty (each chunk costs a search in the table).
 constexpr int64_t CHUNK_MIN = 8192, CHUNK_MAX = 32768;
+// A list of up to TINY values is summed by one workgroup, a chunk of CHUNK_TINY
+// per wave at a time: one launch instead of two, which is what such a call
+// costs (12 tensors, 40,000 values).
+constexpr int64_t TINY = 131072, CHUNK_TINY = 2048;
 constexpr int64_t MAX_GRID = 2048;                     // eight workgroups per CU
 constexpr int64_t STREAM_BYTES = 192 << 20;            // lists from here on outgrow the caches
 
@@ -47,6 +51,7 @@ int64_t chunks_of(int64_t numel, int64_t chunk) { return (numel + chunk - 1) / c
 int64_t chunk_for(const int64_t* numels, int n) {
   int64_t total = 0;
   for (int i = 0; i < n && total < 2 * MAX_GRID * CHUNK_MAX; ++i) total += numels[i];
+  if (total <= TINY && n <= MAX_T) return CHUNK_TINY;
   return total < 2 * MAX_GRID * CHUNK_MAX ? CHUNK_MIN : CHUNK_MAX;
 }
 
@@ -62,8 +67,9 @@ __device__ __forceinline__ int find(const Table& t, int c, int64_t& at) {
   return lo;
 }
 
-template <typename T>
-__device__ __forceinline__ double chunk_sum(const T* __restrict__ x, int n) {
+// (by NT threads, of which this is number t)
+template <int NT, typename T>
+__device__ __forceinline__ double chunk_sum(const T* __restrict__ x, int n, int t) {
   constexpr int W = 16 / (int)sizeof(T);
   double s = 0.0;
   int done = 0;
@@ -71,7 +77,7 @@ __device__ __forceinline__ double chunk_sum(const T* __restrict__ x, int n) {
     const int packs = n / W;
     done = packs * W;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < packs; i += THREADS) {
+    for (int i = t; i < packs; i += NT) {
       const Pack<T, W> p = reinterpret_cast<const Pack<T, W>*>(x)[i];
 #pragma unroll
       for (int w = 0; w < W; ++w) {
@@ -80,20 +86,35 @@ __device__ __forceinline__ double chunk_sum(const T* __restrict__ x, int n) {
       }
     }
   }
-  for (int i = done + threadIdx.x; i < n; i += THREADS) {
+  for (int i = done + t; i < n; i += NT) {
     const double v = (double)to_f32(x[i]);
     s = __builtin_fma(v, v, s);
   }
   return s;
 }
 
+template <int NT>
+__device__ __forceinline__ double table_chunk_sum(const Table& table, int c, int t) {
+  int64_t at;
+  const int i = find(table, c, at);
+  const int64_t left = table.numel[i] - at;
+  const int n = (int)(left < table.chunk ? left : table.chunk);
+  if (table.type[i] == TYPE_F32) return chunk_sum<NT>((const float*)table.x[i] + at, n, t);
+  if (table.type[i] == TYPE_BF16) return chunk_sum<NT>((const bf16_t*)table.x[i] + at, n, t);
+  return chunk_sum<NT>((const f16_t*)table.x[i] + at, n, t);
+}
+
 // Sum over the workgroup, in lane and wave order.
+template <int NT>
 __device__ __forceinline__ double group_sum(double s, double* lds) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o);
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
   __syncthreads();
-  return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+  s = 0.0;
+#pragma unroll
+  for (int w = 0; w < NT / 64; w += 4) s += (lds[w] + lds[w + 1]) + (lds[w + 2] + lds[w + 3]);
+  return s;
 }
 
 // Chunks blockIdx.x, + gridDim.x, ...: one partial sum per workgroup.
@@ -102,17 +123,21 @@ norm_partial_kernel(Table t, double* __restrict__ part) {
   __shared__ double lds[THREADS / 64];
   double s = 0.0;
   const int chunks = t.end[t.n - 1];
-  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-    int64_t at;
-    const int i = find(t, c, at);
-    const int64_t left = t.numel[i] - at;
-    const int n = (int)(left < t.chunk ? left : t.chunk);
-    if (t.type[i] == TYPE_F32) s += chunk_sum((const float*)t.x[i] + at, n);
-    else if (t.type[i] == TYPE_BF16) s += chunk_sum((const bf16_t*)t.x[i] + at, n);
-    else s += chunk_sum((const f16_t*)t.x[i] + at, n);
-  }
-  s = group_sum(s, lds);
+  for (int c = blockIdx.x; c < chunks; c += gridDim.x) s += table_chunk_sum<THREADS>(t, c, threadIdx.x);
+  s = group_sum<THREADS>(s, lds);
   if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+constexpr int TINY_THREADS = 1024;
+__global__ void __launch_bounds__(TINY_THREADS)
+norm_tiny_kernel(Table t, double* __restrict__ sumsq) {
+  __shared__ double lds[TINY_THREADS / 64];
+  double s = 0.0;
+  const int chunks = t.end[t.n - 1];
+  for (int c = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); c < chunks; c += TINY_THREADS / 64)
+    s += table_chunk_sum<64>(t, c, threadIdx.x & 63);
+  s = group_sum<TINY_THREADS>(s, lds);
+  if (threadIdx.x == 0) *sumsq = s;
 }
 
 __global__ void __launch_bounds__(THREADS)
@@ -121,7 +146,7 @@ norm_finish_kernel(const double* __restrict__ part, int n, double* __restrict__ 
   double s = 0.0;
 #pragma unroll 8
   for (int i = threadIdx.x; i < n; i += THREADS) s += part[i];
-  s = group_sum(s, lds);
+  s = group_sum<THREADS>(s, lds);
   if (threadIdx.x == 0) *sumsq = s;
 }
 
@@ -241,6 +266,10 @@ hipError_t launch_grad_norm_sq(const void* const* grads, const int64_t* numels, 
   for (;;) {
     const int64_t grid = fill(t, i, grads, nullptr, numels, types, n);
     if (grid == 0) break;
+    if (t.chunk == CHUNK_TINY) {                       // (such a list fits one table)
+      norm_tiny_kernel<<<dim3(1), dim3(TINY_THREADS), 0, stream>>>(t, sumsq);
+      return hipGetLastError();
+    }
     norm_partial_kernel<<<dim3((unsigned)grid), dim3(THREADS), 0, stream>>>(t, part + parts);
     parts += (int)grid;
   }
@@ -270,6 +299,7 @@ hipError_t launch_grad_clip(const void* const* grads, void* const* outs, const i
 
 void clip_kernels(std::vector<const void*>& out) {
   out.push_back((const void*)norm_partial_kernel);
+  out.push_back((const void*)norm_tiny_kernel);
   out.push_back((const void*)norm_finish_kernel);
   out.push_back((const void*)clip_kernel<false>);
   out.push_back((const void*)clip_kernel<true>);
