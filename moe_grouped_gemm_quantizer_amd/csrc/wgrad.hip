@@ -457,12 +457,13 @@ wgrad_ring_kernel(WgradArgs a, int mblocks, int nblocks) {
 //
 // Measured (T 4096, 8192x8192: 550 GFLOP; T 4096, 8 experts, 4096x7168: 470 MB of
 // results): first version, one barrier and three bursts of copies a step 215 and 209
-// us; two meets, spread copies 205 and 205; 32x32x64, whole-line stores 197 (2.8
-// PFLOP/s; the library's 8-bit product of 8192^3 reaches 3.06 here) and 166.
-// Without copies 168 and 149, without stores 175 and 97, with neither 147 and
-// 85: the large layer is bound by the copies' issue, the experts by writing 128
-// KB per tile after 2 to 15 steps, during which the matrix unit is idle (5 us a
-// tile: half conversion, half stores). Prefetching into L2, operands laid out in tiles,
+// us; two meets, spread copies 205 and 205; 32x32x64, whole-line stores 197 and 166;
+// a tile's first step from a zero operand 192 (2.9 PFLOP/s; the library's 8-bit
+// product of 8192^3 reaches 3.06 here) and 158.
+// Before that last step, without copies 168 and 149, without stores 175 and 97,
+// with neither 147 and 85: the large layer is bound by the copies' issue, the
+// experts by writing 128 KB per tile after 2 to 15 steps, during which the matrix
+// unit is idle and the next copies queue behind the stores. Prefetching into L2, operands laid out in tiles,
 // fewer or more rows per XCD group and shifting the experts' order per XCD or
 // CU changed nothing.
 //
@@ -672,11 +673,11 @@ wgrad_tile_kernel(WgradArgs a, int mblocks, int nblocks, int xcd_remap) {
   for (int slot = first; slot < tiles; slot += grid) {
     Tile tc;
     tile_of(a, ex, slot, mblocks, nblocks, tc);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = v16f{};
-    for (int k = 0; k < tc.steps; ++k, ++s) {
+    // A tile's first step starts its sums from a zero operand: as one loop, the 256
+    // registers are cleared by as many writes before it (dense 196 against 192 us,
+    // experts 166 against 158).
+    auto step = [&](auto first_step) __attribute__((always_inline)) {
+      constexpr bool FIRST = decltype(first_step)::value;
       const uint8_t* __restrict__ cur = lds + (s & 1) * STAGE;
       const uint8_t* __restrict__ nxt = lds + ((s & 1) ^ 1) * STAGE;
       const uint32_t stage = base + (s & 1) * STAGE;
@@ -684,7 +685,8 @@ wgrad_tile_kernel(WgradArgs a, int mblocks, int nblocks, int xcd_remap) {
       // fit their 64 cycles: a run of them would leave the matrix unit waiting)
 #define FP8G_MFMA(I_, J_, H_)                                                          \
   do {                                                                                 \
-    acc[I_][J_] = mfma<FA, FB>(bf[J_][H_], af[I_][H_], acc[I_][J_], J_, sb, I_, sa);   \
+    const v16f c_ = FIRST && H_ == 0 ? v16f{} : acc[I_][J_];                           \
+    acc[I_][J_] = mfma<FA, FB>(bf[J_][H_], af[I_][H_], c_, J_, sb, I_, sa);            \
     /* (a pure instruction: without this it is moved to where it is used) */           \
     asm volatile("" : "+a"(acc[I_][J_]));                                              \
   } while (0)
@@ -716,7 +718,20 @@ wgrad_tile_kernel(WgradArgs a, int mblocks, int nblocks, int xcd_remap) {
       advance();
       sa = sa_n;
       sb = sb_n;
-    }
+      ++s;
+    };
+    // (the sums stay where the matrix unit keeps them from here to the stores)
+    auto pin = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm volatile("" : "+a"(acc[i][j]));
+    };
+    step(std::true_type{});
+    pin();
+#pragma nounroll
+    for (int k = 1; k < tc.steps; ++k) step(std::false_type{});
+    pin();
     const bool full = tc.mv == TS && tc.nv == TS;
     fresh = full ? 3 : 0;
     // A lane holds, of a's position pos, 16 positions of each fragment j of b:
