@@ -323,14 +323,19 @@ __device__ __forceinline__ void token_blocks(const WgradArgs& a, int g, int& kb0
   kb1 = hi < 0 ? 0 : min(hi / 128, last);
 }
 
-// 128x128 tiles, four waves of 64x64, four LDS stages: the copies of three
-// steps are on their way while one is multiplied, since with few workgroups
-// a step's time is what its copies take to arrive. One barrier a step: it
-// publishes the stage that has landed and frees the one read before. Position r
-// of fragment i of a wave's 64 rows is row 2 r + i, so that a lane's exponents
-// are two adjacent bytes and its results runs of 8 columns. Bound by latency: T
-// 128 4 us, T 1024 8 to 10 us, T 4096 21 us (0.6 us a step) up to one workgroup
-// per CU; through registers and one LDS stage it was 13.4 us at T 1024.
+// 128x128 tiles, four waves of 64x64, four LDS stages: a step's fragments are read
+// during the one before, and its copies issued three and a half steps ahead, since
+// with few workgroups a step's time is what its copies take to arrive. One barrier
+// a step, half way: it publishes the stage that has landed and frees the one whose
+// fragments are all in registers. One copy stands behind a matrix instruction, as in
+// the large kernel. Position r of fragment i of a wave's 64 rows is row 2 r + i, so
+// that a lane's exponents are two adjacent bytes and its results runs of 8 columns.
+// Bound by latency: T 128 4.3 us, T 1024 7.6 to 8.5 us, T 4096 18 to 19 us (0.4 us a
+// step, of which the copies' issue and the matrix instructions are 0.25 each) up to
+// one workgroup per CU. With a step's copies, reads and products one after the other
+// 4.3, 8.7 to 9.7 and 22 to 23 us; through registers and one LDS stage 13.4 us at T
+// 1024. Runs of tiles per XCD are faster for some shapes and slower for others
+// (T 4096, 1040x2064: 17.2 against 18.1 us, 2048x2048: 20.5 against 18.8).
 constexpr int BT = 128;
 constexpr int RING = 4;
 constexpr int RSTAGE = 2 * BT * 128 + 2 * BT;
@@ -365,16 +370,24 @@ wgrad_ring_kernel(WgradArgs a, int mblocks, int nblocks) {
     voff[c] = (uint32_t)min(row, last) * ld + (uint32_t)((lane & 7) ^ (lane >> 3) ^ (c & 1)) * 16u;
   }
   const uint32_t base = lds_addr(lds);
-  auto issue_stage = [&](int s) __attribute__((always_inline)) {
-    // (past the end the last step again, for nothing: every wait counts alike)
+  // copy c of a step (past the end the last step's again, for nothing: every wait
+  // counts alike)
+  auto copy = [&](int s, int c) __attribute__((always_inline)) {
     const int64_t kb = kb0 + min(s, steps - 1);
     const uint32_t st = base + (uint32_t)(s % RING) * RSTAGE;
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-      copy16(src + kb * 128, voff[c], st + (uint32_t)((wave >> 1) * BT + band + c * 8) * 128u);
-    if (lane < 32) copy4(esrc + kb * estep, eoff, st + 2 * BT * 128 + (wave & 1) * BT);
+    if (c < 8) copy16(src + kb * 128, voff[c], st + (uint32_t)((wave >> 1) * BT + band + c * 8) * 128u);
+    else if (lane < 32) copy4(esrc + kb * estep, eoff, st + 2 * BT * 128 + (wave & 1) * BT);
   };
   const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+  const int ea = 2 * BT * 128 + wm + (lane & 31) * 2, eb = 2 * BT * 128 + BT + wn + (lane & 31) * 2;
+  // own reads and copies of long enough ago have arrived; then everyone's have
+  auto meet = [&](auto n) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    __builtin_amdgcn_s_waitcnt(vmcnt_only(decltype(n)::value));
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
   v16f acc[2][2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -382,34 +395,50 @@ wgrad_ring_kernel(WgradArgs a, int mblocks, int nblocks) {
     for (int j = 0; j < 2; ++j) acc[i][j] = v16f{};
   if (steps > 0) {
 #pragma unroll
-    for (int s = 0; s < RING - 1; ++s) issue_stage(s);
-    for (int s = 0; s < steps; ++s) {
-      // (own reads of the stage before have fed matrix instructions)
-      __builtin_amdgcn_s_waitcnt(vmcnt_only((RING - 2) * RCOPIES));
-      __builtin_amdgcn_sched_barrier(0);
-      asm volatile("s_barrier" ::: "memory");
-      __builtin_amdgcn_sched_barrier(0);
-      issue_stage(s + RING - 1);
-      const uint8_t* const st = lds + (s % RING) * RSTAGE;
-      const uint32_t sa = *reinterpret_cast<const uint16_t*>(st + 2 * BT * 128 + wm + (lane & 31) * 2);
-      const uint32_t sb =
-          *reinterpret_cast<const uint16_t*>(st + 2 * BT * 128 + BT + wn + (lane & 31) * 2);
+    for (int c = 0; c < 3 * RCOPIES + 5; ++c) copy(c / RCOPIES, c % RCOPIES);
+    meet(std::integral_constant<int, 2 * RCOPIES + 5>{});
+    v8i fa[2][2], fb[2][2];                            // [fragment][half of the 128 tokens]
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        v8i fa[2], fb[2];
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          fa[i] = read_frag(st + wm * 128, i, h, lane);
-          fb[i] = read_frag(st + BT * 128 + wn * 128, i, h, lane);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            acc[i][j] = mfma<FA, FB>(fb[j], fa[i], acc[i][j], j, sb, i, sa);
+      for (int i = 0; i < 2; ++i) {
+        fa[i][h] = read_frag(lds + wm * 128, i, h, lane);
+        fb[i][h] = read_frag(lds + BT * 128 + wn * 128, i, h, lane);
       }
-      // (every LDS read of this stage has arrived before the next barrier)
-      __builtin_amdgcn_s_waitcnt(0xC07F);
+    uint32_t sa = *reinterpret_cast<const uint16_t*>(lds + ea);
+    uint32_t sb = *reinterpret_cast<const uint16_t*>(lds + eb);
+    for (int s = 0; s < steps; ++s) {
+      // (the empty asm keeps a pure instruction from moving to where it is used)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int i = m >> 1, j = m & 1;
+        acc[i][j] = mfma<FA, FB>(fb[j][0], fa[i][0], acc[i][j], j, sb, i, sa);
+        asm volatile("" : "+a"(acc[i][j]));
+        copy(s + 3, 5 + m);
+      }
+      // this stage has been read by all, and the next one's copies have landed: those
+      // of two steps may be on their way
+      meet(std::integral_constant<int, 2 * RCOPIES>{});
+      const uint8_t* const st = lds + ((s + 1) % RING) * RSTAGE;
+      const uint32_t sa_n = *reinterpret_cast<const uint16_t*>(st + ea);
+      const uint32_t sb_n = *reinterpret_cast<const uint16_t*>(st + eb);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int i = m >> 1, j = m & 1;
+        if (i == 0) fa[j][0] = read_frag(st + wm * 128, j, 0, lane);
+        else fb[j][0] = read_frag(st + BT * 128 + wn * 128, j, 0, lane);
+        acc[i][j] = mfma<FA, FB>(fb[j][1], fa[i][1], acc[i][j], j, sb, i, sa);
+        asm volatile("" : "+a"(acc[i][j]));
+        copy(s + 4, m);
+        if (m == 3) copy(s + 4, 4);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        fa[i][1] = read_frag(st + wm * 128, i, 1, lane);
+        fb[i][1] = read_frag(st + BT * 128 + wn * 128, i, 1, lane);
+      }
+      sa = sa_n;
+      sb = sb_n;
     }
     // (no copy may arrive after the workgroup's LDS is someone else's)
     __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
@@ -829,11 +858,12 @@ hipError_t launch_quantize_transpose(const void* x, int type, int64_t rows, int6
 hipError_t launch_wgrad(const WgradArgs& args, int fmt_a, int fmt_b, const DeviceInfo& dev,
                         hipStream_t stream) {
   const int64_t mb = (args.M + TS - 1) / TS, nb = (args.N + TS - 1) / TS, all = mb * nb * args.G;
-  // 256x256 tiles from half the CUs on: below that, at most two rounds of 128x128
-  // tiles, whose copies are further ahead (dense, T 4096: 64 tiles 24.7
-  // against 41.3 us, 112 tiles 43.4 / 41.5, 140 tiles 62.5 / 41.6, 256 tiles 81.7
-  // / 49.4; T 1024: 45 tiles 8.5 / 17.1, 112 tiles 16.8 / 17.2, 140 tiles 23.7 / 16.9)
-  if (all >= dev.cu_count / 2 && args.T > 0) {
+  // 256x256 tiles when they are more than half the CUs; up to there, at most two
+  // rounds of 128x128 tiles, whose copies are further ahead (dense, 128 against 256,
+  // T 4096: 64 tiles of 256x256 18.8 / 38.7 us, 128 tiles 36.0 / 40.5, 140 tiles
+  // 49.3 / 41.6, 256 tiles 67.2 / 48.7; T 1024: 64 tiles 8.8 / 16.2, 128 tiles 15.0 /
+  // 16.3, 140 tiles 20.5 / 16.4)
+  if (all > dev.cu_count / 2 && args.T > 0) {
     const int64_t grid = all < dev.cu_count ? all : dev.cu_count;
     tile_pick(fmt_a, fmt_b)<<<dim3((unsigned)grid), dim3(256), 0, stream>>>(
         args, (int)mb, (int)nb, grid % 8 == 0 ? 1 : 0);
