@@ -581,7 +581,8 @@ def grouped_gemm_fp8_wgrad(a, fmt_a, sa, b, fmt_b, sb, d, group_offsets=None, st
 
 def _grad_list(ts, what):
     """HOST arrays of the tensors' pointers, sizes and types. (Hundreds of
-    tensors: every attribute is read in a loop of the interpreter's own.)"""
+    tensors: every attribute is read in a loop of the interpreter's own.) ts:
+    a tuple or list, since it is gone through several times."""
     torch = _torch()
     cls = torch.Tensor
     types = list(map(_TYPES.get, map(operator.attrgetter("dtype"), ts)))
@@ -601,17 +602,17 @@ def grad_norm_sq_workspace_size(grads):
     """Bytes of workspace grad_norm_sq needs for this list of tensors."""
     out = ctypes.c_size_t(0)
     numels = array.array("q", [t.numel() for t in grads])
-    _check(load().grad_norm_sq_workspace_size(_at(numels), len(grads), ctypes.byref(out)),
+    _check(load().grad_norm_sq_workspace_size(_at(numels), len(numels), ctypes.byref(out)),
            "grad_norm_sq_workspace_size")
     return int(out.value)
 
 
 def grad_norm_sq(grads, sumsq, workspace, stream=None):
-    """Sum of squares over a list of contiguous tensors (float32, bfloat16,
-    float16, mixed) into sumsq, a float64 device tensor of one element.
-    workspace: at least grad_norm_sq_workspace_size(grads) bytes."""
+    """Sum of squares over a list (or any iterable) of contiguous tensors
+    (float32, bfloat16, float16, mixed) into sumsq, a float64 device tensor of
+    one element. workspace: at least grad_norm_sq_workspace_size(grads) bytes."""
     torch = _torch()
-    ptrs, numels, types = _grad_list(grads, "grads")
+    ptrs, numels, types = _grad_list(tuple(grads), "grads")
     out = _out(sumsq, (1,), torch.float64, "sumsq")
     wp, wb = _room(workspace)
     _check(load().grad_norm_sq(_at(ptrs), _at(numels), _at(types), len(ptrs), out, wp, wb, _stream(stream)),
@@ -620,13 +621,15 @@ def grad_norm_sq(grads, sumsq, workspace, stream=None):
 
 def grad_clip(grads, outs, sumsq, max_norm, norm, stream=None):
     """outs[i] = grads[i] * min(1, max_norm / (norm + 1e-6)), norm = sqrt(sumsq)
-    (float32 device tensor of one element, written). outs[i] may be grads[i]."""
+    (float32 device tensor of one element, written). grads and outs: lists or
+    any iterables; outs[i] may be grads[i]."""
     torch = _torch()
-    ptrs, numels, types = _grad_list(grads, "grads")
-    if outs is grads:
+    same = outs is grads                              # (also one iterator given twice)
+    ptrs, numels, types = _grad_list(tuple(grads), "grads")
+    if same:
         optrs = ptrs
     else:
-        optrs, onumels, otypes = _grad_list(outs, "outs")
+        optrs, onumels, otypes = _grad_list(tuple(outs), "outs")
         if onumels != numels or otypes != types:
             _fail("outs must match grads in number, size and type")
     total = _out(sumsq, (1,), torch.float64, "sumsq")
