@@ -291,6 +291,7 @@ struct RouteArgs {
   const uint8_t* mask;
   int64_t T, ld, max_m;
   int E, k, renorm, align, vec;
+  int block0, only;                 // this launch's first block; whether it is the only one of all
   float coef;
   int32_t *ids, *counts, *routed, *offsets, *slots;
   float *weights, *prob_sum, *loss;
@@ -328,7 +329,8 @@ route_rows_kernel(RouteArgs a) {
   if (threadIdx.x == 0) n_routed = 0;
   __syncthreads();
   const int l = threadIdx.x & (LPR - 1), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t0 = (int64_t)blockIdx.x * ROWS;
+  const int64_t block = (int64_t)a.block0 + blockIdx.x;
+  const int64_t t0 = block * ROWS;
   float acc[VPT];
 #pragma unroll
   for (int v = 0; v < VPT; ++v) acc[v] = 0.0f;
@@ -372,7 +374,7 @@ route_rows_kernel(RouteArgs a) {
     if (lane < LPR) psum[wave][L::at(v, l)] = acc[v];
   }
   __syncthreads();
-  const bool only = gridDim.x == 1;
+  const bool only = a.only != 0;
   for (int e = threadIdx.x; e < E; e += NT) {
     const int c = __popc(took[0][e]) + __popc(took[1][e]);
     float p = 0.0f;
@@ -385,13 +387,13 @@ route_rows_kernel(RouteArgs a) {
       psum[0][e] = p;
       count[e] = c;
     } else {
-      a.part_count[(int64_t)blockIdx.x * (E + 1) + e] = c;
-      a.part_prob[(int64_t)blockIdx.x * E + e] = p;
+      a.part_count[block * (E + 1) + e] = c;
+      a.part_prob[block * E + e] = p;
     }
   }
   if (threadIdx.x == 0) {
     if (only) a.routed[0] = n_routed;
-    else a.part_count[(int64_t)blockIdx.x * (E + 1) + E] = n_routed;
+    else a.part_count[block * (E + 1) + E] = n_routed;
   }
   if (only) {
     __syncthreads();
@@ -749,6 +751,9 @@ Pick pick(int type, int E, int64_t T) {
                              : pick_of<f16_t>(E, T);
 }
 
+// Workgroups of a launch: its threads are counted in 32 bits.
+int64_t rows_blocks_max(int threads) { return 0xFFFFFFFFll / threads; }
+
 bool vec_ok(const void* p, int64_t ld, int type) {
   const int64_t size = type == TYPE_F32 ? 4 : 2;
   return (uintptr_t)p % 16 == 0 && ld * size % 16 == 0;
@@ -795,13 +800,26 @@ hipError_t launch_route(const RouteCall& c, hipStream_t stream) {
     return hipGetLastError();
   }
   const Pick p = pick(c.type, c.E, c.T);
-  p.rows<<<dim3((unsigned)nblk), dim3((unsigned)p.rows_threads), 0, stream>>>(a);
+  // A launch holds fewer than 2^32 threads (from 2^28 tokens on the rows take several).
+  // The kernels after it read what it wrote, places in tables among it: none is launched
+  // behind one that was not.
+  const int64_t most = rows_blocks_max(p.rows_threads);
+  a.only = nblk == 1;
+  for (int64_t b = 0; b < nblk; b += most) {
+    a.block0 = (int)b;
+    const int64_t grid = nblk - b < most ? nblk - b : most;
+    p.rows<<<dim3((unsigned)grid), dim3((unsigned)p.rows_threads), 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   if (nblk > 1 && c.E < THREADS && nblk * (c.E + 1) <= JOIN_MAX) {
     int ep = 1;
     while (ep <= c.E) ep *= 2;
     route_join_kernel<<<dim3((unsigned)nblk), dim3(THREADS), 0, stream>>>(a, (int)nblk, ep);
   } else if (nblk > 1) {
     route_scan_kernel<<<dim3((unsigned)(c.E / COLS + 1)), dim3(COLS * RUNS), 0, stream>>>(a, (int)nblk);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     const int64_t grid = (c.T * c.k + PAIRS - 1) / PAIRS;
     route_slots_kernel<<<dim3((unsigned)grid), dim3(THREADS), 0, stream>>>(a);
   }
