@@ -532,8 +532,8 @@ fp8g_status moe_route_backward(const void* logits, int type, int64_t T, int E, i
  *       are written as zeros, so that qt is an operand of R tokens.
  * st    uint8 [R / 128][cols], 4-byte aligned.
  * Errors (nothing is launched): FP8G_ERR_SHAPE, _NULL_PTR, _STRIDE, _ALIGN
- * as stated; _UNSUPPORTED for an unknown type or format, or more than
- * 65535 * 128 rows. rows == 0 is a no-op.
+ * as stated; _UNSUPPORTED for an unknown type or format, for more than
+ * 65535 * 128 rows or (2^24 - 1) * 128 columns. rows == 0 is a no-op.
  */
 fp8g_status fp8_quantize_transpose(const void* x, int type, int64_t rows, int64_t cols,
                                    int64_t ldx, int fmt, uint8_t* qt, int64_t ldq, uint8_t* st,

@@ -142,7 +142,8 @@ fp8g_status fp8_quantize_transpose(const void* x, int type, int64_t rows, int64_
   if (rows == 0) return FP8G_OK;
   if (!x || !qt || !st) return FP8G_ERR_NULL_PTR;
   const int64_t nblk = (rows - 1) / 128 + 1;
-  if (nblk > 65535 || (cols - 1) / 128 >= kInt31) return FP8G_ERR_UNSUPPORTED;
+  // (256 threads for 128 columns, and fewer than 2^32 of them in a launch)
+  if (nblk > 65535 || (cols - 1) / 128 + 1 >= (int64_t(1) << 24)) return FP8G_ERR_UNSUPPORTED;
   if (ldx < cols || ldq < nblk * 128) return FP8G_ERR_STRIDE;
   if (!aligned(x, type_size(type)) || !aligned(qt, 16) || ldq % 16 != 0 || !aligned(st, 4))
     return FP8G_ERR_ALIGN;
