@@ -863,7 +863,9 @@ hipError_t launch_wgrad(const WgradArgs& args, int fmt_a, int fmt_b, const Devic
   // T 4096: 64 tiles of 256x256 18.8 / 38.7 us, 128 tiles 36.0 / 40.5, 140 tiles
   // 49.3 / 41.6, 256 tiles 67.2 / 48.7; T 1024: 64 tiles 8.8 / 16.2, 128 tiles 15.0 /
   // 16.3, 140 tiles 20.5 / 16.4)
-  if (all > dev.cu_count / 2 && args.T > 0) {
+  // (also without tokens, where the large kernel only writes zeros: its grid has
+  // a bound, that of the small one is the number of tiles)
+  if (all > dev.cu_count / 2) {
     const int64_t grid = all < dev.cu_count ? all : dev.cu_count;
     tile_pick(fmt_a, fmt_b)<<<dim3((unsigned)grid), dim3(256), 0, stream>>>(
         args, (int)mb, (int)nb, grid % 8 == 0 ? 1 : 0);
