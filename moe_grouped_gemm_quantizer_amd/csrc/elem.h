@@ -84,11 +84,19 @@ __device__ __forceinline__ double sum_wave(double x) {
   return x;
 }
 
-// exp(x) for x <= 0 (or NaN) as 2^(x log2 e): the product's rounding makes its
-// relative error |x| 2^-24 at most (as much as a difference x = a - b of that
-// size carries already), and -inf gives 0 without a test.
+// exp(x) for x <= 0 (or NaN) within 2 ulp: 2^(x log2 e), with the product's rounding
+// error and the constant's put back to first order. (Where the product is infinite that
+// error is NaN or +inf and the power 0: the minimum, which drops a NaN, makes their
+// product 0. It is below 2^-16 wherever the power is not 0.) The power alone is off by up to
+// 1.2 |x| 2^-24, which bf16 and fp16 logits, whose differences are exact, do not excuse; it
+// saves 0.9 us of 22.2 (T 32768, E 256, fp32; bf16 0.9 of 18.1) and 0.7 of 13.1 in the
+// backward pass (T 30011, E 160, fp32).
 __device__ __forceinline__ float exp_neg(float x) {
-  return __builtin_amdgcn_exp2f(x * 0x1.715476p+0f);
+  constexpr float L2E = 0x1.715476p+0f, L2E_LO = 0x1.4ae0cp-26f, LN2 = 0x1.62e43p-1f;
+  const float t = x * L2E;
+  const float lo = __builtin_fminf(__builtin_fmaf(x, L2E_LO, __builtin_fmaf(x, L2E, -t)), 1.0f);
+  const float y = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(y, lo * LN2, y);
 }
 
 }  // namespace elem

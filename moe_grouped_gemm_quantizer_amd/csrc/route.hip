@@ -16,9 +16,9 @@
 // 64 tokens are one block, and one launch does everything; small tables of
 // counts are scanned by every workgroup of the last step, in two launches.
 //
-// Measured on the GPU: T 1, E 256, k 8 5.1 us; T 4096, E 8, k 2 4.4 + 4.8 us; T
-// 32768, E 256, k 8, fp32 21.1 + 7.4 + 5.2 us where reading the logits takes 6.5;
-// backward T 30011, E 160, k 6, fp32 12.4 us (38 MB: 7.5 us).
+// Measured on the GPU: T 1, E 256, k 8 5.1 us; T 4096, E 8, k 2 4.3 + 4.4 us; T
+// 32768, E 256, k 8, fp32 22.2 + 7.2 + 5.3 us where reading the logits takes 6.5,
+// bf16 18.1 + 7.2 + 5.2; backward T 30011, E 160, k 6, fp32 13.1 us (38 MB: 7.5 us).
 
 #include <type_traits>
 #include <vector>
