@@ -595,13 +595,15 @@ fp8g_status grad_norm_sq_workspace_size(const int64_t* numels, int n, size_t* by
 
 /*
  * grad_clip -- outs[i] = grads[i] * min(1, max_norm / (norm + 1e-6)), with
- * norm = sqrt(*sumsq): the product in fp32, rounded once to the type.
+ * norm = sqrt(*sumsq): the product in fp32, rounded once to the type (a
+ * factor below 2^-126 is not rounded to fp32, where it would lose bits).
  *
  * grads, numels, types as for grad_norm_sq; outs: HOST array of device
  * pointers, outs[i] of the same type and size; outs[i] == grads[i] clips in
  * place (nothing is then read or written where the factor is 1), other
  * overlaps are not allowed.
- * sumsq      DEVICE double [1].  norm  DEVICE float [1]: written.
+ * sumsq      DEVICE double [1].  norm  DEVICE float [1]: written (infinity
+ *            where the norm is beyond fp32; the factor goes by the fp64 norm).
  * max_norm   > 0. A norm that is infinite gives the factor 0 and one that is
  *            NaN gives NaN, as the formula says.
  * Errors (nothing is launched): as for grad_norm_sq; FP8G_ERR_SHAPE for a

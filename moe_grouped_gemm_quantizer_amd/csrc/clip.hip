@@ -152,10 +152,12 @@ norm_finish_kernel(const double* __restrict__ part, int n, double* __restrict__ 
 
 // The product rounded to fp32, then to the type. (Left to itself the compiler
 // turns some fp16 products into a mixed-precision fma, which rounds once, so
-// that an element's result would depend on the path it takes.)
-template <typename T>
-__device__ __forceinline__ T scaled(T x, float f) {
-  float p = to_f32(x) * f;
+// that an element's result would depend on the path it takes.) A factor below
+// fp32's normal numbers comes as fp64: in fp32 it would lose bits, or vanish, where
+// gradients near the end of the range still have normal products.
+template <typename T, typename F>
+__device__ __forceinline__ T scaled(T x, F f) {
+  float p = (float)((F)to_f32(x) * f);
   asm("" : "+v"(p));
   return from_f32<T>(p);
 }
@@ -167,8 +169,8 @@ __device__ __forceinline__ T scaled(T x, float f) {
 // norm's pass left there (8 x 29M: 246 -> 233 us, 8 x 16M: 135 -> 131; but
 // 8 x 8M 66.5 -> 69, 8 x 2M 22.4 -> 29).
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-template <bool STREAM, typename T>
-__device__ __forceinline__ void chunk_scale(const T* x, T* y, int n, float f) {
+template <bool STREAM, typename T, typename F>
+__device__ __forceinline__ void chunk_scale(const T* x, T* y, int n, F f) {
   constexpr int W = 16 / (int)sizeof(T);
   int done = 0;
   if (((uintptr_t)x | (uintptr_t)y) % 16 == 0) {
@@ -184,6 +186,18 @@ __device__ __forceinline__ void chunk_scale(const T* x, T* y, int n, float f) {
     }
   }
   for (int i = done + threadIdx.x; i < n; i += THREADS) y[i] = scaled(x[i], f);
+}
+
+template <bool STREAM, typename F>
+__device__ __forceinline__ void table_chunk_scale(const Table& t, int i, int64_t at, F f) {
+  const int64_t left = t.numel[i] - at;
+  const int n = (int)(left < t.chunk ? left : t.chunk);
+  if (t.type[i] == TYPE_F32)
+    chunk_scale<STREAM>((const float*)t.x[i] + at, (float*)t.y[i] + at, n, f);
+  else if (t.type[i] == TYPE_BF16)
+    chunk_scale<STREAM>((const bf16_t*)t.x[i] + at, (bf16_t*)t.y[i] + at, n, f);
+  else
+    chunk_scale<STREAM>((const f16_t*)t.x[i] + at, (f16_t*)t.y[i] + at, n, f);
 }
 
 // (n == 0: one workgroup writes the norm)
@@ -202,14 +216,8 @@ clip_kernel(Table t, const double* __restrict__ sumsq, float max_norm, float* __
     int64_t at;
     const int i = find(t, c, at);
     if (t.x[i] == t.y[i] && f == 1.0f) continue;
-    const int64_t left = t.numel[i] - at;
-    const int n = (int)(left < t.chunk ? left : t.chunk);
-    if (t.type[i] == TYPE_F32)
-      chunk_scale<STREAM>((const float*)t.x[i] + at, (float*)t.y[i] + at, n, f);
-    else if (t.type[i] == TYPE_BF16)
-      chunk_scale<STREAM>((const bf16_t*)t.x[i] + at, (bf16_t*)t.y[i] + at, n, f);
-    else
-      chunk_scale<STREAM>((const f16_t*)t.x[i] + at, (f16_t*)t.y[i] + at, n, f);
+    if (q < 0x1p-126) table_chunk_scale<STREAM>(t, i, at, q);
+    else table_chunk_scale<STREAM>(t, i, at, f);
   }
 }
 
