@@ -584,13 +584,15 @@ fp8g_status grouped_gemm_fp8_wgrad(const uint8_t* a, int fmt_a, int64_t lda, con
  * workspace  device memory, 8-byte aligned, at least
  *            grad_norm_sq_workspace_size bytes.
  * Errors (nothing is launched): FP8G_ERR_SHAPE (negative sizes),
- * _NULL_PTR, _ALIGN, _UNSUPPORTED (unknown type), _WORKSPACE.
+ * _NULL_PTR, _ALIGN, _UNSUPPORTED (unknown type, a tensor of more than 2^45
+ * elements), _WORKSPACE.
  */
 fp8g_status grad_norm_sq(const void* const* grads, const int64_t* numels, const int* types, int n,
                          double* sumsq, void* workspace, size_t workspace_bytes,
                          hipStream_t stream);
 /* Bytes of workspace that grad_norm_sq needs for this list (HOST arrays).
- * Errors: FP8G_ERR_NULL_PTR, FP8G_ERR_SHAPE (*bytes is then 0). */
+ * Errors: FP8G_ERR_NULL_PTR, FP8G_ERR_SHAPE, FP8G_ERR_UNSUPPORTED as for
+ * grad_norm_sq (*bytes is then 0). */
 fp8g_status grad_norm_sq_workspace_size(const int64_t* numels, int n, size_t* bytes);
 
 /*

@@ -14,6 +14,7 @@ namespace {
 
 inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 constexpr int64_t kInt31 = 0x7FFFFFFF;
+constexpr int64_t kNumelMax = int64_t(1) << 45;     // elements of a tensor of a gradient list
 
 inline bool type_ok(int type) { return type >= FP8G_TYPE_F32 && type <= FP8G_TYPE_F16; }
 inline uintptr_t type_size(int type) { return type == FP8G_TYPE_F32 ? 4 : 2; }
@@ -32,7 +33,7 @@ fp8g_status list_ok(const void* const* grads, const int64_t* numels, const int* 
   if (n > 0 && (!grads || !numels || !types)) return FP8G_ERR_NULL_PTR;
   for (int i = 0; i < n; ++i) {
     if (numels[i] < 0) return FP8G_ERR_SHAPE;
-    if (!type_ok(types[i]) || numels[i] > (int64_t(1) << 45)) return FP8G_ERR_UNSUPPORTED;
+    if (!type_ok(types[i]) || numels[i] > kNumelMax) return FP8G_ERR_UNSUPPORTED;
     if (numels[i] == 0) continue;
     if (!grads[i]) return FP8G_ERR_NULL_PTR;
     if (!aligned(grads[i], type_size(types[i]))) return FP8G_ERR_ALIGN;
@@ -193,8 +194,10 @@ fp8g_status grad_norm_sq_workspace_size(const int64_t* numels, int n, size_t* by
   *bytes = 0;
   if (n < 0) return FP8G_ERR_SHAPE;
   if (n > 0 && !numels) return FP8G_ERR_NULL_PTR;
-  for (int i = 0; i < n; ++i)
+  for (int i = 0; i < n; ++i) {
     if (numels[i] < 0) return FP8G_ERR_SHAPE;
+    if (numels[i] > kNumelMax) return FP8G_ERR_UNSUPPORTED;
+  }
   *bytes = grad_norm_workspace_bytes(numels, n);
   return FP8G_OK;
 }
