@@ -455,7 +455,9 @@ enum { FP8G_TYPE_F32 = 0, FP8G_TYPE_BF16 = 1, FP8G_TYPE_F16 = 2 };
  *                     owns rows group_offsets[e] .. + counts[e], every entry
  *                     a multiple of align (128 for
  *                     grouped_gemm_fp8_contiguous; at most
- *                     T top_k + E (align - 1) rows in all).
+ *                     T top_k + E (align - 1) rows in all). Rows from
+ *                     group_offsets[e] + counts[e] to the next offset hold
+ *                     no token: grouped_gemm_fp8_wgrad needs zeros there.
  *                     max_m > 0, the masked layout: e * max_m (counts is
  *                     then grouped_gemm_fp8_masked's masked_m).
  * Tokens whose token_mask byte is 0 (padding) choose nothing: ids and slots
@@ -527,6 +529,8 @@ fp8g_status moe_route_backward(const void* logits, int type, int64_t T, int E, i
  *
  * x     type FP8G_TYPE_*, [rows][ldx], aligned to its element (16-byte
  *       aligned rows are read faster). rows >= 0, cols > 0, cols % 16 == 0.
+ *       Every row counts, whether a token fills it or not (see
+ *       grouped_gemm_fp8_wgrad): zeros change neither a scale nor a sum.
  * qt    uint8 codes [cols][ldq], 16-byte aligned, ldq % 16 == 0,
  *       ldq >= R = rows rounded up to a multiple of 128. Columns rows .. R-1
  *       are written as zeros, so that qt is an operand of R tokens.
@@ -553,7 +557,14 @@ fp8g_status fp8_quantize_transpose(const void* x, int type, int64_t rows, int64_
  *                128, non-decreasing, from 0 to at most T), or NULL with
  *                G == 1: all T tokens. Entries are clamped into [0, T] and
  *                rounded down to 128: whatever they hold, no access leaves
- *                the arrays.
+ *                the arrays. EVERY row from group_offsets[g] up to
+ *                group_offsets[g + 1] is a row of expert g, those past its
+ *                last token too: they must be zero in both x that were
+ *                quantised (clear the buffers before dealing tokens into
+ *                them), or they enter the scales and the sum; a NaN there
+ *                spoils it even against a zero. So it is with a masked
+ *                layout's slabs (max_m a multiple of 128) past their counts.
+ *                Rows from group_offsets[G] on are not read.
  * d              bf16 bits [G][M][N], 16-byte aligned, every element
  *                written: zeros for an expert without tokens.
  * G >= 0, T >= 0, T % 128 == 0 (the padded token count), M, N > 0 and

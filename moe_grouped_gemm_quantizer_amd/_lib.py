@@ -530,7 +530,7 @@ def fp8_quantize_transpose(x, fmt, qt, st, stream=None):
     """x [rows][cols] (float32, bfloat16 or float16; rows may be strided) ->
     qt uint8 [cols][R] codes in fmt ('e4m3' or 'e5m2'), R = rows rounded up to
     128, and st uint8 [R/128][cols]: one power-of-two scale per column and 128
-    rows, as its exponent + 127."""
+    rows, as its exponent + 127. Rows that hold no token must be zero."""
     torch = _torch()
     xp, rows, cols, ldx = _rows(x, "x")
     nb = (rows + 127) // 128
@@ -551,7 +551,9 @@ def grouped_gemm_fp8_wgrad(a, fmt_a, sa, b, fmt_b, sb, d, group_offsets=None, st
     """Weight gradients of G experts: d bf16 [G][M][N] from a [M][T], sa
     [T/128][M], b [N][T], sb [T/128][N] as fp8_quantize_transpose writes them
     (T a multiple of 128); group_offsets int32 [G+1] (device) or None (G = 1,
-    all tokens)."""
+    all tokens). Every row of x from one offset up to the next is summed, also
+    those past an expert's last token: clear the buffers that tokens are dealt
+    into, since whatever such a row holds enters scales and sum."""
     torch = _torch()
     ap, M, T, lda = _rows(a, "a")
     bp, N, Tb, ldb = _rows(b, "b")
