@@ -733,10 +733,13 @@ Pick pick_for(int E) {
   if (E <= 16) return FP8G_PICK(16, 1);
   if (E <= 32) return FP8G_PICK(16, 2);
   if (E <= 64) return FP8G_PICK(16, 4);
-  if (few && E <= 256) return FP8G_PICK(64, 4);
-  if (E <= 128) return FP8G_PICK(16, 8);
-  if (E <= 192) return FP8G_PICK(16, 12);
-  if (E <= 256) return FP8G_PICK(16, 16);
+  if constexpr (few) {
+    if (E <= 256) return FP8G_PICK(64, 4);
+  } else {
+    if (E <= 128) return FP8G_PICK(16, 8);
+    if (E <= 192) return FP8G_PICK(16, 12);
+    if (E <= 256) return FP8G_PICK(16, 16);
+  }
   if (E <= 512) return FP8G_PICK(64, 8);
   return FP8G_PICK(64, 16);
 #undef FP8G_PICK
