@@ -65,9 +65,12 @@ def test_a_large_list_of_unaligned_views():
     check([base[0][1:69_000_000], base[1][3:], base[0][69_000_001:69_999_990]], 0.25)
 
 
-@pytest.mark.parametrize("total", [131_071, 131_072, 131_073, 1_000_000])
+@pytest.mark.parametrize("total", [65_535, 65_536, 65_537, 131_072, 1_000_000, 1_048_577])
 def test_around_the_single_launch(total):
-    """Lists up to 131,072 values are summed by one workgroup."""
+    """Up to 32 chunks of 2048 values are summed by one workgroup."""
+    check(tensors([total], [F32], total), 0.5)
+    check(tensors([total // 32] * 31 + [total - total // 32 * 31], [BF16] * 32, total), 0.5)
+    check(tensors([total // 33] * 32 + [total - total // 33 * 32], [BF16] * 33, total), 0.5)
     check(tensors([total - 4097, 4096, 1], [F32, BF16, F32], total), 0.5)
     check(tensors([total // 112] * 111 + [total - total // 112 * 111], [F16] * 112, total), 0.5)
     check(tensors([total // 113] * 112 + [total - total // 113 * 112], [F16] * 113, total), 0.5)
