@@ -520,8 +520,12 @@ route_slots_kernel(RouteArgs a) {
 
 // Scan and slots in one launch, for tables of counts so small that every
 // workgroup may read all of it: one workgroup per block of tokens, EP threads
-// (a power of two over E) side by side in a row of the table.
-constexpr int JOIN_MAX = 8192;                         // entries of the table
+// (a power of two over E) side by side in a row of the table. Every workgroup
+// reads blocks x EP / THREADS entries a thread, so that product decides (scan and slots
+// against the joined launch, whole calls): 4096: E 15 13.9 / 12.8 us, E 63 14.8 / 13.0,
+// E 255 21.5 / 19.3; 5120: E 8 14.5 / 14.3, E 31 14.5 / 13.7, E 127 16.6 / 16.4; 6144: E 15
+// 15.6 / 15.8, E 63 14.5 / 15.6, E 255 21.4 / 22.1; 16384: E 255 22.3 / 33.2.
+constexpr int JOIN_MAX = 5120;
 __global__ void __launch_bounds__(THREADS)
 route_join_kernel(RouteArgs a, int nblk, int EP) {
   __shared__ int before[THREADS], total[THREADS];
@@ -815,9 +819,9 @@ hipError_t launch_route(const RouteCall& c, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (nblk > 1 && c.E < THREADS && nblk * (c.E + 1) <= JOIN_MAX) {
-    int ep = 1;
-    while (ep <= c.E) ep *= 2;
+  int ep = 1;
+  while (ep <= c.E) ep *= 2;
+  if (nblk > 1 && ep <= THREADS && nblk * ep <= JOIN_MAX) {
     route_join_kernel<<<dim3((unsigned)nblk), dim3(THREADS), 0, stream>>>(a, (int)nblk, ep);
   } else if (nblk > 1) {
     route_scan_kernel<<<dim3((unsigned)(c.E / COLS + 1)), dim3(COLS * RUNS), 0, stream>>>(a, (int)nblk);
