@@ -857,23 +857,30 @@ hipError_t launch_quantize_transpose(const void* x, int type, int64_t rows, int6
 
 hipError_t launch_wgrad(const WgradArgs& args, int fmt_a, int fmt_b, const DeviceInfo& dev,
                         hipStream_t stream) {
+  const int64_t cus = dev.cu_count;
   const int64_t mb = (args.M + TS - 1) / TS, nb = (args.N + TS - 1) / TS, all = mb * nb * args.G;
+  const int64_t mblocks = (args.M + BT - 1) / BT, nblocks = (args.N + BT - 1) / BT;
+  const int64_t small = mblocks * nblocks * args.G;
   // 256x256 tiles when they are more than half the CUs; up to there, at most two
   // rounds of 128x128 tiles, whose copies are further ahead (dense, 128 against 256,
   // T 4096: 64 tiles of 256x256 18.8 / 38.7 us, 128 tiles 36.0 / 40.5, 140 tiles
   // 49.3 / 41.6, 256 tiles 67.2 / 48.7; T 1024: 64 tiles 8.8 / 16.2, 128 tiles 15.0 /
-  // 16.3, 140 tiles 20.5 / 16.4)
-  // (also without tokens, where the large kernel only writes zeros: its grid has
-  // a bound, that of the small one is the number of tiles)
-  if (all > dev.cu_count / 2) {
-    const int64_t grid = all < dev.cu_count ? all : dev.cu_count;
+  // 16.3, 140 tiles 20.5 / 16.4). And only where 128x128 tiles need more rounds of
+  // the CUs: many narrow experts leave most of a large tile empty (experts of T tokens,
+  // rounds of 128 / of 256: 160 of T 128 64x64, 1 / 1, 4.2 / 8.1 us; 512 of T 128 128x128,
+  // 2 / 2, 9.7 / 13.0; 160 of T 512 128x128, 1 / 1, 6.2 / 11.3; 160 of T 2048 384x128, 2 / 2, 44 / 48;
+  // 160 of T 512 128x640, 4 / 2, 30.5 / 21.3; 400 of T 512 384x128, 5 / 4, 40.2 / 37.2; 64 of
+  // T 512 528x528, 7 / 3, 36.3 / 31.7; but 33 of T 384 512x784, 4 / 2, 21.9 / 24.3).
+  // (Also without tokens, where both only write zeros: the large kernel's grid has a
+  // bound, and as many rounds are at most some hundred tiles more.)
+  if (all > cus / 2 && (small + cus - 1) / cus > (all + cus - 1) / cus) {
+    const int64_t grid = all < cus ? all : cus;
     tile_pick(fmt_a, fmt_b)<<<dim3((unsigned)grid), dim3(256), 0, stream>>>(
         args, (int)mb, (int)nb, grid % 8 == 0 ? 1 : 0);
     return hipGetLastError();
   }
-  const int64_t mblocks = (args.M + BT - 1) / BT, nblocks = (args.N + BT - 1) / BT;
-  ring_pick(fmt_a, fmt_b)<<<dim3((unsigned)(mblocks * nblocks * args.G)), dim3(256), 0, stream>>>(
-      args, (int)mblocks, (int)nblocks);
+  ring_pick(fmt_a, fmt_b)<<<dim3((unsigned)small), dim3(256), 0, stream>>>(args, (int)mblocks,
+                                                                            (int)nblocks);
   return hipGetLastError();
 }
 

@@ -84,6 +84,19 @@ def test_tiles_one_after_the_other(which):
     assert torch.equal(product(ops, M, N, ends, len(counts)).view(torch.int16), d.view(torch.int16))
 
 
+@pytest.mark.parametrize("counts,M,N", [([128] * 300, 128, 128), ([1, 200, 0, 513] * 60, 64, 112),
+                                        ([128] * 700, 16, 48), ([300] * 150, 384, 128)])
+def test_many_narrow_experts(counts, M, N):
+    """More tiles than CUs, none of which 256x256 would fill: several rounds of
+    the small kernel."""
+    banner(f"wgrad narrow: {len(counts)} experts M={M} N={N}")
+    ends = ends_of(counts)
+    T = int(ends[-1])
+    dy, x = integers(T, M, 5), integers(T, N, 6)
+    d = product((*_q(dy, "e5m2"), *_q(x, "e4m3")), M, N, ends, len(counts))
+    assert torch.equal(d.view(torch.int16), exact(dy, x, ends).view(torch.int16))
+
+
 def _q(x, fmt):
     q, s = quantised(x, fmt)
     return q, fmt, s
