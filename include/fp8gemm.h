@@ -450,7 +450,8 @@ enum { FP8G_TYPE_F32 = 0, FP8G_TYPE_BF16 = 1, FP8G_TYPE_F16 = 2 };
  *                     that is not masked out has NaN probabilities).
  *   loss[0]           loss_coef * sum_e (E counts[e] / (top_k n)) (prob_sum[e] / n),
  *                     the balance loss: loss_coef when tokens and
- *                     probability are spread evenly; 0 for n = 0.
+ *                     probability are spread evenly; 0 for n = 0, NaN where
+ *                     prob_sum is.
  *   group_offsets     max_m == 0, the contiguous layout: [E + 1], expert e
  *                     owns rows group_offsets[e] .. + counts[e], every entry
  *                     a multiple of align (128 for
@@ -571,8 +572,10 @@ fp8g_status fp8_quantize_transpose(const void* x, int type, int64_t rows, int64_
  * multiples of 16. lda, ldb >= T, multiples of 16. a, b 16-byte, sa, sb
  * 4-byte aligned.
  * The sums stay in fp32 registers over all of an expert's tokens; the matrix
- * instruction applies the scales. (It adds its 128 products with about 16
- * good bits, which is why the result is bf16 and not fp32.)
+ * instruction applies the scales. (It adds its 64 products with about 16 good
+ * bits: 2^-16 of the sum on normal data, up to 2^-12 of the sum of their
+ * magnitudes on codes from all over a format's range, without growing over
+ * the tokens. That is why the result is bf16 and not fp32.)
  * Errors (nothing is launched): FP8G_ERR_SHAPE, _NULL_PTR, _STRIDE, _ALIGN
  * as stated; _UNSUPPORTED for an unknown format, lda or ldb > 2^24,
  * G > 1024, or more than 2^31 - 1 tiles of 128x128. G == 0 is a no-op;

@@ -309,8 +309,9 @@ __device__ __forceinline__ int slot_of(const RouteArgs& a, int e, int first, int
 // (16 lanes per row) all rows of a block are worked on at once: its time is
 // that of one row's chain of dependent steps, which four waves that walk the
 // block go through four times (T 4096, E 8: 6.4 -> 4.5 us; T 32768, E 256: 27
-// -> 26). Bound by the vector unit at many experts: about 850 instructions for
-// four rows of 256.
+// -> 26). Bound by the vector unit at many experts: about 990 instructions for
+// four rows of 256, 13 us of the 22 at T 32768, after the loads (6.5), which a
+// workgroup's two sets of rows do not overlap with them.
 template <typename T, int LPR, int VPT, int NT>
 __global__ void __launch_bounds__(NT)
 route_rows_kernel(RouteArgs a) {

@@ -485,11 +485,15 @@ wgrad_ring_kernel(WgradArgs a, int mblocks, int nblocks) {
 // 16x16x128 do not; copies in bursts leave the matrix unit waiting.
 //
 // Measured (T 4096, 8192x8192: 550 GFLOP; T 4096, 8 experts, 4096x7168: 470 MB of
-// results): first version, one barrier and three bursts of copies a step 215 and 209
+// results), the kernel alone, repeated, random codes under one scale: first version,
+// one barrier and three bursts of copies a step 215 and 209
 // us; two meets, spread copies 205 and 205; 32x32x64, whole-line stores 197 and 166;
 // a tile's first step from a zero operand 192 (2.9 PFLOP/s; the library's 8-bit
-// product of 8192^3 reaches 3.06 here) and 158.
-// Before that last step, without copies 168 and 149, without stores 175 and 97,
+// product of 8192^3 reaches 3.06 here) and 158. On quantised normal data 206
+// (2.67 PFLOP/s) and 164, since the clock that the chip holds goes by the data (beside the
+// first 1.6 to 1.7 GHz, 1.8 on random codes; beside the second 1.8 to 1.9 and 2.0). Under the
+// kernel trace 236 and 185.
+// Before the last step, without copies 168 and 149, without stores 175 and 97,
 // with neither 147 and 85: the large layer is bound by the copies' issue, the
 // experts by writing 128 KB per tile after 2 to 15 steps, during which the matrix
 // unit is idle and the next copies queue behind the stores. Prefetching into L2, operands laid out in tiles,
