@@ -294,6 +294,8 @@ hipError_t launch_grad_norm_sq(const void* const* grads, const int64_t* numels, 
       return hipGetLastError();
     }
     norm_partial_kernel<<<dim3((unsigned)grid), dim3(THREADS), 0, stream>>>(t, part + parts);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;                     // (the sum would be of what is not there)
     parts += (int)grid;
   }
   norm_finish_kernel<<<dim3(1), dim3(THREADS), 0, stream>>>(part, parts, sumsq);
@@ -314,10 +316,12 @@ hipError_t launch_grad_clip(const void* const* grads, void* const* outs, const i
     if (grid == 0 && !first) break;
     kernel<<<dim3((unsigned)(grid ? grid : 1)), dim3(THREADS), 0, stream>>>(t, sumsq, max_norm, norm,
                                                                             first);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     first = 0;
     if (grid == 0) break;
   }
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 void clip_kernels(std::vector<const void*>& out) {
