@@ -605,8 +605,9 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// workgroups per CU of the backward pass (T 30011, E 160: 8: 15.3 us, 6: 12.5, 4: 12.4,
-// 2: 13.1; with 8 every workgroup has one set of rows and nothing to load ahead)
+// workgroups per CU of the backward pass (T 30011, E 160, fp32: 8: 16.5 us, 6: 13.9, 4: 13.4,
+// 2: 14.3; with 8 every workgroup has one set of rows and nothing to load ahead. T 65536,
+// E 64, bf16: 11.6, 11.5, 12.2, 15.2)
 constexpr int BWD_PER_CU = 4;
 
 struct RouteBwdArgs {
@@ -729,7 +730,8 @@ template <typename T, int NT>
 Pick pick_for(int E) {
   constexpr bool few = NT == THREADS;
   // (from 12 values a lane on, two workgroups of 512 threads fit a CU's registers
-  // and one of 1024 alone: T 32768, E 256 33.7 -> 32.1 us; E 64 19.7 -> 20.3)
+  // and one of 1024 alone: T 32768, fp32, E 256 23.5 -> 22.1 us, E 160 18.9 -> 17.2; whole
+  // calls of E 64 19.7 -> 20.3)
   constexpr int WIDE = NT > 512 ? 512 : NT;
 #define FP8G_PICK(LPR_, VPT_)                                                             \
   Pick { route_rows_kernel<T, LPR_, VPT_, LPR_ == 16 && VPT_ >= 12 ? WIDE : NT>,          \

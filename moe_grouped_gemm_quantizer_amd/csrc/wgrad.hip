@@ -246,8 +246,8 @@ quant_transpose_kernel(const T* __restrict__ x, int64_t rows, int64_t cols, int6
 }
 
 // ---------------------------------------------------------------------------
-// The product. Two kernels: 256x256 tiles where there are enough of them to
-// fill the chip, 128x128 tiles below. In both, codes go from global memory
+// The product. Two kernels: 256x256 tiles where there are enough of them to fill the chip
+// and they are full enough, 128x128 tiles otherwise. In both, codes go from global memory
 // straight into LDS; each 128-byte LDS row holds one row's 128 tokens, its
 // 16-byte chunks swizzled (swz).
 
