@@ -629,6 +629,84 @@ fp8g_status grad_clip(const void* const* grads, void* const* outs, const int64_t
                       const int* types, int n, const double* sumsq, float max_norm, float* norm,
                       hipStream_t stream);
 
+/* ---- Products in 8-bit integers ---------------------------------------------
+ * The other common 8-bit form of a served layer: whole numbers -127 .. 127
+ * with one fp32 scale for each token of the activations and one for each
+ * output channel of the weights. The products are summed exactly in 32-bit
+ * integers and scaled once, so results do not depend on how the work is cut.
+ * Layouts are those of the FP8 products (nxmr §3.2, czchanglian §5.3). */
+
+/*
+ * int8_quantize -- rows as 8-bit integers with one scale each (czchanglian
+ * §2.2: activations per token, weights per channel; a weight matrix [N][K]
+ * has its channels as rows, stacked experts [G][N][K] are G N rows).
+ *
+ * For each row: amax = max |x|; scale = fl32(amax / 127);
+ *   q = rne(fl32(x fl32(127 / amax))), never outside -127 .. 127.
+ * A row with amax < 2^-120 counts as zero: scale 0, codes 0. A row with an
+ * infinity or NaN gets the scale NaN and codes 0, so that each result formed
+ * of it is NaN.
+ *
+ * x       type FP8G_TYPE_*, [rows][ldx], aligned to its element (16-byte
+ *         aligned rows are read faster). rows >= 0, cols > 0, cols % 16 == 0.
+ * q       int8 [rows][ldq], 16-byte aligned, ldq % 16 == 0.
+ * scales  fp32 [rows], 4-byte aligned.
+ * Errors (nothing is launched): FP8G_ERR_SHAPE, _NULL_PTR, _STRIDE, _ALIGN
+ * as stated; _UNSUPPORTED for an unknown type. rows == 0 is a no-op.
+ */
+fp8g_status int8_quantize(const void* x, int type, int64_t rows, int64_t cols, int64_t ldx, int8_t* q,
+                          int64_t ldq, float* scales, hipStream_t stream);
+
+/*
+ * gemm_int8 -- d[m][n] = bf16( (fl32(sum_k a[m][k] b[n][k]) * sa[m]) * sb[n] )
+ *
+ * a   int8 [M][K], b int8 [N][K] (both K contiguous, 16-byte aligned; every
+ *     code may occur, -128 too). sa fp32 [M], sb fp32 [N], 4-byte aligned.
+ * d   bf16 bits [M][N], 16-byte aligned; fully overwritten.
+ * M >= 0; N > 0, K > 0, multiples of 16; K <= 131056, up to which no sum
+ * leaves 32 bits.
+ * Errors (nothing is launched): FP8G_ERR_SHAPE, _NULL_PTR, _ALIGN as stated;
+ * _UNSUPPORTED for a larger K, N > 2^27, M > 2^30 or more than 2^31 - 1
+ * tiles of 128x128. M == 0 is a no-op.
+ */
+fp8g_status gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const float* sb, uint16_t* d,
+                      int64_t M, int64_t N, int64_t K, hipStream_t stream);
+
+/*
+ * grouped_gemm_int8_contiguous -- every expert's product in one launch,
+ * contiguous layout: expert g owns rows [group_offsets[g],
+ * group_offsets[g + 1]) of a, sa and d.
+ *
+ * a  int8 [M_total][K], sa fp32 [M_total]; b int8 [G][N][K], sb fp32 [G][N];
+ * d  bf16 bits [M_total][N]: the experts' rows are written, rows that belong
+ *    to no expert (behind group_offsets[G]) are left as they were.
+ * group_offsets  DEVICE int32 [G + 1], non-decreasing, in [0, M_total]. They
+ *    need not be multiples of 128, nor must M_total (unlike for the FP8 call,
+ *    the scales have no blocks). Entries are clamped into [0, M_total] and an
+ *    expert whose end lies before its start has no rows: whatever they hold,
+ *    no access leaves the arrays.
+ * N, K and errors as for gemm_int8; FP8G_ERR_UNSUPPORTED for G > 1024.
+ * G == 0 and M_total == 0 are no-ops.
+ */
+fp8g_status grouped_gemm_int8_contiguous(const int8_t* a, const float* sa, const int8_t* b, const float* sb,
+                                         uint16_t* d, const int32_t* group_offsets, int G, int64_t M_total,
+                                         int64_t N, int64_t K, hipStream_t stream);
+
+/*
+ * grouped_gemm_int8_masked -- the same in the masked layout: slabs of max_m
+ * rows, of which expert g's first masked_m[g] (DEVICE int32 [G], clamped to
+ * [0, max_m]) are valid. Other rows of d are left as they were, and experts
+ * without rows read none of their weights.
+ *
+ * a int8 [G][max_m][K], sa fp32 [G][max_m], b int8 [G][N][K], sb fp32 [G][N],
+ * d bf16 bits [G][max_m][N]. expected_m: host hint of the typical masked_m
+ * (0 = unknown); it may change the tiles, never the result.
+ * Errors as for the contiguous call, with max_m for M_total.
+ */
+fp8g_status grouped_gemm_int8_masked(const int8_t* a, const float* sa, const int8_t* b, const float* sb,
+                                     uint16_t* d, const int32_t* masked_m, int G, int64_t max_m, int64_t N,
+                                     int64_t K, int expected_m, hipStream_t stream);
+
 /*
  * fp8g_clock_probe -- diagnostic: the shader clock the GPU holds right now.
  *

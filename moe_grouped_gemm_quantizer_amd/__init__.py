@@ -13,6 +13,8 @@ from ._lib import (fp8_quantize, fp8_quantize_bf16, fp8_quantize_tensor, gemm_fp
                    moe_route, moe_route_workspace_size, moe_route_backward,
                    fp8_quantize_transpose, grouped_gemm_fp8_wgrad,
                    grad_norm_sq, grad_norm_sq_workspace_size, grad_clip,
+                   int8_quantize, gemm_int8, grouped_gemm_int8_contiguous,
+                   grouped_gemm_int8_masked,
                    fp8g_clock_probe, fp8g_warmup,
                    fp8g_set_shape_specialisation, fp8g_gemm_kernel_name, fp8g_abi_version,
                    status_string, load,
@@ -26,6 +28,8 @@ __all__ = ["fp8_quantize", "fp8_quantize_bf16", "fp8_quantize_tensor", "gemm_fp8
            "moe_route", "moe_route_workspace_size", "moe_route_backward",
            "fp8_quantize_transpose", "grouped_gemm_fp8_wgrad",
            "grad_norm_sq", "grad_norm_sq_workspace_size", "grad_clip",
+           "int8_quantize", "gemm_int8", "grouped_gemm_int8_contiguous",
+           "grouped_gemm_int8_masked",
            "fp8g_clock_probe", "fp8g_warmup",
            "fp8g_set_shape_specialisation", "fp8g_gemm_kernel_name", "fp8g_abi_version",
            "status_string", "load",

@@ -25,6 +25,8 @@ ENTRY_POINTS = ("fp8_quantize", "fp8_quantize_bf16", "fp8_quantize_tensor", "gem
                 "moe_route", "moe_route_workspace_size", "moe_route_backward",
                 "fp8_quantize_transpose", "grouped_gemm_fp8_wgrad", "grad_norm_sq",
                 "grad_norm_sq_workspace_size", "grad_clip",
+                "int8_quantize", "gemm_int8", "grouped_gemm_int8_contiguous",
+                "grouped_gemm_int8_masked",
                 "fp8g_status_string", "fp8g_abi_version")
 
 _c_i64 = ctypes.c_int64
@@ -73,6 +75,12 @@ _SIGS = {
     "grad_norm_sq": [_c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_sz, _c_vp],
     "grad_norm_sq_workspace_size": [_c_vp, _c_int, ctypes.POINTER(_c_sz)],
     "grad_clip": [_c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_f, _c_vp, _c_vp],
+    "int8_quantize": [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp],
+    "gemm_int8": [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp],
+    "grouped_gemm_int8_contiguous": [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_i64, _c_i64,
+                                     _c_i64, _c_vp],
+    "grouped_gemm_int8_masked": [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_i64, _c_i64,
+                                 _c_i64, _c_int, _c_vp],
 }
 
 LAYOUTS = {"dense": 0, "contiguous": 1, "masked": 2, "pertensor": 3}
@@ -638,6 +646,90 @@ def grad_clip(grads, outs, sumsq, max_norm, norm, stream=None):
     nrm = _out(norm, (1,), torch.float32, "norm")
     _check(load().grad_clip(_at(ptrs), _at(optrs), _at(numels), _at(types), len(ptrs), total, max_norm, nrm,
                             _stream(stream)), "grad_clip")
+
+
+def _one_device(*ts):
+    """The calls below launch on the current device, whose memory the tensors
+    have to be."""
+    at = _torch()._C._cuda_getDevice()
+    for t in ts:
+        if t.get_device() != at:
+            _fail(f"tensors must live on the current device (cuda:{at})")
+
+
+def int8_quantize(x, q, scales, stream=None):
+    """x [rows][cols] (float32, bfloat16 or float16; rows may be strided) ->
+    q int8 [rows][cols] (rows may be strided) and scales float32 [rows]: one
+    scale a row, amax / 127. For activations rows are tokens, for weights
+    [N][K] output channels."""
+    torch = _torch()
+    xp, rows, cols, ldx = _rows(x, "x")
+    qp, qrows, qcols, ldq = _rows(q, "q")
+    typ = _TYPES.get(x.dtype)
+    if typ is None:
+        _fail("x must be float32, bfloat16 or float16")
+    if q.dtype is not torch.int8 or qrows != rows or qcols != cols:
+        _fail("q must be int8 of x's shape")
+    sp = _out(scales, (rows,), torch.float32, "scales")
+    _one_device(x, q, scales)
+    st = load().int8_quantize(xp, typ, rows, cols, ldx, qp, ldq, sp, _stream(stream))
+    if st:
+        _check(st, "int8_quantize")
+
+
+def _int8_args(a, sa, b, sb, d, rows, weights, group, groups):
+    """Pointers of an integer product's operands: a and d with the row shape
+    `rows`, b and sb with the leading shape `weights`."""
+    torch = _torch()
+    K, N = a.shape[-1], b.shape[-2]
+    i8, f32 = torch.int8, torch.float32
+    dt = d.dtype
+    if dt is not torch.bfloat16 and dt is not torch.int16 and dt is not torch.uint16:
+        _fail("d must hold bf16 values (bfloat16, or int16/uint16 bit patterns)")
+    ptrs = [_out(a, rows + (K,), i8, "a"), _out(sa, rows, f32, "sa"), _out(b, weights + (N, K), i8, "b"),
+            _out(sb, weights + (N,), f32, "sb"), _out(d, rows + (N,), dt, "d")]
+    _one_device(a, sa, b, sb, d)
+    if group is not None:
+        ptrs.append(_out(group, (groups,), torch.int32, "group metadata"))
+        _one_device(group)
+    return ptrs, N, K
+
+
+def gemm_int8(a, sa, b, sb, d, stream=None):
+    """a int8 [M][K], sa float32 [M], b int8 [N][K], sb float32 [N], d bf16
+    (int16/bfloat16) [M][N]: the exact integer product times both scales."""
+    if a.dim() != 2 or b.dim() != 2:
+        _fail("a and b must be matrices")
+    M = a.shape[0]
+    ptrs, N, K = _int8_args(a, sa, b, sb, d, (M,), (), None, 0)
+    st = load().gemm_int8(*ptrs, M, N, K, _stream(stream))
+    if st:
+        _check(st, "gemm_int8")
+
+
+def grouped_gemm_int8_contiguous(a, sa, b, sb, d, group_offsets, stream=None):
+    """a int8 [M_total][K], sa float32 [M_total], b int8 [G][N][K], sb float32
+    [G][N], d [M_total][N], group_offsets int32 [G+1] (device; any
+    non-decreasing rows). Rows of no expert are left as they were."""
+    if a.dim() != 2 or b.dim() != 3:
+        _fail("a must be [M_total][K] and b [G][N][K]")
+    M, G = a.shape[0], b.shape[0]
+    ptrs, N, K = _int8_args(a, sa, b, sb, d, (M,), (G,), group_offsets, G + 1)
+    st = load().grouped_gemm_int8_contiguous(*ptrs, G, M, N, K, _stream(stream))
+    if st:
+        _check(st, "grouped_gemm_int8_contiguous")
+
+
+def grouped_gemm_int8_masked(a, sa, b, sb, d, masked_m, expected_m=0, stream=None):
+    """a int8 [G][max_m][K], sa float32 [G][max_m], b int8 [G][N][K], sb
+    float32 [G][N], d [G][max_m][N], masked_m int32 [G] (device)."""
+    if a.dim() != 3 or b.dim() != 3:
+        _fail("a must be [G][max_m][K] and b [G][N][K]")
+    G, max_m = a.shape[0], a.shape[1]
+    ptrs, N, K = _int8_args(a, sa, b, sb, d, (G, max_m), (G,), masked_m, G)
+    st = load().grouped_gemm_int8_masked(*ptrs, G, max_m, N, K, int(expected_m), _stream(stream))
+    if st:
+        _check(st, "grouped_gemm_int8_masked")
 
 
 def fp8g_clock_probe(out, ticks=2000, stream=None):

@@ -99,6 +99,7 @@ fp8g_status fp8g_warmup(void) {
   route_kernels(kernels);
   wgrad_kernels(kernels);
   clip_kernels(kernels);
+  int8_kernels(kernels);
   for (const void* k : kernels) {
     hipFuncAttributes attr;
     if (hipFuncGetAttributes(&attr, k) != hipSuccess) {

@@ -154,6 +154,23 @@ hipError_t launch_grad_clip(const void* const* grads, void* const* outs, const i
                             float* norm, hipStream_t stream);
 void clip_kernels(std::vector<const void*>& out);
 
+// Products in 8-bit integers (int8.hip).
+hipError_t launch_int8_quantize(const void* x, int type, int64_t rows, int64_t cols, int64_t ldx, int8_t* q,
+                                int64_t ldq, float* scales, hipStream_t stream);
+struct Int8Args {
+  const int8_t* a;         // codes, rows of K
+  const float* sa;         // a scale for each row of a
+  const int8_t* b;         // codes [G][N][K]
+  const float* sb;         // [G][N]
+  uint16_t* d;             // bf16 bits, rows of N
+  const int32_t* group;    // contiguous: offsets [G + 1]; masked: counts [G]; dense: null
+  int64_t rows;            // dense: M; contiguous: M_total; masked: max_m
+  int64_t N, K;
+  int G, mode;             // MODE_DENSE, MODE_CONTIGUOUS or MODE_MASKED
+};
+hipError_t launch_int8(const Int8Args& args, const DeviceInfo& dev, int expected_m, hipStream_t stream);
+void int8_kernels(std::vector<const void*>& out);
+
 // The allocation-free contiguous entry point's scratch: its size, and its
 // device address on `device` (looked up once per device; nullptr on failure;
 // call with that device current).
