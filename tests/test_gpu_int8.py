@@ -105,6 +105,16 @@ def test_dense_columns(N, M, K):
     assert np.array_equal(got, want)
 
 
+@pytest.mark.parametrize("M,N,K", [
+    # (the kernels from few rows to many, each with K a multiple of 128 and not)
+    (9, 784, 640), (16, 4096, 528), (30, 2144, 384), (100, 2768, 240), (180, 960, 2480), (306, 2768, 384),
+    (777, 2064, 1040), (1024, 2048, 256), (1128, 7184, 144), (2048, 4096, 128), (2048, 4096, 1024), (3001, 3600, 256),
+    (4096, 4096, 256), (2305, 6672, 272), (2000, 4096, 272)])
+def test_dense_kernels(M, N, K):
+    got, want = run_dense(np.random.default_rng(M + K), M, N, K)
+    assert np.array_equal(got, want)
+
+
 @pytest.mark.parametrize("M,N,K", [(4, 16, 131056), (40, 32, 131056), (300, 272, 131056)])
 def test_largest_sums(M, N, K):
     """Every code -128, as deep as the call allows: the sum is 2^31 - 2^18."""
