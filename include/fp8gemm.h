@@ -629,6 +629,57 @@ fp8g_status grad_clip(const void* const* grads, void* const* outs, const int64_t
                       const int* types, int n, const double* sumsq, float max_norm, float* norm,
                       hipStream_t stream);
 
+/*
+ * adamw_step -- one AdamW step over a list of tensors, with the clipping of
+ * their gradients in it (grad_clip's factor, without a pass of its own; the
+ * gradients are only read).
+ *   f  = min(1, max_norm / (sqrt(*sumsq) + 1e-6)), 1 without sumsq;  g = f grad
+ *   m' = beta1 m + (1 - beta1) g;   v' = beta2 v + (1 - beta2) g^2
+ *   p' = p (1 - lr weight_decay)
+ *        - lr / (1 - beta1^t) m' / (sqrt(v' / (1 - beta2^t)) + eps)
+ * in fp32, p' rounded once to the parameter's type (bf16 and fp16 parameters
+ * lose updates below half their step: keep fp32 ones and let the call write
+ * the 16-bit copies).
+ * If *sumsq is infinite or NaN the step is left out: only norm is written.
+ *
+ * All lists are HOST arrays of n entries, read before the call returns:
+ * params, grads      device pointers, types FP8G_TYPE_*, aligned to their
+ *                    element; params are updated in place.
+ * exp_avgs, exp_avg_sqs  the states m and v, updated in place.
+ *    avg_scales and sq_scales NULL: fp32, 4-byte aligned.
+ *    otherwise 8 bits: exp_avgs holds m and exp_avg_sqs holds sqrt(v) as e4m3
+ *    codes (uint8 [numel]), and the scale arrays one exponent byte (e8m0, 2^(b
+ *    - 127)) for each 128 elements (uint8 [ceil(numel / 128)]): the smallest
+ *    power of two that brings the block's largest value to 448 or below. Codes
+ *    of zeros are a fresh state, whatever the scales. A value is rounded up
+ *    with the probability of the part that is cut off: 16 bits of a hash of
+ *    (seed, t, the tensor's number in the list, element) decide, so that the
+ *    same call gives the same bits. sqrt(v) becomes code 0 only where it is 0.
+ *    A state that is infinite or NaN becomes the NaN code.
+ * copies             NULL, or device pointers (each may be NULL), types
+ *                    copy_types bf16 or fp16, 2-byte aligned: receive p'
+ *                    rounded once.
+ * numels             elements; 0 is left out. No tensor that is written may
+ *                    overlap another of the list.
+ * step, lr           DEVICE int64 [1] and float [1], read when the step runs
+ *                    (a captured graph's next replay takes new values), or
+ *                    NULL: step_value (t >= 1), lr_value. A *step below 1 is
+ *                    taken as 1.
+ * sumsq, norm        DEVICE double [1] (grad_norm_sq's, sums over processes
+ *                    added) or NULL, and DEVICE float [1] or NULL: the norm.
+ * Errors (nothing is launched): FP8G_ERR_SHAPE (negative sizes, step_value < 1,
+ * a beta outside [0, 1), eps negative, a hyperparameter that is not finite,
+ * max_norm not > 0 with sumsq), _NULL_PTR (also norm without sumsq), _ALIGN,
+ * _UNSUPPORTED (unknown types, more than 2^43 elements, 2^38 in 8 bits).
+ */
+fp8g_status adamw_step(void* const* params, const int* param_types, const void* const* grads,
+                       const int* grad_types, void* const* exp_avgs, void* const* exp_avg_sqs,
+                       uint8_t* const* avg_scales, uint8_t* const* sq_scales, void* const* copies,
+                       const int* copy_types, const int64_t* numels, int n, const int64_t* step,
+                       int64_t step_value, const float* lr, double lr_value, double beta1, double beta2,
+                       double eps, double weight_decay, const double* sumsq, float max_norm, float* norm,
+                       uint32_t seed, hipStream_t stream);
+
 /* ---- Products in 8-bit integers ---------------------------------------------
  * The other common 8-bit form of a served layer: whole numbers -127 .. 127
  * with one fp32 scale for each token of the activations and one for each

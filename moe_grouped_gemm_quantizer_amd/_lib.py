@@ -25,7 +25,7 @@ ENTRY_POINTS = ("fp8_quantize", "fp8_quantize_bf16", "fp8_quantize_tensor", "gem
                 "moe_route", "moe_route_workspace_size", "moe_route_backward",
                 "fp8_quantize_transpose", "grouped_gemm_fp8_wgrad", "grad_norm_sq",
                 "grad_norm_sq_workspace_size", "grad_clip",
-                "int8_quantize", "gemm_int8", "grouped_gemm_int8_contiguous",
+                "adamw_step", "int8_quantize", "gemm_int8", "grouped_gemm_int8_contiguous",
                 "grouped_gemm_int8_masked",
                 "fp8g_status_string", "fp8g_abi_version")
 
@@ -34,6 +34,7 @@ _c_int = ctypes.c_int
 _c_vp = ctypes.c_void_p
 _c_sz = ctypes.c_size_t
 _c_f = ctypes.c_float
+_c_d = ctypes.c_double
 
 _SIGS = {
     "fp8_quantize": [_c_vp, _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp],
@@ -75,6 +76,8 @@ _SIGS = {
     "grad_norm_sq": [_c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_sz, _c_vp],
     "grad_norm_sq_workspace_size": [_c_vp, _c_int, ctypes.POINTER(_c_sz)],
     "grad_clip": [_c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_f, _c_vp, _c_vp],
+    "adamw_step": [_c_vp] * 11 + [_c_int, _c_vp, _c_i64, _c_vp, _c_d, _c_d, _c_d, _c_d, _c_d, _c_vp, _c_f,
+                                  _c_vp, ctypes.c_uint32, _c_vp],
     "int8_quantize": [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp],
     "gemm_int8": [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp],
     "grouped_gemm_int8_contiguous": [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_i64, _c_i64,
@@ -646,6 +649,91 @@ def grad_clip(grads, outs, sumsq, max_norm, norm, stream=None):
     nrm = _out(norm, (1,), torch.float32, "norm")
     _check(load().grad_clip(_at(ptrs), _at(optrs), _at(numels), _at(types), len(ptrs), total, max_norm, nrm,
                             _stream(stream)), "grad_clip")
+
+
+class AdamwTensors:
+    """The tensors of an AdamW step (made by adamw_tensors): their pointers,
+    sizes and types as HOST arrays, and the tensors themselves, which keep the
+    memory alive."""
+
+    __slots__ = ("held", "lists", "n", "device")
+
+
+def adamw_tensors(params, grads, exp_avgs, exp_avg_sqs, copies=None, m_scales=None, v_scales=None):
+    """The list of an AdamW step, for adamw_step: made once and used for many
+    steps, as long as the tensors keep their memory (make a new one where a
+    gradient or parameter becomes another tensor).
+
+    params, grads: float32, bfloat16 or float16, contiguous, alike in number and
+    size. States: exp_avgs and exp_avg_sqs float32 of the same sizes, or, with
+    m_scales and v_scales (uint8 [ceil(numel/128)] each), uint8 e4m3 codes of m and
+    sqrt(v) (zeros: a fresh state). copies: bfloat16 or float16 tensors that
+    receive the parameters, or None; single ones may be None."""
+    torch = _torch()
+    eight = m_scales is not None or v_scales is not None
+    if eight and (m_scales is None or v_scales is None):
+        _fail("m_scales and v_scales go together")
+    lists = [list(ts) for ts in (params, grads, exp_avgs, exp_avg_sqs)]
+    n = len(lists[0])
+    lists += [list(ts) if ts is not None else [None] * n for ts in (m_scales, v_scales, copies)]
+    if any(len(ts) != n for ts in lists):
+        _fail("the lists must have as many tensors as params")
+    numels = [p.numel() for p in lists[0]]
+    state = torch.uint8 if eight else torch.float32
+    at = torch._C._cuda_getDevice() if n else -1
+    kinds = (None, None, (state,), (state,), (torch.uint8,), (torch.uint8,), (torch.bfloat16, torch.float16))
+    names = ("params", "grads", "exp_avgs", "exp_avg_sqs", "m_scales", "v_scales", "copies")
+    for ts, kind, what in zip(lists, kinds, names):
+        for t, numel in zip(ts, numels):
+            if t is None:
+                if what == "copies" or not eight and what in ("m_scales", "v_scales"):
+                    continue
+                _fail(f"{what} must not hold None")
+            if t.dtype not in (kind or _TYPES):
+                _fail(f"{what}: {t.dtype} is not among the types allowed")
+            if t.numel() != (-(-numel // 128) if what in ("m_scales", "v_scales") else numel):
+                _fail(f"{what} must match params in size")
+            if not t.is_cuda or not t.is_contiguous() or t.get_device() != at:
+                _fail(f"{what} must be contiguous and on the current device")
+    written = [t.data_ptr() for ts in lists[:1] + lists[2:] for t in ts if t is not None and t.numel()]
+    if len(set(written)) != len(written):
+        _fail("a tensor that the step writes is in the list twice")
+    out = AdamwTensors()
+    # (without the tensors' graphs)
+    out.held = [[None if t is None else t.detach() for t in ts] for ts in lists]
+    ptr = [array.array("Q", [0 if t is None else t.data_ptr() for t in ts]) for ts in lists]
+    typ = [array.array("i", [0 if t is None else _TYPES[t.dtype] for t in lists[i]]) for i in (0, 1, 6)]
+    out.lists = (ptr[0], typ[0], ptr[1], typ[1], ptr[2], ptr[3], ptr[4] if eight else (), ptr[5] if eight else (),
+                 ptr[6] if copies is not None else (), typ[2], array.array("q", numels))
+    out.n = n
+    out.device = at
+    return out
+
+
+def adamw_step(tensors, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, sumsq=None, max_norm=0.0,
+               norm=None, seed=0, stream=None):
+    """One AdamW step over `tensors` (adamw_tensors), in place.
+
+    step: the step's number, from 1 on, and lr: numbers, or device tensors of one
+    element (int64, float32), which a captured graph reads again at each replay.
+    sumsq (float64 device tensor of one element, grad_norm_sq's): the gradients are
+    clipped to max_norm within the step, norm (float32, one element, or None) is
+    written, and a sum that is infinite or NaN leaves the step out. seed: of the
+    8-bit states' rounding."""
+    if tensors.n and tensors.device != _torch()._C._cuda_getDevice():
+        _fail("the tensors are not on the current device")
+    torch = _torch()
+    sp = lp = None
+    if isinstance(step, torch.Tensor):
+        sp, step = _out(step, (1,) if step.dim() else (), torch.int64, "step"), 1
+    if isinstance(lr, torch.Tensor):
+        lp, lr = _out(lr, (1,) if lr.dim() else (), torch.float32, "lr"), 0.0
+    total = None if sumsq is None else _out(sumsq, (1,), torch.float64, "sumsq")
+    nrm = None if norm is None else _out(norm, (1,), torch.float32, "norm")
+    st = load().adamw_step(*map(_at, tensors.lists), tensors.n, sp, step, lp, lr, beta1, beta2, eps, weight_decay,
+                           total, max_norm, nrm, seed & 0xFFFFFFFF, _stream(stream))
+    if st:
+        _check(st, "adamw_step")
 
 
 def _one_device(*ts):

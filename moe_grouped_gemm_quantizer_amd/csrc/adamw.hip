@@ -1,0 +1,475 @@
+// An AdamW step over a list of tensors, with the gradients' clipping in it and the states in
+// 32 bits or in 8.
+//
+//   g  = grad min(1, max_norm / (norm + 1e-6))         (where a sum of squares is given)
+//   m' = b1 m + (1 - b1) g,  v' = b2 v + (1 - b2) g^2
+//   p' = p (1 - lr wd) - lr / (1 - b1^t) m' / (sqrt(v' / (1 - b2^t)) + eps)
+//
+// States in 8 bits: m and r = sqrt(v) (half the range of exponents to hold) as e4m3 codes, 128
+// elements of a tensor to a power-of-two scale, the smallest that brings the block into range.
+// A step moves v by 1 - b2 of its distance from g^2, far less than a code's step, so rounding to
+// the nearest would leave it where it is: a value is rounded up with the probability of the part
+// that is cut off, by 16 bits of a hash of (seed, step, tensor, element). r is never rounded to
+// 0 unless it is 0: m / (r + eps) would then be as large as eps is small.
+//
+// An HBM stream: every tensor is read and written once. The list travels in the kernel's
+// arguments (MAX_T tensors a launch): nothing of it stays on the device or in the library.
+
+#include <math.h>
+#include <vector>
+
+#include "elem.h"
+#include "internal.h"
+
+namespace fp8g {
+namespace {
+
+using namespace elem;
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int THREADS = 256;
+constexpr int MAX_T = 52;
+constexpr int BLOCK = 128;                             // elements of an 8-bit state that share a scale
+constexpr int64_t CHUNK_MIN = 2048, CHUNK_MAX = 8192;  // elements of a chunk, multiples of 2048
+constexpr int64_t MAX_GRID = 2048;                     // eight workgroups per CU
+
+struct Table {
+  void* p[MAX_T];
+  const void* g[MAX_T];
+  void* m[MAX_T];
+  void* v[MAX_T];
+  void* copy[MAX_T];
+  uint8_t* ms[MAX_T];
+  uint8_t* vs[MAX_T];
+  int64_t numel[MAX_T];
+  int end[MAX_T];                                      // chunks of this tensor and those before it
+  int index[MAX_T];                                    // its number in the caller's list
+  uint8_t types[MAX_T];                                // of p + 3 of g
+  uint8_t ctype[MAX_T];
+  int n, chunk;
+};
+
+struct Hyper {
+  const double* sumsq;
+  float* norm;                                         // written by this launch, or null
+  const int64_t* step_at;
+  const float* lr_at;
+  double log1, log2, lr, decay;                        // log b1, log b2
+  float b1, c1, b2, c2, eps, max_norm;                 // c1 = 1 - b1, c2 = 1 - b2
+  int64_t step;
+  uint32_t seed;
+};
+struct Args {
+  Table t;
+  Hyper h;
+};
+static_assert(sizeof(Args) <= 4096, "a kernel's arguments");
+
+// What a step multiplies with, the same in every thread.
+struct Factors {
+  float clip, b1, c1, b2, c2, keep, size, inv, eps;    // keep = 1 - lr wd, size = lr / (1 - b1^t), inv = 1 / sqrt(1 - b2^t)
+  uint32_t key;
+};
+
+// A 32-bit hash: xor-shifts and odd multipliers.
+__device__ __forceinline__ uint32_t mix(uint32_t h) {
+  h = (h ^ (h >> 16)) * 0x7FEB352Du;
+  h = (h ^ (h >> 15)) * 0x846CA68Bu;
+  return h ^ (h >> 16);
+}
+
+// (false: the sum of squares is infinite or NaN, and the step is left out)
+__device__ __forceinline__ bool factors(const Hyper& h, Factors& f) {
+  f.clip = 1.0f;
+  if (h.sumsq) {
+    const double norm = sqrt(*h.sumsq);
+    if (h.norm && blockIdx.x == 0 && threadIdx.x == 0) *h.norm = (float)norm;
+    if (!(norm < __builtin_inf())) return false;
+    const double q = (double)h.max_norm / (norm + 1e-6);
+    f.clip = q >= 1.0 ? 1.0f : (float)q;
+  }
+  const int64_t step = h.step_at ? max(*h.step_at, (int64_t)1) : h.step;
+  const double lr = h.lr_at ? (double)*h.lr_at : h.lr;
+  // (1 - b^t without the cancellation at small t; b = 0 has log b = -inf)
+  f.size = (float)(lr / -expm1((double)step * h.log1));
+  f.inv = (float)(1.0 / sqrt(-expm1((double)step * h.log2)));
+  f.keep = (float)(1.0 - lr * h.decay);
+  f.b1 = h.b1;
+  f.c1 = h.c1;
+  f.b2 = h.b2;
+  f.c2 = h.c2;
+  f.eps = h.eps;
+  f.key = mix(h.seed + mix((uint32_t)step));
+  return true;
+}
+
+// One element. Products and sums of the states are rounded one by one, so that their bits do
+// not depend on which of them the compiler joins.
+struct Moved {
+  float p, m, v, r;
+};
+__device__ __forceinline__ Moved move(float p, float g, float m, float v, const Factors& f) {
+#pragma clang fp contract(off)
+  Moved o;
+  g = g * f.clip;
+  o.m = m * f.b1 + g * f.c1;
+  o.v = v * f.b2 + g * g * f.c2;
+  o.r = __builtin_sqrtf(o.v);
+  o.p = p * f.keep - f.size * o.m * __builtin_amdgcn_rcpf(o.r * f.inv + f.eps);
+  return o;
+}
+
+// N values of type T as fp32: in 16-byte accesses (the address is aligned to what they move),
+// or one by one, `left` of them.
+template <typename T, int N>
+struct Raw {
+  static constexpr int W = N * (int)sizeof(T) < 16 ? N * (int)sizeof(T) / 4 : 4;       // dwords of an access
+  static constexpr int K = N * (int)sizeof(T) / (4 * W);
+  typedef uint32_t Word __attribute__((ext_vector_type(W)));
+  Word w[K];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k] = __builtin_nontemporal_load(reinterpret_cast<const Word*>(p) + k);
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int k = 0; k < K; ++k) __builtin_nontemporal_store(w[k], reinterpret_cast<Word*>(p) + k);
+  }
+  __device__ __forceinline__ void get(float (&x)[N]) const {
+    const Pack<T, N> v = __builtin_bit_cast(Pack<T, N>, w);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = to_f32(v.v[i]);
+  }
+  __device__ __forceinline__ void set(const float (&x)[N]) {
+    Pack<T, N> v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v.v[i] = from_f32<T>(x[i]);
+    __builtin_memcpy(&w, &v, sizeof(w));
+  }
+};
+template <typename T, int N>
+__device__ __forceinline__ void load_few(const T* p, int left, float (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = i < left ? to_f32(p[i]) : 0.0f;
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_few(T* p, int left, const float (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i < left) p[i] = from_f32<T>(x[i]);
+}
+template <int N>
+__device__ __forceinline__ void store_copy(void* c, int64_t at, int type, bool vec, int left, const float (&x)[N]) {
+  const auto put = [&](auto* p) __attribute__((always_inline)) {
+    typedef __remove_reference_t(decltype(*p)) T;
+    if (vec) {
+      Raw<T, N> r;
+      r.set(x);
+      r.store(p + at);
+    } else {
+      store_few<T, N>(p + at, left, x);
+    }
+  };
+  if (type == TYPE_BF16) put((bf16_t*)c);
+  else put((f16_t*)c);
+}
+
+// A chunk with fp32 states: four elements a lane.
+template <typename P, typename G>
+__device__ __forceinline__ void chunk32(const Table& t, int i, int64_t at, int n, const Factors& f) {
+  P* const p = (P*)t.p[i] + at;
+  const G* const g = (const G*)t.g[i] + at;
+  float* const m = (float*)t.m[i] + at;
+  float* const v = (float*)t.v[i] + at;
+  void* const c = t.copy[i];
+  constexpr int N = 4;
+  const bool vec = (((uintptr_t)p % (N * sizeof(P))) | ((uintptr_t)g % (N * sizeof(G))) |
+                    (((uintptr_t)m | (uintptr_t)v) % 16) | ((uintptr_t)c % 8)) == 0;
+#pragma unroll 2
+  for (int e = threadIdx.x * N; e < n; e += THREADS * N) {
+    float xp[N], xg[N], xm[N], xv[N];
+    const int left = n - e;
+    const bool whole = vec && left >= N;
+    if (whole) {
+      Raw<P, N> rp;
+      Raw<G, N> rg;
+      Raw<float, N> rm, rv;
+      rp.load(p + e);
+      rg.load(g + e);
+      rm.load(m + e);
+      rv.load(v + e);
+      rp.get(xp);
+      rg.get(xg);
+      rm.get(xm);
+      rv.get(xv);
+    } else {
+      load_few<P, N>(p + e, left, xp);
+      load_few<G, N>(g + e, left, xg);
+      load_few<float, N>(m + e, left, xm);
+      load_few<float, N>(v + e, left, xv);
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const Moved o = move(xp[k], xg[k], xm[k], xv[k], f);
+      xp[k] = o.p;
+      xm[k] = o.m;
+      xv[k] = o.v;
+    }
+    if (whole) {
+      Raw<P, N> rp;
+      Raw<float, N> rm, rv;
+      rp.set(xp);
+      rm.set(xm);
+      rv.set(xv);
+      rp.store(p + e);
+      rm.store(m + e);
+      rv.store(v + e);
+    } else {
+      store_few<P, N>(p + e, left, xp);
+      store_few<float, N>(m + e, left, xm);
+      store_few<float, N>(v + e, left, xv);
+    }
+    if (c) store_copy<N>(c, at + e, t.ctype[i], whole, left, xp);
+  }
+}
+
+// The exponent of a block's scale: the smallest e with amax <= 448 2^e = 0.875 2^(e + 9), held
+// to -126 and above; 0 for a block of zeros.
+__device__ __forceinline__ int scale_exp(uint32_t amax) {
+  const int e = (int)(amax >> 23) - 135 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return amax == 0u ? 0 : max(e, -126);
+}
+__device__ __forceinline__ float two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// |x| 2^-e (up to 448) as the lower 7 bits of an e4m3 code: 20 bits are cut off after 16 random
+// ones are added above the lowest four. Below 2^-6, where a code's step stays 2^-9, 2^-6 is added
+// first, which gives those values the same step, and taken off the code.
+__device__ __forceinline__ uint32_t code7(float x, float scale, uint32_t cut) {
+#pragma clang fp contract(off)
+  const float z = __builtin_fabsf(x) * scale;
+  const bool small = z < 0x1p-6f;
+  const uint32_t u = __float_as_uint(small ? z + 0x1p-6f : z);
+  return ((u + (cut << 4)) >> 20) - (small ? 968u : 960u);
+}
+
+// A chunk with states in 8 bits: eight elements a lane, 16 lanes a block.
+template <typename P, typename G>
+__device__ __forceinline__ void chunk8(const Table& t, int i, int64_t at, int n, const Factors& f) {
+  P* const p = (P*)t.p[i] + at;
+  const G* const g = (const G*)t.g[i] + at;
+  uint8_t* const m = (uint8_t*)t.m[i] + at;
+  uint8_t* const v = (uint8_t*)t.v[i] + at;
+  uint8_t* const ms = t.ms[i] + at / BLOCK;
+  uint8_t* const vs = t.vs[i] + at / BLOCK;
+  void* const c = t.copy[i];
+  constexpr int N = 8;
+  const bool vec = (((uintptr_t)p | (uintptr_t)g | (uintptr_t)c) % 16 | ((uintptr_t)m | (uintptr_t)v) % 8) == 0;
+  const uint32_t key = mix(f.key + (uint32_t)t.index[i]) + (uint32_t)(at / BLOCK);
+  const int lane = threadIdx.x & 15;
+  // (whole blocks: all 16 lanes of one take part in its maxima)
+  for (int e = threadIdx.x * N; e - lane * N < n; e += THREADS * N) {
+    float xp[N], xg[N];
+    uint32_t cm[2] = {0, 0}, cv[2] = {0, 0};
+    const int left = n - e, blk = e / BLOCK;
+    const bool whole = vec && left >= N;
+    const uint32_t sm = ms[blk], sv = vs[blk];
+    if (whole) {
+      Raw<P, N> rp;
+      Raw<G, N> rg;
+      Raw<uint32_t, 2> rm, rv;
+      rp.load(p + e);
+      rg.load(g + e);
+      rm.load(reinterpret_cast<const uint32_t*>(m + e));
+      rv.load(reinterpret_cast<const uint32_t*>(v + e));
+      rp.get(xp);
+      rg.get(xg);
+      cm[0] = rm.w[0][0];
+      cm[1] = rm.w[0][1];
+      cv[0] = rv.w[0][0];
+      cv[1] = rv.w[0][1];
+    } else {
+      load_few<P, N>(p + e, left, xp);
+      load_few<G, N>(g + e, left, xg);
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (k < left) {
+          cm[k / 4] |= (uint32_t)m[e + k] << (8 * (k % 4));
+          cv[k / 4] |= (uint32_t)v[e + k] << (8 * (k % 4));
+        }
+    }
+    const float fm = __uint_as_float(sm << 23), fv = __uint_as_float(sv << 23);
+    float xm[N], xr[N];
+    uint32_t am = 0, ar = 0;
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+      const auto dm = (k & 2) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)cm[k / 4], true)
+                              : __builtin_amdgcn_cvt_pk_f32_fp8((int)cm[k / 4], false);
+      const auto dv = (k & 2) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)cv[k / 4], true)
+                              : __builtin_amdgcn_cvt_pk_f32_fp8((int)cv[k / 4], false);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float r = dv[h] * fv;
+        const Moved o = move(xp[k + h], xg[k + h], dm[h] * fm, r * r, f);
+        xp[k + h] = o.p;
+        xm[k + h] = o.m;
+        xr[k + h] = o.r;
+        const uint32_t um = __float_as_uint(o.m) & 0x7FFFFFFFu, ur = __float_as_uint(o.r);
+        am = max(am, um < 0x7F800000u ? um : 0u);
+        ar = max(ar, ur < 0x7F800000u ? ur : 0u);      // (r is not negative; NaN has a large pattern)
+      }
+    }
+    const auto umax = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+    const int em = scale_exp(reduce_u32<16>(am, umax)), er = scale_exp(reduce_u32<16>(ar, umax));
+    const uint32_t base = mix(key + (uint32_t)blk) + (uint32_t)(lane * N) * 0x9E3779B9u;
+    const float im = two(-em), ir = two(-er);
+    uint32_t om[2] = {0, 0}, ov[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const uint32_t cut = mix(base + (uint32_t)k * 0x9E3779B9u);
+      const uint32_t um = __float_as_uint(xm[k]), ur = __float_as_uint(xr[k]);
+      uint32_t a = code7(xm[k], im, cut & 0xFFFFu);
+      uint32_t b = code7(xr[k], ir, cut >> 16);
+      a = (um & 0x7FFFFFFFu) < 0x7F800000u ? a : 0x7Fu;
+      b = ur < 0x7F800000u ? max(b, xr[k] > 0.0f ? 1u : 0u) : 0x7Fu;
+      om[k / 4] |= (a | (um >> 24 & 0x80u)) << (8 * (k % 4));
+      ov[k / 4] |= b << (8 * (k % 4));
+    }
+    if (whole) {
+      Raw<P, N> rp;
+      Raw<uint32_t, 2> rm, rv;
+      rp.set(xp);
+      rm.w[0][0] = om[0];
+      rm.w[0][1] = om[1];
+      rv.w[0][0] = ov[0];
+      rv.w[0][1] = ov[1];
+      rp.store(p + e);
+      rm.store(reinterpret_cast<uint32_t*>(m + e));
+      rv.store(reinterpret_cast<uint32_t*>(v + e));
+    } else {
+      store_few<P, N>(p + e, left, xp);
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (k < left) {
+          m[e + k] = (uint8_t)(om[k / 4] >> (8 * (k % 4)));
+          v[e + k] = (uint8_t)(ov[k / 4] >> (8 * (k % 4)));
+        }
+    }
+    if (c) store_copy<N>(c, at + e, t.ctype[i], whole, left, xp);
+    if (lane == 0) {
+      ms[blk] = (uint8_t)(em + 127);
+      vs[blk] = (uint8_t)(er + 127);
+    }
+  }
+}
+
+// (n == 0: one workgroup writes the norm)
+template <int BITS>
+__global__ void __launch_bounds__(THREADS)
+adamw_kernel(Args a) {
+  const Table& t = a.t;
+  Factors f;
+  if (!factors(a.h, f)) return;
+  const int chunks = t.n ? t.end[t.n - 1] : 0;
+  for (int c = (int)blockIdx.x; c < chunks; c += (int)gridDim.x) {
+    int lo = 0, hi = t.n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (c < t.end[mid]) hi = mid;
+      else lo = mid + 1;
+    }
+    const int64_t at = (int64_t)(c - (lo ? t.end[lo - 1] : 0)) * t.chunk;
+    const int64_t left = t.numel[lo] - at;
+    const int n = (int)(left < t.chunk ? left : t.chunk);
+    const auto run = [&](auto p, auto g) __attribute__((always_inline)) {
+      if constexpr (BITS == 8) chunk8<decltype(p), decltype(g)>(t, lo, at, n, f);
+      else chunk32<decltype(p), decltype(g)>(t, lo, at, n, f);
+    };
+    switch (t.types[lo]) {
+      case 0: run(0.0f, 0.0f); break;
+      case 1: run(bf16_t(), 0.0f); break;
+      case 2: run(f16_t(), 0.0f); break;
+      case 3: run(0.0f, bf16_t()); break;
+      case 4: run(bf16_t(), bf16_t()); break;
+      case 5: run(f16_t(), bf16_t()); break;
+      case 6: run(0.0f, f16_t()); break;
+      case 7: run(bf16_t(), f16_t()); break;
+      default: run(f16_t(), f16_t()); break;
+    }
+  }
+}
+
+// Chunks small enough for a short list to reach all CUs.
+int chunk_for(const AdamwCall& c) {
+  int64_t total = 0;
+  for (int i = 0; i < c.n && total < MAX_GRID * CHUNK_MAX; ++i) total += c.numels[i];
+  return (int)(total < MAX_GRID * CHUNK_MAX ? CHUNK_MIN : CHUNK_MAX);
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamwCall& c, hipStream_t stream) {
+  Args a;
+  Table& t = a.t;
+  Hyper& h = a.h;
+  h.sumsq = c.sumsq;
+  h.norm = c.norm;
+  h.step_at = c.step_at;
+  h.lr_at = c.lr_at;
+  h.log1 = log(c.beta1);
+  h.log2 = log(c.beta2);
+  h.lr = c.lr;
+  h.decay = c.weight_decay;
+  h.b1 = (float)c.beta1;
+  h.c1 = (float)(1.0 - c.beta1);
+  h.b2 = (float)c.beta2;
+  h.c2 = (float)(1.0 - c.beta2);
+  h.eps = (float)c.eps;
+  h.max_norm = c.max_norm;
+  h.step = c.step;
+  h.seed = c.seed;
+  t.chunk = chunk_for(c);
+  const auto kernel = c.ms ? adamw_kernel<8> : adamw_kernel<32>;
+  int i = 0;
+  bool first = true;
+  for (;;) {
+    t.n = 0;
+    int64_t chunks = 0;
+    for (; i < c.n && t.n < MAX_T; ++i) {
+      if (c.numels[i] == 0) continue;
+      const int64_t k = (c.numels[i] + t.chunk - 1) / t.chunk;
+      if (chunks + k > 0x7FFFFFFF) break;              // (each tensor fits by itself: checked before)
+      chunks += k;
+      t.p[t.n] = c.params[i];
+      t.g[t.n] = c.grads[i];
+      t.m[t.n] = c.m[i];
+      t.v[t.n] = c.v[i];
+      t.copy[t.n] = c.copies ? c.copies[i] : nullptr;
+      t.ctype[t.n] = (uint8_t)(c.copies ? c.copy_types[i] : 0);
+      t.ms[t.n] = c.ms ? c.ms[i] : nullptr;
+      t.vs[t.n] = c.vs ? c.vs[i] : nullptr;
+      t.numel[t.n] = c.numels[i];
+      t.types[t.n] = (uint8_t)(c.param_types[i] + 3 * c.grad_types[i]);
+      t.index[t.n] = i;
+      t.end[t.n] = (int)chunks;
+      ++t.n;
+    }
+    // (nothing to do, but a norm to write)
+    if (chunks == 0 && !(first && c.norm)) break;
+    const int64_t grid = chunks < 1 ? 1 : (chunks < MAX_GRID ? chunks : MAX_GRID);
+    kernel<<<dim3((unsigned)grid), dim3(THREADS), 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    h.norm = nullptr;
+    first = false;
+    if (chunks == 0) break;
+  }
+  return hipSuccess;
+}
+
+void adamw_kernels(std::vector<const void*>& out) {
+  out.push_back((const void*)adamw_kernel<8>);
+  out.push_back((const void*)adamw_kernel<32>);
+}
+
+}  // namespace fp8g

@@ -100,6 +100,7 @@ fp8g_status fp8g_warmup(void) {
   wgrad_kernels(kernels);
   clip_kernels(kernels);
   int8_kernels(kernels);
+  adamw_kernels(kernels);
   for (const void* k : kernels) {
     hipFuncAttributes attr;
     if (hipFuncGetAttributes(&attr, k) != hipSuccess) {

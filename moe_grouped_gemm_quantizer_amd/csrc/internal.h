@@ -171,6 +171,32 @@ struct Int8Args {
 hipError_t launch_int8(const Int8Args& args, const DeviceInfo& dev, int expected_m, hipStream_t stream);
 void int8_kernels(std::vector<const void*>& out);
 
+// The AdamW step (adamw.hip); arguments as for adamw_step.
+struct AdamwCall {
+  void* const* params;
+  const int* param_types;
+  const void* const* grads;
+  const int* grad_types;
+  void* const* m;
+  void* const* v;
+  uint8_t* const* ms;      // null: states in 32 bits
+  uint8_t* const* vs;
+  void* const* copies;     // null: none
+  const int* copy_types;
+  const int64_t* numels;
+  int n;
+  const int64_t* step_at;
+  int64_t step;
+  const float* lr_at;
+  double lr, beta1, beta2, eps, weight_decay;
+  const double* sumsq;
+  float max_norm;
+  float* norm;
+  uint32_t seed;
+};
+hipError_t launch_adamw(const AdamwCall& c, hipStream_t stream);
+void adamw_kernels(std::vector<const void*>& out);
+
 // The allocation-free contiguous entry point's scratch: its size, and its
 // device address on `device` (looked up once per device; nullptr on failure;
 // call with that device current).

@@ -41,6 +41,35 @@ fp8g_status list_ok(const void* const* grads, const int64_t* numels, const int* 
   return FP8G_OK;
 }
 
+constexpr int64_t kNumel32Max = int64_t(1) << 43;   // (chunks of 8192 elements and
+constexpr int64_t kNumel8Max = int64_t(1) << 38;    // blocks of 128 are counted in 31 bits)
+
+fp8g_status adamw_list_ok(const AdamwCall& c) {
+  const bool eight = c.ms || c.vs;
+  if (c.n < 0) return FP8G_ERR_SHAPE;
+  if (c.n == 0) return FP8G_OK;
+  if (!c.params || !c.param_types || !c.grads || !c.grad_types || !c.m || !c.v || !c.numels ||
+      (eight && (!c.ms || !c.vs)) || (c.copies && !c.copy_types))
+    return FP8G_ERR_NULL_PTR;
+  const uintptr_t state = eight ? 1 : 4;
+  for (int i = 0; i < c.n; ++i) {
+    if (c.numels[i] < 0) return FP8G_ERR_SHAPE;
+    if (!type_ok(c.param_types[i]) || !type_ok(c.grad_types[i]) ||
+        c.numels[i] > (eight ? kNumel8Max : kNumel32Max))
+      return FP8G_ERR_UNSUPPORTED;
+    void* const copy = c.copies ? c.copies[i] : nullptr;
+    if (copy && c.copy_types[i] != FP8G_TYPE_BF16 && c.copy_types[i] != FP8G_TYPE_F16)
+      return FP8G_ERR_UNSUPPORTED;
+    if (c.numels[i] == 0) continue;
+    if (!c.params[i] || !c.grads[i] || !c.m[i] || !c.v[i] || (eight && (!c.ms[i] || !c.vs[i])))
+      return FP8G_ERR_NULL_PTR;
+    if (!aligned(c.params[i], type_size(c.param_types[i])) || !aligned(c.grads[i], type_size(c.grad_types[i])) ||
+        !aligned(c.m[i], state) || !aligned(c.v[i], state) || !aligned(copy, 2))
+      return FP8G_ERR_ALIGN;
+  }
+  return FP8G_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -229,6 +258,51 @@ fp8g_status grad_clip(const void* const* grads, void* const* outs, const int64_t
   if (current_device_info(&dev) != 0) return FP8G_ERR_DEVICE;
   return launched(
       launch_grad_clip(grads, outs, numels, types, n, sumsq, max_norm, norm, stream));
+}
+
+fp8g_status adamw_step(void* const* params, const int* param_types, const void* const* grads,
+                       const int* grad_types, void* const* exp_avgs, void* const* exp_avg_sqs,
+                       uint8_t* const* avg_scales, uint8_t* const* sq_scales, void* const* copies,
+                       const int* copy_types, const int64_t* numels, int n, const int64_t* step,
+                       int64_t step_value, const float* lr, double lr_value, double beta1, double beta2,
+                       double eps, double weight_decay, const double* sumsq, float max_norm, float* norm,
+                       uint32_t seed, hipStream_t stream) {
+  AdamwCall c;
+  c.params = params;
+  c.param_types = param_types;
+  c.grads = grads;
+  c.grad_types = grad_types;
+  c.m = exp_avgs;
+  c.v = exp_avg_sqs;
+  c.ms = avg_scales;
+  c.vs = sq_scales;
+  c.copies = copies;
+  c.copy_types = copy_types;
+  c.numels = numels;
+  c.n = n;
+  c.step_at = step;
+  c.step = step_value;
+  c.lr_at = lr;
+  c.lr = lr_value;
+  c.beta1 = beta1;
+  c.beta2 = beta2;
+  c.eps = eps;
+  c.weight_decay = weight_decay;
+  c.sumsq = sumsq;
+  c.max_norm = max_norm;
+  c.norm = norm;
+  c.seed = seed;
+  const fp8g_status s = adamw_list_ok(c);
+  if (s != FP8G_OK) return s;
+  if ((!step && step_value < 1) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) ||
+      !(eps >= 0.0) || !isfinite(eps) || !isfinite(weight_decay) || (!lr && !isfinite(lr_value)))
+    return FP8G_ERR_SHAPE;
+  if (sumsq && !(max_norm > 0.0f)) return FP8G_ERR_SHAPE;
+  if (norm && !sumsq) return FP8G_ERR_NULL_PTR;
+  if (!aligned(step, 8) || !aligned(lr, 4) || !aligned(sumsq, 8) || !aligned(norm, 4)) return FP8G_ERR_ALIGN;
+  DeviceInfo dev;
+  if (current_device_info(&dev) != 0) return FP8G_ERR_DEVICE;
+  return launched(launch_adamw(c, stream));
 }
 
 }  // extern "C"
