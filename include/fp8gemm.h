@@ -670,7 +670,7 @@ fp8g_status grad_clip(const void* const* grads, void* const* outs, const int64_t
  * Errors (nothing is launched): FP8G_ERR_SHAPE (negative sizes, step_value < 1,
  * a beta outside [0, 1), eps negative, a hyperparameter that is not finite,
  * max_norm not > 0 with sumsq), _NULL_PTR (also norm without sumsq), _ALIGN,
- * _UNSUPPORTED (unknown types, more than 2^43 elements, 2^38 in 8 bits).
+ * _UNSUPPORTED (unknown types, a tensor of more than 2^35 - 2048 elements).
  */
 fp8g_status adamw_step(void* const* params, const int* param_types, const void* const* grads,
                        const int* grad_types, void* const* exp_avgs, void* const* exp_avg_sqs,

@@ -653,8 +653,8 @@ def grad_clip(grads, outs, sumsq, max_norm, norm, stream=None):
 
 class AdamwTensors:
     """The tensors of an AdamW step (made by adamw_tensors): their pointers,
-    sizes and types as HOST arrays, and the tensors themselves, which keep the
-    memory alive."""
+    sizes and types as HOST arrays, and their storages, which keeps the memory
+    alive."""
 
     __slots__ = ("held", "lists", "n", "device")
 
@@ -681,27 +681,32 @@ def adamw_tensors(params, grads, exp_avgs, exp_avg_sqs, copies=None, m_scales=No
     numels = [p.numel() for p in lists[0]]
     state = torch.uint8 if eight else torch.float32
     at = torch._C._cuda_getDevice() if n else -1
-    kinds = (None, None, (state,), (state,), (torch.uint8,), (torch.uint8,), (torch.bfloat16, torch.float16))
-    names = ("params", "grads", "exp_avgs", "exp_avg_sqs", "m_scales", "v_scales", "copies")
-    for ts, kind, what in zip(lists, kinds, names):
-        for t, numel in zip(ts, numels):
-            if t is None:
-                if what == "copies" or not eight and what in ("m_scales", "v_scales"):
-                    continue
+    blocks = [(k + 127) // 128 for k in numels]
+    cls = torch.Tensor
+    # (hundreds of tensors: every attribute is read in a loop of the interpreter's own)
+    for ts, kinds, sizes, what in ((lists[0], _TYPES, numels, "params"), (lists[1], _TYPES, numels, "grads"),
+                                   (lists[2], (state,), numels, "exp_avgs"), (lists[3], (state,), numels, "exp_avg_sqs"),
+                                   (lists[4], (torch.uint8,), blocks, "m_scales"),
+                                   (lists[5], (torch.uint8,), blocks, "v_scales"),
+                                   (lists[6], (torch.bfloat16, torch.float16), numels, "copies")):
+        if any(t is None for t in ts):
+            if what == "copies" or not eight and what in ("m_scales", "v_scales"):
+                ts, sizes = [t for t in ts if t is not None], [k for t, k in zip(ts, sizes) if t is not None]
+            else:
                 _fail(f"{what} must not hold None")
-            if t.dtype not in (kind or _TYPES):
-                _fail(f"{what}: {t.dtype} is not among the types allowed")
-            if t.numel() != (-(-numel // 128) if what in ("m_scales", "v_scales") else numel):
-                _fail(f"{what} must match params in size")
-            if not t.is_cuda or not t.is_contiguous() or t.get_device() != at:
-                _fail(f"{what} must be contiguous and on the current device")
-    written = [t.data_ptr() for ts in lists[:1] + lists[2:] for t in ts if t is not None and t.numel()]
+        if not set(map(operator.attrgetter("dtype"), ts)) <= set(kinds):
+            _fail(f"{what} must be of {list(kinds)}")
+        if list(map(cls.numel, ts)) != sizes:
+            _fail(f"{what} must match params in size" + (" (a byte for each 128 elements)" if sizes is blocks else ""))
+        if not (all(map(cls.is_contiguous, ts)) and set(map(cls.get_device, ts)) <= {at}):
+            _fail(f"{what} must be contiguous and on the current device")
+    ptr = [array.array("Q", [0 if t is None else t.data_ptr() for t in ts]) for ts in lists]
+    written = [p for ps in ptr[:1] + ptr[2:] for p in ps if p]
     if len(set(written)) != len(written):
         _fail("a tensor that the step writes is in the list twice")
     out = AdamwTensors()
-    # (without the tensors' graphs)
-    out.held = [[None if t is None else t.detach() for t in ts] for ts in lists]
-    ptr = [array.array("Q", [0 if t is None else t.data_ptr() for t in ts]) for ts in lists]
+    # (the memory, whatever becomes of the tensors)
+    out.held = [[t.untyped_storage() for t in ts if t is not None] for ts in lists]
     typ = [array.array("i", [0 if t is None else _TYPES[t.dtype] for t in lists[i]]) for i in (0, 1, 6)]
     out.lists = (ptr[0], typ[0], ptr[1], typ[1], ptr[2], ptr[3], ptr[4] if eight else (), ptr[5] if eight else (),
                  ptr[6] if copies is not None else (), typ[2], array.array("q", numels))

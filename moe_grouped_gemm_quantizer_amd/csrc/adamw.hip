@@ -32,7 +32,8 @@ constexpr int THREADS = 256;
 constexpr int MAX_T = 52;
 constexpr int BLOCK = 128;                             // elements of an 8-bit state that share a scale
 constexpr int64_t CHUNK_MIN = 2048, CHUNK_MAX = 8192;  // elements of a chunk, multiples of 2048
-constexpr int64_t MAX_GRID = 2048;                     // eight workgroups per CU
+constexpr int64_t LONG = int64_t(1) << 24;             // elements of a list that takes large chunks
+constexpr int64_t CHUNKS = (1 << 24) - 1;              // of a launch: fewer than 2^32 threads
 
 struct Table {
   void* p[MAX_T];
@@ -58,7 +59,8 @@ struct Hyper {
   double log1, log2, lr, decay;                        // log b1, log b2
   float b1, c1, b2, c2, eps, max_norm;                 // c1 = 1 - b1, c2 = 1 - b2
   int64_t step;
-  uint32_t seed;
+  uint32_t seed, key;
+  float size, inv, keep;                               // Factors', where the host knows step and lr
 };
 struct Args {
   Table t;
@@ -73,10 +75,19 @@ struct Factors {
 };
 
 // A 32-bit hash: xor-shifts and odd multipliers.
-__device__ __forceinline__ uint32_t mix(uint32_t h) {
+__host__ __device__ __forceinline__ uint32_t mix(uint32_t h) {
   h = (h ^ (h >> 16)) * 0x7FEB352Du;
   h = (h ^ (h >> 15)) * 0x846CA68Bu;
   return h ^ (h >> 16);
+}
+
+// (1 - b^t without the cancellation at small t; b = 0 has log b = -inf)
+template <typename O>
+__host__ __device__ __forceinline__ void of_step(const Hyper& h, int64_t step, double lr, O& o) {
+  o.size = (float)(lr / -expm1((double)step * h.log1));
+  o.inv = (float)(1.0 / sqrt(-expm1((double)step * h.log2)));
+  o.keep = (float)(1.0 - lr * h.decay);
+  o.key = mix(h.seed + mix((uint32_t)step));
 }
 
 // (false: the sum of squares is infinite or NaN, and the step is left out)
@@ -89,35 +100,43 @@ __device__ __forceinline__ bool factors(const Hyper& h, Factors& f) {
     const double q = (double)h.max_norm / (norm + 1e-6);
     f.clip = q >= 1.0 ? 1.0f : (float)q;
   }
-  const int64_t step = h.step_at ? max(*h.step_at, (int64_t)1) : h.step;
-  const double lr = h.lr_at ? (double)*h.lr_at : h.lr;
-  // (1 - b^t without the cancellation at small t; b = 0 has log b = -inf)
-  f.size = (float)(lr / -expm1((double)step * h.log1));
-  f.inv = (float)(1.0 / sqrt(-expm1((double)step * h.log2)));
-  f.keep = (float)(1.0 - lr * h.decay);
+  if (h.step_at || h.lr_at) {
+    of_step(h, h.step_at ? max(*h.step_at, (int64_t)1) : h.step, h.lr_at ? (double)*h.lr_at : h.lr, f);
+  } else {
+    f.size = h.size;
+    f.inv = h.inv;
+    f.keep = h.keep;
+    f.key = h.key;
+  }
   f.b1 = h.b1;
   f.c1 = h.c1;
   f.b2 = h.b2;
   f.c2 = h.c2;
   f.eps = h.eps;
-  f.key = mix(h.seed + mix((uint32_t)step));
   return true;
 }
 
-// One element. Products and sums of the states are rounded one by one, so that their bits do
-// not depend on which of them the compiler joins.
-struct Moved {
-  float p, m, v, r;
-};
-__device__ __forceinline__ Moved move(float p, float g, float m, float v, const Factors& f) {
+// One element's states. Products and sums are rounded one by one, so that their bits do not
+// depend on which of them the compiler joins.
+__device__ __forceinline__ void move(float g, float& m, float& v, const Factors& f) {
 #pragma clang fp contract(off)
-  Moved o;
   g = g * f.clip;
-  o.m = m * f.b1 + g * f.c1;
-  o.v = v * f.b2 + g * g * f.c2;
-  o.r = __builtin_sqrtf(o.v);
-  o.p = p * f.keep - f.size * o.m * __builtin_amdgcn_rcpf(o.r * f.inv + f.eps);
-  return o;
+  m = m * f.b1 + g * f.c1;
+  v = v * f.b2 + g * g * f.c2;
+}
+// (the reciprocal within one ulp)
+__device__ __forceinline__ float moved(float p, float m, float r, const Factors& f) {
+#pragma clang fp contract(off)
+  return p * f.keep - f.size * m * __builtin_amdgcn_rcpf(r * f.inv + f.eps);
+}
+
+// The square root, correctly rounded for every x from ROOT_MIN to below ROOT_END (compared on
+// all of them): five instructions for the fourteen that the whole range takes.
+constexpr float ROOT_MIN = 0x1p-96f, ROOT_END = 0x1p126f;
+__device__ __forceinline__ float root(float x) {
+#pragma clang fp contract(off)
+  const float q = __builtin_amdgcn_rsqf(x), s = x * q;
+  return __builtin_fmaf(__builtin_fmaf(-s, s, x), 0.5f * q, s);
 }
 
 // N values of type T as fp32: in 16-byte accesses (the address is aligned to what they move),
@@ -211,10 +230,8 @@ __device__ __forceinline__ void chunk32(const Table& t, int i, int64_t at, int n
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const Moved o = move(xp[k], xg[k], xm[k], xv[k], f);
-      xp[k] = o.p;
-      xm[k] = o.m;
-      xv[k] = o.v;
+      move(xg[k], xm[k], xv[k], f);
+      xp[k] = moved(xp[k], xm[k], __builtin_amdgcn_sqrtf(xv[k]), f);
     }
     if (whole) {
       Raw<P, N> rp;
@@ -243,14 +260,14 @@ __device__ __forceinline__ int scale_exp(uint32_t amax) {
 __device__ __forceinline__ float two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // |x| 2^-e (up to 448) as the lower 7 bits of an e4m3 code: 20 bits are cut off after 16 random
-// ones are added above the lowest four. Below 2^-6, where a code's step stays 2^-9, 2^-6 is added
-// first, which gives those values the same step, and taken off the code.
+// ones are added above the lowest four (`cut`: already there). Below 2^-6, where a code's step
+// stays 2^-9, 2^-6 is added first, which gives those values the same step, and taken off the code.
 __device__ __forceinline__ uint32_t code7(float x, float scale, uint32_t cut) {
 #pragma clang fp contract(off)
   const float z = __builtin_fabsf(x) * scale;
   const bool small = z < 0x1p-6f;
-  const uint32_t u = __float_as_uint(small ? z + 0x1p-6f : z);
-  return ((u + (cut << 4)) >> 20) - (small ? 968u : 960u);
+  const uint32_t u = __float_as_uint(z + (small ? 0x1p-6f : 0.0f));
+  return (u + cut - ((small ? 968u : 960u) << 20)) >> 20;
 }
 
 // A chunk with states in 8 bits: eight elements a lane, 16 lanes a block.
@@ -300,7 +317,6 @@ __device__ __forceinline__ void chunk8(const Table& t, int i, int64_t at, int n,
     }
     const float fm = __uint_as_float(sm << 23), fv = __uint_as_float(sv << 23);
     float xm[N], xr[N];
-    uint32_t am = 0, ar = 0;
 #pragma unroll
     for (int k = 0; k < N; k += 2) {
       const auto dm = (k & 2) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)cm[k / 4], true)
@@ -310,17 +326,50 @@ __device__ __forceinline__ void chunk8(const Table& t, int i, int64_t at, int n,
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float r = dv[h] * fv;
-        const Moved o = move(xp[k + h], xg[k + h], dm[h] * fm, r * r, f);
-        xp[k + h] = o.p;
-        xm[k + h] = o.m;
-        xr[k + h] = o.r;
-        const uint32_t um = __float_as_uint(o.m) & 0x7FFFFFFFu, ur = __float_as_uint(o.r);
-        am = max(am, um < 0x7F800000u ? um : 0u);
-        ar = max(ar, ur < 0x7F800000u ? ur : 0u);      // (r is not negative; NaN has a large pattern)
+        xm[k + h] = dm[h] * fm;
+        xr[k + h] = r * r;
+        move(xg[k + h], xm[k + h], xr[k + h], f);
       }
     }
+    float lo = xr[0], hi = xr[0];
+#pragma unroll
+    for (int k = 1; k < N; ++k) {
+      lo = __builtin_fminf(lo, xr[k]);
+      hi = __builtin_fmaxf(hi, xr[k]);
+    }
+    // (a NaN among them is dropped here, and root gives NaN for it as well)
+    if (lo >= ROOT_MIN && hi < ROOT_END) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) xr[k] = root(xr[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k) xr[k] = __builtin_sqrtf(xr[k]);
+    }
+    // (r is not negative, so that the patterns of both are in the values' order, infinities
+    // and NaN above them)
+    uint32_t am = 0, ar = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      xp[k] = moved(xp[k], xm[k], xr[k], f);
+      am = max(am, __float_as_uint(xm[k]) << 1);
+      ar = max(ar, __float_as_uint(xr[k]));
+    }
     const auto umax = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
-    const int em = scale_exp(reduce_u32<16>(am, umax)), er = scale_exp(reduce_u32<16>(ar, umax));
+    am = reduce_u32<16>(am, umax) >> 1;
+    ar = reduce_u32<16>(ar, umax);
+    const bool odd = am >= 0x7F800000u || ar >= 0x7F800000u;         // (the same in a block's lanes)
+    if (odd) {
+      am = ar = 0;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const uint32_t um = __float_as_uint(xm[k]) & 0x7FFFFFFFu, ur = __float_as_uint(xr[k]);
+        am = max(am, um < 0x7F800000u ? um : 0u);
+        ar = max(ar, ur < 0x7F800000u ? ur : 0u);
+      }
+      am = reduce_u32<16>(am, umax);
+      ar = reduce_u32<16>(ar, umax);
+    }
+    const int em = scale_exp(am), er = scale_exp(ar);
     const uint32_t base = mix(key + (uint32_t)blk) + (uint32_t)(lane * N) * 0x9E3779B9u;
     const float im = two(-em), ir = two(-er);
     uint32_t om[2] = {0, 0}, ov[2] = {0, 0};
@@ -328,10 +377,12 @@ __device__ __forceinline__ void chunk8(const Table& t, int i, int64_t at, int n,
     for (int k = 0; k < N; ++k) {
       const uint32_t cut = mix(base + (uint32_t)k * 0x9E3779B9u);
       const uint32_t um = __float_as_uint(xm[k]), ur = __float_as_uint(xr[k]);
-      uint32_t a = code7(xm[k], im, cut & 0xFFFFu);
-      uint32_t b = code7(xr[k], ir, cut >> 16);
-      a = (um & 0x7FFFFFFFu) < 0x7F800000u ? a : 0x7Fu;
-      b = ur < 0x7F800000u ? max(b, xr[k] > 0.0f ? 1u : 0u) : 0x7Fu;
+      uint32_t a = code7(xm[k], im, (cut & 0xFFFFu) << 4);
+      uint32_t b = max(code7(xr[k], ir, (cut >> 12) & 0xFFFF0u), min(ur, 1u));
+      if (odd) {
+        a = (um & 0x7FFFFFFFu) < 0x7F800000u ? a : 0x7Fu;
+        b = ur < 0x7F800000u ? b : 0x7Fu;
+      }
       om[k / 4] |= (a | (um >> 24 & 0x80u)) << (8 * (k % 4));
       ov[k / 4] |= b << (8 * (k % 4));
     }
@@ -363,47 +414,54 @@ __device__ __forceinline__ void chunk8(const Table& t, int i, int64_t at, int n,
   }
 }
 
-// (n == 0: one workgroup writes the norm)
+// A workgroup a chunk (n == 0: one writes the norm).
 template <int BITS>
 __global__ void __launch_bounds__(THREADS)
 adamw_kernel(Args a) {
   const Table& t = a.t;
   Factors f;
   if (!factors(a.h, f)) return;
-  const int chunks = t.n ? t.end[t.n - 1] : 0;
-  for (int c = (int)blockIdx.x; c < chunks; c += (int)gridDim.x) {
-    int lo = 0, hi = t.n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (c < t.end[mid]) hi = mid;
-      else lo = mid + 1;
-    }
-    const int64_t at = (int64_t)(c - (lo ? t.end[lo - 1] : 0)) * t.chunk;
-    const int64_t left = t.numel[lo] - at;
-    const int n = (int)(left < t.chunk ? left : t.chunk);
-    const auto run = [&](auto p, auto g) __attribute__((always_inline)) {
-      if constexpr (BITS == 8) chunk8<decltype(p), decltype(g)>(t, lo, at, n, f);
-      else chunk32<decltype(p), decltype(g)>(t, lo, at, n, f);
-    };
-    switch (t.types[lo]) {
-      case 0: run(0.0f, 0.0f); break;
-      case 1: run(bf16_t(), 0.0f); break;
-      case 2: run(f16_t(), 0.0f); break;
-      case 3: run(0.0f, bf16_t()); break;
-      case 4: run(bf16_t(), bf16_t()); break;
-      case 5: run(f16_t(), bf16_t()); break;
-      case 6: run(0.0f, f16_t()); break;
-      case 7: run(bf16_t(), f16_t()); break;
-      default: run(f16_t(), f16_t()); break;
-    }
+  const int c = (int)blockIdx.x;
+  if (t.n == 0) return;
+  int lo = 0, hi = t.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (c < t.end[mid]) hi = mid;
+    else lo = mid + 1;
+  }
+  const int64_t at = (int64_t)(c - (lo ? t.end[lo - 1] : 0)) * t.chunk;
+  const int64_t left = t.numel[lo] - at;
+  const int n = (int)(left < t.chunk ? left : t.chunk);
+  const auto run = [&](auto p, auto g) __attribute__((always_inline)) {
+    if constexpr (BITS == 8) chunk8<decltype(p), decltype(g)>(t, lo, at, n, f);
+    else chunk32<decltype(p), decltype(g)>(t, lo, at, n, f);
+  };
+  switch (t.types[lo]) {
+    case 0: run(0.0f, 0.0f); break;
+    case 1: run(bf16_t(), 0.0f); break;
+    case 2: run(f16_t(), 0.0f); break;
+    case 3: run(0.0f, bf16_t()); break;
+    case 4: run(bf16_t(), bf16_t()); break;
+    case 5: run(f16_t(), bf16_t()); break;
+    case 6: run(0.0f, f16_t()); break;
+    case 7: run(bf16_t(), f16_t()); break;
+    default: run(f16_t(), f16_t()); break;
   }
 }
 
-// Chunks small enough for a short list to reach all CUs.
+// A list's chunk. Small ones where HBM is the bound: they reach all CUs and end evenly (2048 /
+// 8192 elements: 300 tensors of 50M, fp32 parameters, fp32 states 266 / 295 us, 8-bit states 189 /
+// 207; 8 x 29M 8-bit 690 / 734; 3M elements 15.2 / 18.9). Large lists of 16-bit parameters with
+// 8-bit states are bound by the vector unit, which what a workgroup does once (the clipping
+// factor in fp64, the search) keeps busy too (2 x 50M bf16 239 / 214).
 int chunk_for(const AdamwCall& c) {
-  int64_t total = 0;
-  for (int i = 0; i < c.n && total < MAX_GRID * CHUNK_MAX; ++i) total += c.numels[i];
-  return (int)(total < MAX_GRID * CHUNK_MAX ? CHUNK_MIN : CHUNK_MAX);
+  if (!c.ms) return CHUNK_MIN;
+  int64_t total = 0, narrow = 0;
+  for (int i = 0; i < c.n; ++i) {
+    total += c.numels[i];
+    if (c.param_types[i] != TYPE_F32) narrow += c.numels[i];
+  }
+  return (int)(total >= LONG && narrow > total / 2 ? CHUNK_MAX : CHUNK_MIN);
 }
 
 }  // namespace
@@ -428,6 +486,7 @@ hipError_t launch_adamw(const AdamwCall& c, hipStream_t stream) {
   h.max_norm = c.max_norm;
   h.step = c.step;
   h.seed = c.seed;
+  if (!c.step_at && !c.lr_at) of_step(h, c.step, c.lr, h);
   t.chunk = chunk_for(c);
   const auto kernel = c.ms ? adamw_kernel<8> : adamw_kernel<32>;
   int i = 0;
@@ -438,7 +497,7 @@ hipError_t launch_adamw(const AdamwCall& c, hipStream_t stream) {
     for (; i < c.n && t.n < MAX_T; ++i) {
       if (c.numels[i] == 0) continue;
       const int64_t k = (c.numels[i] + t.chunk - 1) / t.chunk;
-      if (chunks + k > 0x7FFFFFFF) break;              // (each tensor fits by itself: checked before)
+      if (chunks + k > CHUNKS && t.n > 0) break;       // (each tensor fits by itself: checked before)
       chunks += k;
       t.p[t.n] = c.params[i];
       t.g[t.n] = c.grads[i];
@@ -456,8 +515,7 @@ hipError_t launch_adamw(const AdamwCall& c, hipStream_t stream) {
     }
     // (nothing to do, but a norm to write)
     if (chunks == 0 && !(first && c.norm)) break;
-    const int64_t grid = chunks < 1 ? 1 : (chunks < MAX_GRID ? chunks : MAX_GRID);
-    kernel<<<dim3((unsigned)grid), dim3(THREADS), 0, stream>>>(a);
+    kernel<<<dim3((unsigned)(chunks ? chunks : 1)), dim3(THREADS), 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     h.norm = nullptr;

@@ -41,8 +41,7 @@ fp8g_status list_ok(const void* const* grads, const int64_t* numels, const int* 
   return FP8G_OK;
 }
 
-constexpr int64_t kNumel32Max = int64_t(1) << 43;   // (chunks of 8192 elements and
-constexpr int64_t kNumel8Max = int64_t(1) << 38;    // blocks of 128 are counted in 31 bits)
+constexpr int64_t kNumelStepMax = ((int64_t(1) << 24) - 1) * 2048;   // chunks of 2048 in a launch
 
 fp8g_status adamw_list_ok(const AdamwCall& c) {
   const bool eight = c.ms || c.vs;
@@ -55,7 +54,7 @@ fp8g_status adamw_list_ok(const AdamwCall& c) {
   for (int i = 0; i < c.n; ++i) {
     if (c.numels[i] < 0) return FP8G_ERR_SHAPE;
     if (!type_ok(c.param_types[i]) || !type_ok(c.grad_types[i]) ||
-        c.numels[i] > (eight ? kNumel8Max : kNumel32Max))
+        c.numels[i] > kNumelStepMax)
       return FP8G_ERR_UNSUPPORTED;
     void* const copy = c.copies ? c.copies[i] : nullptr;
     if (copy && c.copy_types[i] != FP8G_TYPE_BF16 && c.copy_types[i] != FP8G_TYPE_F16)
