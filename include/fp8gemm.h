@@ -516,6 +516,73 @@ fp8g_status moe_route_backward(const void* logits, int type, int64_t T, int E, i
                                const int32_t* counts, const int32_t* routed, void* d_logits,
                                int64_t ld_d, hipStream_t stream);
 
+/* Scores of a routed expert. */
+enum { FP8G_SCORE_SIGMOID = 0, FP8G_SCORE_SOFTMAX = 1 };
+
+/*
+ * moe_route_scored -- moe_route with the experts chosen by a score plus a
+ * bias inside groups of experts (a router that keeps its experts evenly
+ * loaded by moving the bias).
+ *
+ * For each token t, s the sigmoids or the softmax of its logits:
+ *   v = s + bias; an expert whose logit or v is -inf or NaN is never chosen.
+ *   Experts lie in `groups` groups of E / groups adjacent ones. A group's
+ *   value is the sum of its group_best (1 or 2) largest v that may be chosen
+ *   (of one where there is one); the open_groups groups of largest value are
+ *   open, ties to the lower group, a group without any such expert never.
+ *   expert_ids[t][j]  the expert of the j-th largest v in the open groups,
+ *                     ties to the lower index; -1 past the last. Without a
+ *                     bias and with every group open the choice goes by the
+ *                     logits (the same order). Which of two values is larger
+ *                     is decided as in 64-bit arithmetic.
+ *   weights[t][j]     scale * s[expert_ids[t][j]], with renormalise over the
+ *                     row's sum of the chosen s (their shares of it, however
+ *                     small the scores are);
+ *                     0 where the id is -1. A row with a NaN logit (with
+ *                     softmax: or +inf) has NaN in all k weights; with
+ *                     softmax its v are NaN too, so that it chooses nothing
+ *                     where the choice goes by v.
+ *   prob_sum[e]       sum over the routed tokens of s[e] / sum_e' s[e'] (and
+ *                     NaN if a token not masked out has NaN scores).
+ * slots, counts, routed, loss, group_offsets and everything else as for
+ * moe_route.
+ *
+ * bias  fp32 [E], 4-byte aligned, or NULL (zeros).
+ * groups >= 1 divides E (up to 32); 1 <= open_groups <= groups; 1 <=
+ * group_best <= min(2, E / groups); top_k <= open_groups * (E / groups).
+ * workspace  moe_route_workspace_size's.
+ * Errors (nothing is launched): as for moe_route; FP8G_ERR_SHAPE for groups
+ * as stated, _UNSUPPORTED for an unknown score, more than 32 groups or
+ * group_best > 2, _ALIGN for bias.
+ */
+fp8g_status moe_route_scored(const void* logits, int type, int64_t T, int E, int64_t ld, const float* bias,
+                             int score, int groups, int open_groups, int group_best, const uint8_t* token_mask,
+                             int top_k, int renormalise, float scale, float loss_coef, int align,
+                             int64_t max_m, int32_t* expert_ids, float* weights, int32_t* counts,
+                             int32_t* routed, float* prob_sum, float* loss, int32_t* group_offsets,
+                             int32_t* slots, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * moe_route_scored_backward -- the gradient of moe_route_scored's weights and
+ * loss with respect to the logits (the choice, counts and the bias are
+ * constants).
+ *   f_e  = E counts[e] / (top_k n^2) * loss_coef * d_loss
+ *   dw'_j = scale (d_weights[t][j] - [renormalise] sum_i d_weights[t][i] u_i) / S
+ *           for the chosen, with renormalise S the sum of the chosen s and
+ *           u = s / S, without S = 1
+ *   softmax: d_logits = s (f + dw' - sum s (f + dw'))
+ *   sigmoid: d_logits = s (1 - s) ((f - sum f s / z) / z + dw'), z = sum s
+ * in fp32, rounded once to the logits' type. Rows whose first id is -1 get
+ * zeros, and so does a -inf logit.
+ * Arguments and errors as for moe_route_backward; score and scale as given
+ * to moe_route_scored (FP8G_ERR_UNSUPPORTED for an unknown score).
+ */
+fp8g_status moe_route_scored_backward(const void* logits, int type, int64_t T, int E, int64_t ld, int score,
+                                      const int32_t* expert_ids, int top_k, int renormalise, float scale,
+                                      float loss_coef, const float* d_weights, const float* d_loss,
+                                      const int32_t* counts, const int32_t* routed, void* d_logits,
+                                      int64_t ld_d, hipStream_t stream);
+
 /*
  * fp8_quantize_transpose -- an operand of the weight gradient: x quantised
  * along its rows (tokens) and written transposed.

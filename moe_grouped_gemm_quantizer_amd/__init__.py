@@ -13,6 +13,7 @@ from ._lib import (fp8_quantize, fp8_quantize_bf16, fp8_quantize_tensor, gemm_fp
                    moe_route, moe_route_workspace_size, moe_route_backward,
                    fp8_quantize_transpose, grouped_gemm_fp8_wgrad,
                    grad_norm_sq, grad_norm_sq_workspace_size, grad_clip,
+                   moe_route_scored, moe_route_scored_backward,
                    adamw_tensors, adamw_step,
                    int8_quantize, gemm_int8, grouped_gemm_int8_contiguous,
                    grouped_gemm_int8_masked,
@@ -29,6 +30,7 @@ __all__ = ["fp8_quantize", "fp8_quantize_bf16", "fp8_quantize_tensor", "gemm_fp8
            "moe_route", "moe_route_workspace_size", "moe_route_backward",
            "fp8_quantize_transpose", "grouped_gemm_fp8_wgrad",
            "grad_norm_sq", "grad_norm_sq_workspace_size", "grad_clip",
+           "moe_route_scored", "moe_route_scored_backward",
            "adamw_tensors", "adamw_step",
            "int8_quantize", "gemm_int8", "grouped_gemm_int8_contiguous",
            "grouped_gemm_int8_masked",

@@ -25,6 +25,7 @@ ENTRY_POINTS = ("fp8_quantize", "fp8_quantize_bf16", "fp8_quantize_tensor", "gem
                 "moe_route", "moe_route_workspace_size", "moe_route_backward",
                 "fp8_quantize_transpose", "grouped_gemm_fp8_wgrad", "grad_norm_sq",
                 "grad_norm_sq_workspace_size", "grad_clip",
+                "moe_route_scored", "moe_route_scored_backward",
                 "adamw_step", "int8_quantize", "gemm_int8", "grouped_gemm_int8_contiguous",
                 "grouped_gemm_int8_masked",
                 "fp8g_status_string", "fp8g_abi_version")
@@ -76,6 +77,11 @@ _SIGS = {
     "grad_norm_sq": [_c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_sz, _c_vp],
     "grad_norm_sq_workspace_size": [_c_vp, _c_int, ctypes.POINTER(_c_sz)],
     "grad_clip": [_c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_f, _c_vp, _c_vp],
+    "moe_route_scored": [_c_vp, _c_int, _c_i64, _c_int, _c_i64, _c_vp, _c_int, _c_int, _c_int, _c_int, _c_vp,
+                         _c_int, _c_int, _c_f, _c_f, _c_int, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp,
+                         _c_vp, _c_vp, _c_vp, _c_vp, _c_sz, _c_vp],
+    "moe_route_scored_backward": [_c_vp, _c_int, _c_i64, _c_int, _c_i64, _c_int, _c_vp, _c_int, _c_int, _c_f,
+                                  _c_f, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp],
     "adamw_step": [_c_vp] * 11 + [_c_int, _c_vp, _c_i64, _c_vp, _c_d, _c_d, _c_d, _c_d, _c_d, _c_vp, _c_f,
                                   _c_vp, ctypes.c_uint32, _c_vp],
     "int8_quantize": [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp],
@@ -88,6 +94,7 @@ _SIGS = {
 
 LAYOUTS = {"dense": 0, "contiguous": 1, "masked": 2, "pertensor": 3}
 FORMATS = {"e4m3": 0, "e5m2": 1}
+SCORES = {"sigmoid": 0, "softmax": 1}
 
 _lib = None
 
@@ -510,6 +517,72 @@ def moe_route(logits, top_k, expert_ids, weights, counts, routed, prob_sum, loss
                           align, max_m, ids, wts, cnt, rtd, psm, los, off, slt, wp, wb, _stream(stream))
     if st:
         _check(st, "moe_route")
+
+
+def _score(name):
+    if name not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}")
+    return SCORES[name]
+
+
+def moe_route_scored(logits, top_k, expert_ids, weights, counts, routed, prob_sum, loss, group_offsets, slots,
+                     workspace=None, score="sigmoid", bias=None, groups=1, open_groups=1, group_best=1,
+                     token_mask=None, renormalise=False, scale=1.0, loss_coef=1.0, align=128, max_m=0,
+                     stream=None):
+    """Routing by scores: 'sigmoid' or 'softmax' of the logits, plus bias
+    (float32 [E] or None) for the choice alone, inside the open_groups of groups
+    equal groups of experts whose group_best (1 or 2) largest values sum to the
+    most; weights scale times the scores without the bias, over their sum with
+    renormalise. Everything else as for moe_route."""
+    torch = _torch()
+    ptr, T, E, ld = _rows(logits, "logits")
+    typ = _TYPES.get(logits.dtype)
+    if typ is None:
+        _fail("logits must be float32, bfloat16 or float16")
+    i32, f32, pairs = torch.int32, torch.float32, (T, top_k)
+    ids = _out(expert_ids, pairs, i32, "expert_ids")
+    wts = _out(weights, pairs, f32, "weights")
+    cnt = _out(counts, (E,), i32, "counts")
+    rtd = _out(routed, (1,), i32, "routed")
+    psm = _out(prob_sum, (E,), f32, "prob_sum")
+    los = _out(loss, (1,), f32, "loss")
+    off = _out(group_offsets, (E + 1,), i32, "group_offsets")
+    slt = _out(slots, pairs, i32, "slots")
+    bia = None if bias is None else _out(bias, (E,), f32, "bias")
+    mask = None
+    if token_mask is not None:
+        mask = _out(token_mask, (T,), torch.uint8 if token_mask.dtype is torch.uint8 else torch.bool, "token_mask")
+    wp, wb = _room(workspace)
+    _one_device(logits, expert_ids, weights, slots, counts)
+    st = load().moe_route_scored(ptr, typ, T, E, ld, bia, _score(score), groups, open_groups, group_best, mask,
+                                 top_k, 1 if renormalise else 0, scale, loss_coef, align, max_m, ids, wts, cnt,
+                                 rtd, psm, los, off, slt, wp, wb, _stream(stream))
+    if st:
+        _check(st, "moe_route_scored")
+
+
+def moe_route_scored_backward(logits, expert_ids, d_weights, d_loss, counts, routed, d_logits, score="sigmoid",
+                              renormalise=False, scale=1.0, loss_coef=1.0, stream=None):
+    """Gradient of moe_route_scored's weights and loss with respect to the
+    logits; score, renormalise, scale and loss_coef as given there, the rest as
+    for moe_route_backward."""
+    torch = _torch()
+    ptr, T, E, ld = _rows(logits, "logits")
+    dptr, dT, dE, ldd = _rows(d_logits, "d_logits")
+    typ = _TYPES.get(logits.dtype)
+    if typ is None or d_logits.dtype is not logits.dtype or dT != T or dE != E:
+        _fail("logits and d_logits must be float32, bfloat16 or float16, alike in type and shape")
+    top_k = expert_ids.shape[-1]
+    ids = _out(expert_ids, (T, top_k), torch.int32, "expert_ids")
+    dw = None if d_weights is None else _out(d_weights, (T, top_k), torch.float32, "d_weights")
+    dl = None if d_loss is None else _out(d_loss, (1,), torch.float32, "d_loss")
+    cnt = _out(counts, (E,), torch.int32, "counts")
+    rtd = _out(routed, (1,), torch.int32, "routed")
+    _one_device(logits, expert_ids, d_logits, counts)
+    st = load().moe_route_scored_backward(ptr, typ, T, E, ld, _score(score), ids, top_k, 1 if renormalise else 0,
+                                          scale, loss_coef, dw, dl, cnt, rtd, dptr, ldd, _stream(stream))
+    if st:
+        _check(st, "moe_route_scored_backward")
 
 
 def moe_route_backward(logits, expert_ids, d_weights, d_loss, counts, routed, d_logits,

@@ -97,6 +97,7 @@ fp8g_status fp8g_warmup(void) {
   gemm_kernels(kernels);
   quantize_kernels(kernels);
   route_kernels(kernels);
+  route_scored_kernels(kernels);
   wgrad_kernels(kernels);
   clip_kernels(kernels);
   int8_kernels(kernels);

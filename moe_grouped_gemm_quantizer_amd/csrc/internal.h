@@ -128,7 +128,26 @@ struct RouteBwdCall {
 size_t route_workspace_bytes(int64_t T, int E);
 hipError_t launch_route(const RouteCall& c, hipStream_t stream);
 hipError_t launch_route_backward(const RouteBwdCall& c, hipStream_t stream, int cu_count);
+// What follows the rows' kernel of more than one block, or of none: the scan of the blocks' counts,
+// slots, offsets and loss (a choice's rank inside its block is in its slot by then).
+hipError_t launch_route_places(const RouteCall& c, hipStream_t stream);
 void route_kernels(std::vector<const void*>& out);
+// Routing by scores (route_scored.hip); arguments as for moe_route_scored and its gradient.
+enum RouteScore { SCORE_SIGMOID = 0, SCORE_SOFTMAX = 1 };
+struct ScoredCall {
+  RouteCall route;
+  const float* bias;
+  int score, groups, open, best;
+  float scale;
+};
+struct ScoredBwdCall {
+  RouteBwdCall route;
+  int score;
+  float scale;
+};
+hipError_t launch_route_scored(const ScoredCall& c, hipStream_t stream);
+hipError_t launch_route_scored_backward(const ScoredBwdCall& c, hipStream_t stream, int cu_count);
+void route_scored_kernels(std::vector<const void*>& out);
 
 // The weight gradient (wgrad.hip).
 hipError_t launch_quantize_transpose(const void* x, int type, int64_t rows, int64_t cols,

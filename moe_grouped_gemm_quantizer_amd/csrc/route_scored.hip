@@ -1,0 +1,639 @@
+// Routing by scores: sigmoid or softmax of the logits, the experts chosen by score plus a bias
+// that keeps them evenly loaded, inside the groups of experts whose best values' sum is largest;
+// weights from the scores without the bias. The gradient of weights and balance loss.
+//
+//   s = sigmoid(x) or softmax(x);  v = s + b;  a group's value is the sum of its `best` (1 or 2)
+//   largest v; the `open` groups of largest value are open; ids: the k largest v in them, ties to
+//   the lower expert;  w = scale s[id] (over the sum of the chosen s);
+//   loss = coef sum_e (E c_e / (k n)) (P_e / n), P_e the sum over tokens of s_e / sum s.
+// With every group open and no bias the choice goes by the logits themselves (both scores rise
+// with them), as in route.hip, whose scan and slots follow here too.
+//
+// Which of two values is larger is decided exactly: as in 64 bits. The fp32 values choose, as
+// whole numbers of 24 (22) bits of the row's range with the expert's number below; where two
+// neighbours among the chosen and the next, or the last open and the first closed group, are
+// nearer than their errors and not alike (the same logit and bias), the row is put on a list and
+// done again in 64 bits by a wave of its own: about 0.1% of the rows of random fp32 logits.
+
+#include <vector>
+
+#include "route_common.h"
+
+namespace fp8g {
+namespace {
+
+constexpr int MAX_GROUPS = 32;
+
+struct ScoredArgs {
+  RouteArgs r;
+  const float* bias;
+  int score, groups, open, best, size;                 // size: experts of a group
+  float scale;
+};
+
+// Sums of scores below this are formed again from exponentials shifted by the largest logit: both
+// scores are exp(x) times a factor of the row there (sigmoid to 2^-90), and shares of a sum do not
+// depend on it, however far below fp32's range the scores are.
+constexpr float LITTLE = 0x1p-90f;
+
+// A row's scores, and what of them its share of the loss is: 1 / sum s (0 for a row without any,
+// NaN where a logit is NaN, or with softmax infinite).
+struct RowSum {
+  float share, top, norm;                              // softmax: s = exp(x - top) norm
+};
+// sigmoid from exp(-|x|), exact to 4 ulp at both ends; and what it lacks of 1.
+__device__ __forceinline__ float sigmoid(float x) {
+  const float t = exp_neg(-__builtin_fabsf(x));
+  return (x >= 0.0f ? 1.0f : t) * __builtin_amdgcn_rcpf(1.0f + t);
+}
+__device__ __forceinline__ float sigmoid(float x, float& rest) {
+  const float t = exp_neg(-__builtin_fabsf(x)), q = __builtin_amdgcn_rcpf(1.0f + t), p = t * q;
+  rest = x >= 0.0f ? p : q;
+  return x >= 0.0f ? q : p;
+}
+template <int LPR, int VPT>
+__device__ __forceinline__ RowSum row_scores(const float (&x)[VPT], int score, float (&s)[VPT]) {
+  RowSum r;
+  if (score == SCORE_SOFTMAX) {
+    r.norm = row_softmax<LPR, VPT>(x, r.top, s);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) s[v] *= r.norm;
+    r.share = r.norm > 0.0f ? 1.0f : r.norm;           // (0 and NaN stay)
+  } else {
+    float z = 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      s[v] = sigmoid(x[v]);
+      z += s[v];
+    }
+    z = sum_lanes<LPR>(z);
+    r.share = z == 0.0f ? 0.0f : 1.0f / z;
+    r.top = r.norm = 0.0f;
+  }
+  return r;
+}
+__device__ __forceinline__ float score_of(float x, int score, const RowSum& r) {
+  return score == SCORE_SOFTMAX ? exp_neg(x - r.top) * r.norm : sigmoid(x);
+}
+// A row whose sigmoids are all little: s and share by shifted exponentials.
+template <int LPR, int VPT>
+__device__ __forceinline__ void little_scores(const float (&x)[VPT], bool little, float (&s)[VPT], float& share) {
+  if (__ballot(little) == 0) return;                   // (uniform over the wave)
+  float e[VPT], top;
+  const float norm = row_softmax<LPR, VPT>(x, top, e);
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) s[v] = little ? e[v] : s[v];
+  share = little ? norm : share;
+}
+// The chosen scores' shares of their sum, each lane its own (`on`: it has one).
+template <int LPR>
+__device__ __forceinline__ float chosen_share(float s, float x, bool on) {
+  float z = sum_lanes<LPR>(on ? s : 0.0f);
+  const bool little = z < LITTLE;
+  if (__ballot(little && on)) {
+    const float top = max_lanes<LPR>(on ? x : -__builtin_inff());
+    const float e = on ? exp_neg(x - top) : 0.0f;
+    const float ze = sum_lanes<LPR>(e);
+    s = little ? e : s;
+    z = little ? ze : z;
+  }
+  return on ? s / z : 0.0f;
+}
+
+// One row by a wave in 64 bits: lane l holds experts l, l + 64, ... Lane j gets the j-th choice
+// (-1: none) and its score.
+template <typename T, int PER>
+__device__ __forceinline__ int choose64(const T* __restrict__ row, const ScoredArgs& a, int l, double& score) {
+  const int E = a.r.E, k = a.r.k;
+  const double none = -__builtin_inf();
+  double s[PER], v[PER];
+  double top = none;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int e = l + 64 * q;
+    s[q] = e < E ? (double)to_f32(row[e]) : none;
+    top = fmax(top, s[q]);
+  }
+  uint32_t may = 0;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) may |= (s[q] > none ? 1u : 0u) << q;
+  if (a.score == SCORE_SOFTMAX) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) top = fmax(top, __shfl_xor(top, o));
+    double z = 0.0;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      s[q] = l + 64 * q < E ? exp(s[q] - (top > none ? top : 0.0)) : 0.0;
+      z += s[q];
+    }
+    z = sum_wave(z);
+#pragma unroll
+    for (int q = 0; q < PER; ++q) s[q] = s[q] / z;
+  } else {
+#pragma unroll
+    for (int q = 0; q < PER; ++q) s[q] = 1.0 / (1.0 + exp(-s[q]));
+  }
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int e = l + 64 * q;
+    v[q] = (may >> q & 1) ? (a.bias ? s[q] + (double)a.bias[e] : s[q]) : none;
+    if (!(v[q] > none)) v[q] = none;                   // (NaN)
+  }
+  if (a.open < a.groups) {
+    double mine = none;                                // lane g: group g's value
+    for (int g = 0; g < a.groups; ++g) {
+      double t1 = none, t2 = none;
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        const int e = l + 64 * q;
+        const double x = e >= g * a.size && e < (g + 1) * a.size ? v[q] : none;
+        t2 = fmax(t2, fmin(t1, x));
+        t1 = fmax(t1, x);
+      }
+#pragma unroll
+      for (int o = 32; o >= 1; o >>= 1) {
+        const double u1 = __shfl_xor(t1, o), u2 = __shfl_xor(t2, o);
+        t2 = fmax(fmax(t2, u2), fmin(t1, u1));
+        t1 = fmax(t1, u1);
+      }
+      const double value = a.best > 1 && t2 > none ? t1 + t2 : t1;
+      mine = l == g ? value : mine;
+    }
+    int rank = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const double x = __shfl(mine, g);
+      rank += x > mine || (x == mine && g < l) ? 1 : 0;
+    }
+    const uint64_t open = __ballot(l < a.groups && rank < a.open && mine > none);
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const int e = l + 64 * q;
+      if (e < E && !(open >> (e / a.size) & 1)) v[q] = none;
+    }
+  }
+  if (!a.bias) {                                       // (the logits tell more of what is near 0 or 1)
+#pragma unroll
+    for (int q = 0; q < PER; ++q)
+      if (v[q] > none) v[q] = (double)to_f32(row[l + 64 * q]);
+  }
+  int id = -1;
+  score = 0.0;
+  for (int j = 0; j < k; ++j) {
+    double best = none, at = 0.0;
+    int e = 1 << 30;
+#pragma unroll
+    for (int q = PER - 1; q >= 0; --q)
+      if (v[q] > none && v[q] >= best) {
+        best = v[q];
+        at = s[q];
+        e = l + 64 * q;
+      }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+      const double ob = __shfl_xor(best, o), oa = __shfl_xor(at, o);
+      const int oe = __shfl_xor(e, o);
+      if (ob > best || (ob == best && oe < e)) {
+        best = ob;
+        at = oa;
+        e = oe;
+      }
+    }
+    if (!(best > none)) break;                         // (the same in all lanes)
+    if (l == j) {
+      id = e;
+      score = at;
+    }
+#pragma unroll
+    for (int q = 0; q < PER; ++q)
+      if (l + 64 * q == e) v[q] = none;
+  }
+  return id;
+}
+
+// One block of 64 tokens per workgroup, LPR lanes a row, as in route.hip.
+template <typename T, int LPR, int VPT, int NT>
+__global__ void __launch_bounds__(NT)
+route_scored_rows_kernel(ScoredArgs a) {
+  using L = Lay<T, LPR, VPT>;
+  constexpr int AT_ONCE = NT / LPR, WAVES = NT / 64;
+  constexpr int BITS = LPR * VPT <= 256 ? 8 : 10;      // of a key, for the expert's number
+  constexpr uint32_t LOW = (1u << BITS) - 1u;
+  // Two values are surely in the keys' order from NEAR on: each is off by up to 4 ulp of the
+  // score, half a one of the sum with the bias and 1.5 of the key's forming, at 2^-24 of the
+  // range's half M = 2^(31 - BITS) units.
+  constexpr uint32_t NEAR = BITS == 8 ? 16 : 8;
+  __shared__ uint32_t took[2][MAX_E];
+  __shared__ short chosen[ROWS][MAX_K];
+  __shared__ float psum[WAVES][LPR * VPT];
+  __shared__ int count[MAX_E], off[MAX_E + 1];
+  __shared__ int wave_sum[WAVES];
+  __shared__ int n_routed, n_again;
+  __shared__ short again[ROWS];                        // rows that are done again in 64 bits
+  __shared__ float values[AT_ONCE][LPR * VPT];         // where groups are chosen
+  __shared__ float group_value[AT_ONCE][MAX_GROUPS];
+  const int E = a.r.E, k = a.r.k;
+  for (int e = threadIdx.x; e < E; e += NT) took[0][e] = took[1][e] = 0u;
+  if (threadIdx.x == 0) n_routed = n_again = 0;
+  __syncthreads();
+  const int l = threadIdx.x & (LPR - 1), lane = threadIdx.x & 63;
+  const int at_row = threadIdx.x / LPR;
+  const int64_t block = (int64_t)a.r.block0 + blockIdx.x;
+  const int64_t t0 = block * ROWS;
+  const bool by_value = a.bias || a.open < a.groups;
+  const auto take = [&](int64_t t, int r, int id, float w) __attribute__((always_inline)) {
+    a.r.ids[t * k + l] = id;
+    a.r.weights[t * k + l] = w;
+    chosen[r][l] = (short)id;
+    if (id >= 0) atomicOr(&took[r >> 5][id], 1u << (r & 31));
+  };
+  float acc[VPT], b[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    acc[v] = 0.0f;
+    const int e = L::at(v, l);
+    b[v] = a.bias && e < E ? a.bias[e] : 0.0f;
+  }
+  for (int r0 = 0; r0 < ROWS && t0 + r0 < a.r.T; r0 += AT_ONCE) {
+    const int r = r0 + at_row;
+    const int64_t t = t0 + r;
+    const bool in = t < a.r.T;
+    const bool on = in && (!a.r.mask || a.r.mask[t] != 0);
+    const T* const row = (const T*)a.r.logits + (in ? t : 0) * a.r.ld;
+    float x[VPT], s[VPT];
+    load_row<T, LPR, VPT>(row, E, l, on, a.r.vec != 0, x);
+    const RowSum sum = row_scores<LPR, VPT>(x, a.score, s);
+    int id;
+    float xj;                                          // the choice's logit
+    bool redo = false;
+    if (!by_value) {
+      id = choose<T, LPR, VPT>(x, row, l, k, xj);
+    } else {
+      // values; what is never chosen is -inf
+      float val[VPT], m = -1.0f;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const float y = s[v] + b[v];
+        const bool may = x[v] > -__builtin_inff() && y > -__builtin_inff();
+        val[v] = may ? y : -__builtin_inff();
+        m = may ? __builtin_fmaxf(m, __builtin_fmaxf(__builtin_fabsf(y), s[v])) : m;
+      }
+      m = max_lanes<LPR>(m);
+      // (m < 0: nothing to choose from; no range to count in otherwise)
+      redo = m >= 0.0f && !(m > 1e-30f && m < 1e30f);
+      uint32_t open = 0xFFFFFFFFu;
+      if (a.open < a.groups) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) values[at_row][L::at(v, l)] = val[v];
+        wave_sync();
+        for (int g = l; g < a.groups; g += LPR) {
+          // (lanes start at different places: their groups lie banks apart)
+          float t1 = -__builtin_inff(), t2 = -__builtin_inff();
+          int i = lane % a.size;
+          for (int n = 0; n < a.size; ++n) {
+            const float y = values[at_row][g * a.size + i];
+            t2 = __builtin_fmaxf(t2, __builtin_fminf(t1, y));
+            t1 = __builtin_fmaxf(t1, y);
+            i = i + 1 == a.size ? 0 : i + 1;
+          }
+          group_value[at_row][g] = a.best > 1 && t2 > -__builtin_inff() ? t1 + t2 : t1;
+        }
+        wave_sync();
+        // a group's rank among all; the least open and the largest closed value
+        float least = __builtin_inff(), most = -__builtin_inff();
+        uint32_t bits = 0u;
+        for (int g = l; g < a.groups; g += LPR) {
+          const float mine = group_value[at_row][g];
+          int rank = 0;
+          for (int h = 0; h < a.groups; ++h) {
+            const float y = group_value[at_row][h];
+            rank += y > mine || (y == mine && h < g) ? 1 : 0;
+          }
+          const bool is_open = rank < a.open && mine > -__builtin_inff();
+          bits |= is_open ? 1u << g : 0u;
+          if (is_open) least = __builtin_fminf(least, mine);
+          else most = __builtin_fmaxf(most, mine);
+        }
+        open = reduce_u32<LPR>(bits, [](uint32_t p, uint32_t q) { return p | q; });
+        least = reduce_f32<LPR>(least, [](float p, float q) { return __builtin_fminf(p, q); });
+        most = max_lanes<LPR>(most);
+        // (two values a side, each off by 5.5 2^-24 of m at most, and their sums' rounding)
+        redo = redo || (most > -__builtin_inff() && !(least - most > m * 0x1p-19f));
+        wave_sync();
+      }
+      const float to_units = (float)(1u << (31 - BITS)) / m;
+      uint32_t key[VPT];
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int e = L::at(v, l);
+        const bool may = val[v] > -__builtin_inff() && (open >> (a.open < a.groups ? e / a.size : 0) & 1u);
+        const uint32_t u = min((uint32_t)((val[v] + m) * to_units) + 1u, (1u << (32 - BITS)) - 1u);
+        key[v] = may ? u << BITS | (LOW - (uint32_t)e) : 0u;
+      }
+      // the largest keys one after the other: the next one is the largest below the last, and
+      // with d = key - last in wrapping arithmetic every key below it has a larger d than
+      // every key from it on
+      const auto umax = [](uint32_t p, uint32_t q) { return p > q ? p : q; };
+      uint32_t last = 0u, mine = 0u;
+      const auto next = [&]() __attribute__((always_inline)) {
+        uint32_t d = key[0] - last;
+#pragma unroll
+        for (int v = 1; v < VPT; ++v) d = umax(d, key[v] - last);
+        d = reduce_u32<LPR>(d, umax);
+        const uint32_t n = last + d;
+        const bool none = n == 0u || (last != 0u && n >= last);
+        last = none ? last : n;
+        return none ? 0u : n;
+      };
+      for (int j = 0; j < k; ++j) {
+        const uint32_t n = next();
+        if (l == j) mine = n;
+      }
+      const uint32_t extra = next();
+      id = mine ? (int)(LOW - (mine & LOW)) : -1;
+      const int ie = extra ? (int)(LOW - (extra & LOW)) : -1;
+      xj = id >= 0 ? to_f32(row[id]) : 0.0f;
+      const float bj = id >= 0 && a.bias ? a.bias[id] : 0.0f;
+      const float xe = ie >= 0 ? to_f32(row[ie]) : 0.0f, be = ie >= 0 && a.bias ? a.bias[ie] : 0.0f;
+      // (LPR lanes: the one behind the k-th takes the next candidate)
+      uint32_t kn = (uint32_t)__shfl_down((int)mine, 1, LPR);
+      float xn = __shfl_down(xj, 1, LPR), bn = __shfl_down(bj, 1, LPR);
+      if (l == k - 1) {
+        kn = extra;
+        xn = xe;
+        bn = be;
+      }
+      const bool close = l < k && kn && (mine >> BITS) - (kn >> BITS) <= NEAR && !(xj == xn && bj == bn);
+      redo = redo || reduce_u32<LPR>(close ? 1u : 0u, umax) != 0u;
+    }
+    const bool routed = __shfl(id, 0, LPR) >= 0;
+    float w = id >= 0 ? score_of(xj, a.score, sum) : 0.0f;
+    if (a.r.renorm) w = chosen_share<LPR>(w, xj, id >= 0);
+    const bool bad = sum.share != sum.share;
+    w = bad ? sum.share : w * a.scale;
+    // (a token that chooses nothing is not in the sums, unless it is NaN)
+    float share = routed || bad ? sum.share : 0.0f;
+    if (a.score == SCORE_SIGMOID)
+      little_scores<LPR, VPT>(x, routed && !(sum.share <= 1.0f / LITTLE && sum.share > 0.0f) && !bad, s, share);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) acc[v] += share != 0.0f ? s[v] * share : 0.0f;
+    if (in && l == 0 && routed) atomicAdd(&n_routed, 1);
+    if (in && l < k && !redo) take(t, r, id, w);
+    if (in && l == 0 && redo) again[atomicAdd(&n_again, 1)] = (short)r;
+  }
+  __syncthreads();
+  // rows whose values are too near: a wave each
+  constexpr int PER = (LPR * VPT + 63) / 64;
+  for (int i = threadIdx.x >> 6; i < n_again; i += WAVES) {
+    const int r = again[i];
+    const int64_t t = t0 + r;
+    const T* const row = (const T*)a.r.logits + t * a.r.ld;
+    double score;
+    const int id = choose64<T, PER>(row, a, lane, score);
+    bool bad = false;
+    for (int e = lane; e < E; e += 64) {
+      const float x = to_f32(row[e]);
+      bad = bad || x != x || (a.score == SCORE_SOFTMAX && x == __builtin_inff());
+    }
+    float w = (float)score;
+    if (a.r.renorm) w = chosen_share<64>(w, id >= 0 ? to_f32(row[id]) : 0.0f, id >= 0);
+    w = __ballot(bad) ? __builtin_nanf("") : w * a.scale;
+    if (lane < k) {
+      a.r.ids[t * k + lane] = id;
+      a.r.weights[t * k + lane] = w;
+      chosen[r][lane] = (short)id;
+      if (id >= 0) atomicOr(&took[r >> 5][id], 1u << (r & 31));
+    }
+  }
+  finish_block<T, LPR, VPT, NT>(a.r, block, acc, took, chosen, psum, count, off, wave_sum, n_routed);
+}
+
+constexpr int BWD_PER_CU = 4;                          // workgroups per CU of the backward pass
+
+struct ScoredBwdArgs {
+  const void* logits;
+  void* d_logits;
+  const int32_t *ids, *counts, *routed;
+  const float *dw, *dloss;
+  int64_t T, ld, ldd;
+  int E, k, renorm, vec, score;
+  float coef, scale;
+};
+
+// A workgroup walks rows, LPR lanes a row, the scores formed again from the logits. With
+// f_e = E c_e / (k n^2) coef dL, shares q = s / sum s and u = s / (the sum of the chosen s), d = scale
+// dw, and for the chosen
+//   softmax: c = u (d - sum d u) with renormalise, else s d;   dx = q (f - sum f q - [else] sum s d) + c
+//   sigmoid: c = u (1 - s) (d - sum d u), else s (1 - s) d;   dx = q (1 - s) (f - sum f q) + c
+// which divides by no sum that could be little, and forms 1 - s without cancellation.
+template <typename T, int LPR, int VPT>
+__global__ void __launch_bounds__(THREADS)
+route_scored_backward_kernel(ScoredBwdArgs a) {
+  using L = Lay<T, LPR, VPT>;
+  constexpr int AT_ONCE = THREADS / LPR;
+  __shared__ __attribute__((aligned(16))) float chosen[AT_ONCE][LPR * VPT];
+  const int E = a.E, k = a.k;
+  const int l = threadIdx.x & (LPR - 1), group = threadIdx.x / LPR;
+  const int n = a.routed[0];
+  const float fac = a.dloss && n > 0
+                        ? (float)((double)a.dloss[0] * a.coef * E / ((double)k * (double)n * (double)n))
+                        : 0.0f;
+  float f[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int e = L::at(v, l);
+    f[v] = e < E ? fac * (float)a.counts[e] : 0.0f;
+  }
+  // (a row's loads are issued while the one before it is worked on)
+  const int64_t stride = (int64_t)gridDim.x * AT_ONCE;
+  int id_n;
+  float dw_n, x_n[VPT];
+  const auto fetch = [&](int64_t t) __attribute__((always_inline)) {
+    const bool in = t < a.T;
+    id_n = in && l < k ? a.ids[t * k + l] : -1;
+    dw_n = in && l < k && a.dw ? a.dw[t * k + l] : 0.0f;
+    load_row<T, LPR, VPT>((const T*)a.logits + (in ? t : 0) * a.ld, E, l, in, a.vec != 0, x_n);
+  };
+  fetch((int64_t)blockIdx.x * AT_ONCE + group);
+  for (int64_t t0 = (int64_t)blockIdx.x * AT_ONCE; t0 < a.T; t0 += stride) {
+    const int64_t t = t0 + group;
+    const bool in = t < a.T;
+    const T* const row = (const T*)a.logits + (in ? t : 0) * a.ld;
+    int id = id_n;
+    float dwj = dw_n * a.scale;
+    float x[VPT], s[VPT], rest[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) x[v] = x_n[v];
+    if (t0 + stride < a.T) fetch(t + stride);
+    if (id >= E || id < 0) id = -1;
+    const float xj = id >= 0 ? to_f32(row[id]) : 0.0f;
+    const bool on = __shfl(id, 0, LPR) >= 0;
+    float sj, rj = 1.0f, share = 1.0f;
+    if (a.score == SCORE_SOFTMAX) {
+      float top;
+      const float norm = row_softmax<LPR, VPT>(x, top, s);
+      sj = exp_neg(xj - top) * norm;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        s[v] *= norm;
+        rest[v] = 1.0f;
+      }
+    } else {
+      float z = 0.0f;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        s[v] = sigmoid(x[v], rest[v]);
+        z += s[v];
+      }
+      z = sum_lanes<LPR>(z);
+      share = 1.0f / z;
+      sj = sigmoid(xj, rj);
+      little_scores<LPR, VPT>(x, z < LITTLE, s, share);
+    }
+    float c = 0.0f, dot = 0.0f;
+    if (a.renorm) {
+      const float u = chosen_share<LPR>(sj, xj, id >= 0);
+      c = u * rj * (dwj - sum_lanes<LPR>(id >= 0 ? dwj * u : 0.0f));
+    } else if (id >= 0) {
+      c = sj * rj * dwj;
+      if (a.score == SCORE_SOFTMAX) dot = c;
+    }
+    // sum f q [+ sum s d]
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) dot = __builtin_fmaf(s[v] * share, f[v], dot);
+    dot = sum_lanes<LPR>(dot);
+    // (a row is its wave's own: LDS accesses of a wave stay in order)
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) chosen[group][L::at(v, l)] = 0.0f;
+    wave_sync();
+    if (id >= 0) chosen[group][id] = c;
+    wave_sync();
+    float g[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+      g[v] = s[v] * share * rest[v] * (f[v] - dot) + chosen[group][L::at(v, l)];
+    wave_sync();
+    if (!in) continue;                                 // (whole rows: no lane of a row is left out)
+    T* const out = (T*)a.d_logits + t * a.ldd;
+#pragma unroll
+    for (int q = 0; q < VPT / L::W; ++q) {
+      const int e0 = L::at(q * L::W, l);
+      Pack<T, L::W> p;
+#pragma unroll
+      for (int w = 0; w < L::W; ++w) p.v[w] = from_f32<T>(on ? g[q * L::W + w] : 0.0f);
+      if (a.vec != 0 && e0 + L::W <= E) {
+        *reinterpret_cast<Pack<T, L::W>*>(out + e0) = p;
+      } else {
+#pragma unroll
+        for (int w = 0; w < L::W; ++w)
+          if (e0 + w < E) out[e0 + w] = p.v[w];
+      }
+    }
+  }
+}
+
+// The kernels for a type and an E: as in route.hip, 16 lanes a row up to 256 experts, 64 above and
+// for up to four tokens.
+typedef void (*RowsFn)(ScoredArgs);
+typedef void (*BwdFn)(ScoredBwdArgs);
+struct Pick {
+  RowsFn rows;
+  int rows_threads;
+  BwdFn bwd;
+  int rows_at_once;
+};
+template <typename T, int NT>
+Pick pick_for(int E) {
+  constexpr bool few = NT == THREADS;
+  constexpr int WIDE = NT > 512 ? 512 : NT;
+#define FP8G_PICK(LPR_, VPT_)                                                                    \
+  Pick { route_scored_rows_kernel<T, LPR_, VPT_, LPR_ == 16 && VPT_ >= 12 ? WIDE : NT>,          \
+         LPR_ == 16 && VPT_ >= 12 ? WIDE : NT, route_scored_backward_kernel<T, LPR_, VPT_>,      \
+         THREADS / LPR_ }
+  if (E <= 16) return FP8G_PICK(16, 1);
+  if (E <= 32) return FP8G_PICK(16, 2);
+  if (E <= 64) return FP8G_PICK(16, 4);
+  if constexpr (few) {
+    if (E <= 256) return FP8G_PICK(64, 4);
+  } else {
+    if (E <= 128) return FP8G_PICK(16, 8);
+    if (E <= 192) return FP8G_PICK(16, 12);
+    if (E <= 256) return FP8G_PICK(16, 16);
+  }
+  if (E <= 512) return FP8G_PICK(64, 8);
+  return FP8G_PICK(64, 16);
+#undef FP8G_PICK
+}
+template <typename T>
+Pick pick_of(int E, int64_t tokens) {
+  return tokens <= 4 ? pick_for<T, THREADS>(E) : pick_for<T, 1024>(E);
+}
+Pick pick(int type, int E, int64_t T) {
+  return type == TYPE_F32    ? pick_of<float>(E, T)
+         : type == TYPE_BF16 ? pick_of<bf16_t>(E, T)
+                             : pick_of<f16_t>(E, T);
+}
+
+}  // namespace
+
+hipError_t launch_route_scored(const ScoredCall& c, hipStream_t stream) {
+  ScoredArgs a;
+  a.r = route_args(c.route);
+  a.bias = c.bias;
+  a.score = c.score;
+  a.groups = c.groups;
+  a.open = c.open;
+  a.best = c.best;
+  a.size = c.route.E / c.groups;
+  a.scale = c.scale;
+  const int64_t nblk = (c.route.T + ROWS - 1) / ROWS;
+  if (nblk == 0) return launch_route_places(c.route, stream);
+  const Pick p = pick(c.route.type, c.route.E, c.route.T);
+  const int64_t most = rows_blocks_max(p.rows_threads);
+  for (int64_t b = 0; b < nblk; b += most) {
+    a.r.block0 = (int)b;
+    const int64_t grid = nblk - b < most ? nblk - b : most;
+    p.rows<<<dim3((unsigned)grid), dim3((unsigned)p.rows_threads), 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return nblk > 1 ? launch_route_places(c.route, stream) : hipSuccess;
+}
+
+hipError_t launch_route_scored_backward(const ScoredBwdCall& c, hipStream_t stream, int cu_count) {
+  const RouteBwdCall& r = c.route;
+  ScoredBwdArgs a;
+  a.logits = r.logits;
+  a.d_logits = r.d_logits;
+  a.ids = r.ids;
+  a.counts = r.counts;
+  a.routed = r.routed;
+  a.dw = r.dw;
+  a.dloss = r.dloss;
+  a.T = r.T;
+  a.ld = r.ld;
+  a.ldd = r.ldd;
+  a.E = r.E;
+  a.k = r.k;
+  a.renorm = r.renorm;
+  a.vec = vec_ok(r.logits, r.ld, r.type) && vec_ok(r.d_logits, r.ldd, r.type);
+  a.score = c.score;
+  a.coef = r.coef;
+  a.scale = c.scale;
+  const Pick p = pick(r.type, r.E, r.T);
+  int64_t grid = (r.T + p.rows_at_once - 1) / p.rows_at_once;
+  if (grid > (int64_t)cu_count * BWD_PER_CU) grid = (int64_t)cu_count * BWD_PER_CU;
+  p.bwd<<<dim3((unsigned)grid), dim3(THREADS), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+void route_scored_kernels(std::vector<const void*>& out) {
+  for (int type : {TYPE_F32, TYPE_BF16, TYPE_F16})
+    for (int E : {16, 32, 64, 128, 192, 256, 512, 1024})
+      for (int T : {1, 64}) {
+        const Pick p = pick(type, E, T);
+        out.push_back((const void*)p.rows);
+        out.push_back((const void*)p.bwd);
+      }
+}
+
+}  // namespace fp8g

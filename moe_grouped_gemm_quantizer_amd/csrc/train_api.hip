@@ -28,6 +28,80 @@ fp8g_status route_sizes(int type, int64_t T, int E, int64_t ld, int top_k) {
   return FP8G_OK;
 }
 
+// The checks that both routings share; fills c.
+fp8g_status route_call(const void* logits, int type, int64_t T, int E, int64_t ld, const uint8_t* token_mask,
+                       int top_k, int renormalise, float loss_coef, int align, int64_t max_m,
+                       int32_t* expert_ids, float* weights, int32_t* counts, int32_t* routed,
+                       float* prob_sum, float* loss, int32_t* group_offsets, int32_t* slots, void* workspace,
+                       size_t workspace_bytes, RouteCall& c) {
+  const fp8g_status s = route_sizes(type, T, E, ld, top_k);
+  if (s != FP8G_OK) return s;
+  if (align < 1 || max_m < 0) return FP8G_ERR_SHAPE;
+  if (max_m > kInt31 / E || (int64_t)align > kInt31 / E ||
+      T * top_k > kInt31 - (int64_t)E * align)
+    return FP8G_ERR_UNSUPPORTED;
+  if (!counts || !routed || !prob_sum || !loss || !group_offsets) return FP8G_ERR_NULL_PTR;
+  if (T > 0 && (!logits || !expert_ids || !weights || !slots)) return FP8G_ERR_NULL_PTR;
+  if (!aligned(logits, type_size(type)) || !aligned(expert_ids, 4) || !aligned(weights, 4) ||
+      !aligned(counts, 4) || !aligned(routed, 4) || !aligned(prob_sum, 4) || !aligned(loss, 4) ||
+      !aligned(group_offsets, 4) || !aligned(slots, 4) || !aligned(workspace, 16))
+    return FP8G_ERR_ALIGN;
+  if (workspace_bytes < route_workspace_bytes(T, E)) return FP8G_ERR_WORKSPACE;
+  if (!workspace && workspace_bytes != 0) return FP8G_ERR_NULL_PTR;
+  c.logits = logits;
+  c.type = type;
+  c.T = T;
+  c.ld = ld;
+  c.max_m = max_m;
+  c.E = E;
+  c.k = top_k;
+  c.renorm = renormalise != 0;
+  c.align = align;
+  c.coef = loss_coef;
+  c.mask = token_mask;
+  c.ids = expert_ids;
+  c.counts = counts;
+  c.routed = routed;
+  c.offsets = group_offsets;
+  c.slots = slots;
+  c.weights = weights;
+  c.prob_sum = prob_sum;
+  c.loss = loss;
+  c.workspace = workspace;
+  return FP8G_OK;
+}
+
+fp8g_status route_bwd_call(const void* logits, int type, int64_t T, int E, int64_t ld, const int32_t* expert_ids,
+                           int top_k, int renormalise, float loss_coef, const float* d_weights,
+                           const float* d_loss, const int32_t* counts, const int32_t* routed, void* d_logits,
+                           int64_t ld_d, RouteBwdCall& c) {
+  const fp8g_status s = route_sizes(type, T, E, ld, top_k);
+  if (s != FP8G_OK) return s;
+  if (ld_d < E) return FP8G_ERR_STRIDE;
+  c.T = T;
+  if (T == 0) return FP8G_OK;
+  if (!logits || !expert_ids || !counts || !routed || !d_logits) return FP8G_ERR_NULL_PTR;
+  if (!aligned(logits, type_size(type)) || !aligned(d_logits, type_size(type)) ||
+      !aligned(expert_ids, 4) || !aligned(d_weights, 4) || !aligned(d_loss, 4) ||
+      !aligned(counts, 4) || !aligned(routed, 4))
+    return FP8G_ERR_ALIGN;
+  c.logits = logits;
+  c.type = type;
+  c.ld = ld;
+  c.ldd = ld_d;
+  c.E = E;
+  c.k = top_k;
+  c.renorm = renormalise != 0;
+  c.coef = loss_coef;
+  c.ids = expert_ids;
+  c.counts = counts;
+  c.routed = routed;
+  c.dw = d_weights;
+  c.dloss = d_loss;
+  c.d_logits = d_logits;
+  return FP8G_OK;
+}
+
 fp8g_status list_ok(const void* const* grads, const int64_t* numels, const int* types, int n) {
   if (n < 0) return FP8G_ERR_SHAPE;
   if (n > 0 && (!grads || !numels || !types)) return FP8G_ERR_NULL_PTR;
@@ -88,43 +162,13 @@ fp8g_status moe_route(const void* logits, int type, int64_t T, int E, int64_t ld
                       int32_t* counts, int32_t* routed, float* prob_sum, float* loss,
                       int32_t* group_offsets, int32_t* slots, void* workspace,
                       size_t workspace_bytes, hipStream_t stream) {
-  const fp8g_status s = route_sizes(type, T, E, ld, top_k);
+  RouteCall c;
+  const fp8g_status s =
+      route_call(logits, type, T, E, ld, token_mask, top_k, renormalise, loss_coef, align, max_m, expert_ids,
+                 weights, counts, routed, prob_sum, loss, group_offsets, slots, workspace, workspace_bytes, c);
   if (s != FP8G_OK) return s;
-  if (align < 1 || max_m < 0) return FP8G_ERR_SHAPE;
-  if (max_m > kInt31 / E || (int64_t)align > kInt31 / E ||
-      T * top_k > kInt31 - (int64_t)E * align)
-    return FP8G_ERR_UNSUPPORTED;
-  if (!counts || !routed || !prob_sum || !loss || !group_offsets) return FP8G_ERR_NULL_PTR;
-  if (T > 0 && (!logits || !expert_ids || !weights || !slots)) return FP8G_ERR_NULL_PTR;
-  if (!aligned(logits, type_size(type)) || !aligned(expert_ids, 4) || !aligned(weights, 4) ||
-      !aligned(counts, 4) || !aligned(routed, 4) || !aligned(prob_sum, 4) || !aligned(loss, 4) ||
-      !aligned(group_offsets, 4) || !aligned(slots, 4) || !aligned(workspace, 16))
-    return FP8G_ERR_ALIGN;
-  if (workspace_bytes < route_workspace_bytes(T, E)) return FP8G_ERR_WORKSPACE;
-  if (!workspace && workspace_bytes != 0) return FP8G_ERR_NULL_PTR;
   DeviceInfo dev;
   if (current_device_info(&dev) != 0) return FP8G_ERR_DEVICE;
-  RouteCall c;
-  c.logits = logits;
-  c.type = type;
-  c.T = T;
-  c.ld = ld;
-  c.max_m = max_m;
-  c.E = E;
-  c.k = top_k;
-  c.renorm = renormalise != 0;
-  c.align = align;
-  c.coef = loss_coef;
-  c.mask = token_mask;
-  c.ids = expert_ids;
-  c.counts = counts;
-  c.routed = routed;
-  c.offsets = group_offsets;
-  c.slots = slots;
-  c.weights = weights;
-  c.prob_sum = prob_sum;
-  c.loss = loss;
-  c.workspace = workspace;
   return launched(launch_route(c, stream));
 }
 
@@ -133,34 +177,60 @@ fp8g_status moe_route_backward(const void* logits, int type, int64_t T, int E, i
                                float loss_coef, const float* d_weights, const float* d_loss,
                                const int32_t* counts, const int32_t* routed, void* d_logits,
                                int64_t ld_d, hipStream_t stream) {
-  const fp8g_status s = route_sizes(type, T, E, ld, top_k);
-  if (s != FP8G_OK) return s;
-  if (ld_d < E) return FP8G_ERR_STRIDE;
-  if (T == 0) return FP8G_OK;
-  if (!logits || !expert_ids || !counts || !routed || !d_logits) return FP8G_ERR_NULL_PTR;
-  if (!aligned(logits, type_size(type)) || !aligned(d_logits, type_size(type)) ||
-      !aligned(expert_ids, 4) || !aligned(d_weights, 4) || !aligned(d_loss, 4) ||
-      !aligned(counts, 4) || !aligned(routed, 4))
-    return FP8G_ERR_ALIGN;
+  RouteBwdCall c;
+  const fp8g_status s = route_bwd_call(logits, type, T, E, ld, expert_ids, top_k, renormalise, loss_coef, d_weights,
+                                       d_loss, counts, routed, d_logits, ld_d, c);
+  if (s != FP8G_OK || T == 0) return s;
   DeviceInfo dev;
   if (current_device_info(&dev) != 0) return FP8G_ERR_DEVICE;
-  RouteBwdCall c;
-  c.logits = logits;
-  c.type = type;
-  c.T = T;
-  c.ld = ld;
-  c.ldd = ld_d;
-  c.E = E;
-  c.k = top_k;
-  c.renorm = renormalise != 0;
-  c.coef = loss_coef;
-  c.ids = expert_ids;
-  c.counts = counts;
-  c.routed = routed;
-  c.dw = d_weights;
-  c.dloss = d_loss;
-  c.d_logits = d_logits;
   return launched(launch_route_backward(c, stream, dev.cu_count));
+}
+
+fp8g_status moe_route_scored(const void* logits, int type, int64_t T, int E, int64_t ld, const float* bias,
+                             int score, int groups, int open_groups, int group_best, const uint8_t* token_mask,
+                             int top_k, int renormalise, float scale, float loss_coef, int align,
+                             int64_t max_m, int32_t* expert_ids, float* weights, int32_t* counts,
+                             int32_t* routed, float* prob_sum, float* loss, int32_t* group_offsets,
+                             int32_t* slots, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  ScoredCall c;
+  const fp8g_status s =
+      route_call(logits, type, T, E, ld, token_mask, top_k, renormalise, loss_coef, align, max_m, expert_ids,
+                 weights, counts, routed, prob_sum, loss, group_offsets, slots, workspace, workspace_bytes,
+                 c.route);
+  if (s != FP8G_OK) return s;
+  if (groups < 1 || E % groups != 0 || open_groups < 1 || open_groups > groups || group_best < 1 ||
+      group_best > E / groups || top_k > open_groups * (E / groups))
+    return FP8G_ERR_SHAPE;
+  if ((score != FP8G_SCORE_SIGMOID && score != FP8G_SCORE_SOFTMAX) || groups > 32 || group_best > 2)
+    return FP8G_ERR_UNSUPPORTED;
+  if (!aligned(bias, 4)) return FP8G_ERR_ALIGN;
+  DeviceInfo dev;
+  if (current_device_info(&dev) != 0) return FP8G_ERR_DEVICE;
+  c.bias = bias;
+  c.score = score;
+  c.groups = groups;
+  c.open = open_groups;
+  c.best = group_best;
+  c.scale = scale;
+  return launched(launch_route_scored(c, stream));
+}
+
+fp8g_status moe_route_scored_backward(const void* logits, int type, int64_t T, int E, int64_t ld, int score,
+                                      const int32_t* expert_ids, int top_k, int renormalise, float scale,
+                                      float loss_coef, const float* d_weights, const float* d_loss,
+                                      const int32_t* counts, const int32_t* routed, void* d_logits,
+                                      int64_t ld_d, hipStream_t stream) {
+  ScoredBwdCall c;
+  const fp8g_status s = route_bwd_call(logits, type, T, E, ld, expert_ids, top_k, renormalise, loss_coef, d_weights,
+                                       d_loss, counts, routed, d_logits, ld_d, c.route);
+  if (s != FP8G_OK) return s;
+  if (score != FP8G_SCORE_SIGMOID && score != FP8G_SCORE_SOFTMAX) return FP8G_ERR_UNSUPPORTED;
+  if (T == 0) return FP8G_OK;
+  DeviceInfo dev;
+  if (current_device_info(&dev) != 0) return FP8G_ERR_DEVICE;
+  c.score = score;
+  c.scale = scale;
+  return launched(launch_route_scored_backward(c, stream, dev.cu_count));
 }
 
 fp8g_status fp8_quantize_transpose(const void* x, int type, int64_t rows, int64_t cols,
