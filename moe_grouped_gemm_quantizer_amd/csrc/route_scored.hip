@@ -22,12 +22,14 @@
 namespace fp8g {
 namespace {
 
-constexpr int MAX_GROUPS = 32;
+constexpr uint32_t MAX_GROUPS = 32;
 
 struct ScoredArgs {
   RouteArgs r;
   const float* bias;
   int score, groups, open, best, size;                 // size: experts of a group
+  uint32_t per_size;                                   // e / size = e per_size >> 20
+  int vec_bias, part_bits;
   float scale;
 };
 
@@ -136,7 +138,7 @@ __device__ __forceinline__ int choose64(const T* __restrict__ row, const ScoredA
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     const int e = l + 64 * q;
-    v[q] = (may >> q & 1) ? (a.bias ? s[q] + (double)a.bias[e] : s[q]) : none;
+    v[q] = (may >> q & 1) ? (a.bias ? s[q] + (double)a.bias[e] : (a.open < a.groups ? s[q] : 0.0)) : none;
     if (!(v[q] > none)) v[q] = none;                   // (NaN)
   }
   if (a.open < a.groups) {
@@ -212,15 +214,15 @@ __device__ __forceinline__ int choose64(const T* __restrict__ row, const ScoredA
 
 // One block of 64 tokens per workgroup, LPR lanes a row, as in route.hip.
 template <typename T, int LPR, int VPT, int NT>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, NT == 512 ? 4 : 1)
 route_scored_rows_kernel(ScoredArgs a) {
   using L = Lay<T, LPR, VPT>;
   constexpr int AT_ONCE = NT / LPR, WAVES = NT / 64;
   constexpr int BITS = LPR * VPT <= 256 ? 8 : 10;      // of a key, for the expert's number
   constexpr uint32_t LOW = (1u << BITS) - 1u;
-  // Two values are surely in the keys' order from NEAR on: each is off by up to 4 ulp of the
-  // score, half a one of the sum with the bias and 1.5 of the key's forming, at 2^-24 of the
-  // range's half M = 2^(31 - BITS) units.
+  // Two values are surely in the keys' order where these differ by more than NEAR: each is off by up to
+  // 4 ulp of the score and half a one of the sum with the bias, in units of 2^-23 of the range's
+  // half (2^-21 for 10 BITS) 2.25 at most, and by 4 of the key's own forming.
   constexpr uint32_t NEAR = BITS == 8 ? 16 : 8;
   __shared__ uint32_t took[2][MAX_E];
   __shared__ short chosen[ROWS][MAX_K];
@@ -229,17 +231,28 @@ route_scored_rows_kernel(ScoredArgs a) {
   __shared__ int wave_sum[WAVES];
   __shared__ int n_routed, n_again;
   __shared__ short again[ROWS];                        // rows that are done again in 64 bits
-  __shared__ float values[AT_ONCE][LPR * VPT];         // where groups are chosen
+  __shared__ __attribute__((aligned(8))) float values[AT_ONCE][LPR * VPT];     // where groups are chosen
   __shared__ float group_value[AT_ONCE][MAX_GROUPS];
+  __shared__ __attribute__((aligned(16))) uint32_t group_key[AT_ONCE][MAX_GROUPS];
   const int E = a.r.E, k = a.r.k;
   for (int e = threadIdx.x; e < E; e += NT) took[0][e] = took[1][e] = 0u;
   if (threadIdx.x == 0) n_routed = n_again = 0;
+  // (past the last group: none)
+  for (int i = threadIdx.x; i < AT_ONCE * (int)MAX_GROUPS; i += NT) (&group_key[0][0])[i] = 0u;
   __syncthreads();
   const int l = threadIdx.x & (LPR - 1), lane = threadIdx.x & 63;
   const int at_row = threadIdx.x / LPR;
   const int64_t block = (int64_t)a.r.block0 + blockIdx.x;
   const int64_t t0 = block * ROWS;
   const bool by_value = a.bias || a.open < a.groups;
+  const bool quads = VPT % 4 == 0 && a.size % 4 == 0;  // (a lane's values lie in fours side by side)
+  const int n_quads = a.size / 4;
+  uint32_t group_of[(VPT + 3) / 4];                    // of a lane's experts, a byte each
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const uint32_t g = min((uint32_t)L::at(v, l) * a.per_size >> 20, MAX_GROUPS - 1u);
+    group_of[v / 4] = (v % 4 ? group_of[v / 4] : 0u) | g << (8 * (v % 4));
+  }
   const auto take = [&](int64_t t, int r, int id, float w) __attribute__((always_inline)) {
     a.r.ids[t * k + l] = id;
     a.r.weights[t * k + l] = w;
@@ -248,136 +261,228 @@ route_scored_rows_kernel(ScoredArgs a) {
   };
   float acc[VPT], b[VPT];
 #pragma unroll
-  for (int v = 0; v < VPT; ++v) {
-    acc[v] = 0.0f;
-    const int e = L::at(v, l);
-    b[v] = a.bias && e < E ? a.bias[e] : 0.0f;
+  for (int v = 0; v < VPT; ++v) acc[v] = b[v] = 0.0f;
+  if (a.bias) {
+    constexpr int W = VPT % 4 == 0 ? 4 : VPT;          // (a lane's values lie in as many side by side)
+#pragma unroll
+    for (int v = 0; v < VPT; v += W) {
+      const int e0 = L::at(v, l);
+      if (a.vec_bias && e0 + W <= E) {
+        const Pack<float, W> p = *reinterpret_cast<const Pack<float, W>*>(a.bias + e0);
+#pragma unroll
+        for (int w = 0; w < W; ++w) b[v + w] = p.v[w];
+      } else {
+#pragma unroll
+        for (int w = 0; w < W; ++w) b[v + w] = e0 + w < E ? a.bias[e0 + w] : 0.0f;
+      }
+    }
   }
+  // the range of values, but for what the row adds to it (-inf and NaN close an expert)
+  float range = 0.0f;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const float y = __builtin_fabsf(b[v]);
+    range = __builtin_fmaxf(range, b[v] > -__builtin_inff() ? y : 0.0f);
+  }
+  range = max_lanes<LPR>(range);
+  float x[VPT];
+  bool on = false;
+  const T* row = nullptr;
+  const auto fetch = [&](int64_t t) __attribute__((always_inline)) {
+    const bool in = t < a.r.T;
+    on = in && (!a.r.mask || a.r.mask[t] != 0);
+    row = (const T*)a.r.logits + (in ? t : 0) * a.r.ld;
+    load_row<T, LPR, VPT>(row, E, l, on, a.r.vec != 0, x);
+  };
+  fetch(t0 + at_row);
   for (int r0 = 0; r0 < ROWS && t0 + r0 < a.r.T; r0 += AT_ONCE) {
     const int r = r0 + at_row;
     const int64_t t = t0 + r;
     const bool in = t < a.r.T;
-    const bool on = in && (!a.r.mask || a.r.mask[t] != 0);
-    const T* const row = (const T*)a.r.logits + (in ? t : 0) * a.r.ld;
-    float x[VPT], s[VPT];
-    load_row<T, LPR, VPT>(row, E, l, on, a.r.vec != 0, x);
-    const RowSum sum = row_scores<LPR, VPT>(x, a.score, s);
-    int id;
-    float xj;                                          // the choice's logit
-    bool redo = false;
-    if (!by_value) {
-      id = choose<T, LPR, VPT>(x, row, l, k, xj);
-    } else {
-      // values; what is never chosen is -inf
-      float val[VPT], m = -1.0f;
+    const T* const this_row = row;
+    RowSum sum;
+    float val[VPT], m, top = -__builtin_inff();        // values (-inf or NaN: never chosen), half their range
+    {
+      float s[VPT];
+      sum = row_scores<LPR, VPT>(x, a.score, s);
+      if (by_value) {
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const float y = s[v] + b[v];
-        const bool may = x[v] > -__builtin_inff() && y > -__builtin_inff();
-        val[v] = may ? y : -__builtin_inff();
-        m = may ? __builtin_fmaxf(m, __builtin_fmaxf(__builtin_fabsf(y), s[v])) : m;
-      }
-      m = max_lanes<LPR>(m);
-      // (m < 0: nothing to choose from; no range to count in otherwise)
-      redo = m >= 0.0f && !(m > 1e-30f && m < 1e30f);
-      uint32_t open = 0xFFFFFFFFu;
-      if (a.open < a.groups) {
+        for (int v = 0; v < VPT; ++v) val[v] = x[v] > -__builtin_inff() ? s[v] + b[v] : -__builtin_inff();
+        m = range + (a.score == SCORE_SOFTMAX ? sum.norm : 1.0f);
+      } else {
+        m = 0.0f;
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) values[at_row][L::at(v, l)] = val[v];
-        wave_sync();
-        for (int g = l; g < a.groups; g += LPR) {
-          // (lanes start at different places: their groups lie banks apart)
-          float t1 = -__builtin_inff(), t2 = -__builtin_inff();
-          int i = lane % a.size;
-          for (int n = 0; n < a.size; ++n) {
-            const float y = values[at_row][g * a.size + i];
-            t2 = __builtin_fmaxf(t2, __builtin_fminf(t1, y));
-            t1 = __builtin_fmaxf(t1, y);
-            i = i + 1 == a.size ? 0 : i + 1;
-          }
-          group_value[at_row][g] = a.best > 1 && t2 > -__builtin_inff() ? t1 + t2 : t1;
+        for (int v = 0; v < VPT; ++v) {
+          val[v] = x[v] + 0.0f;
+          m = __builtin_fmaxf(m, x[v] > -__builtin_inff() ? __builtin_fabsf(val[v]) : 0.0f);
         }
-        wave_sync();
-        // a group's rank among all; the least open and the largest closed value
-        float least = __builtin_inff(), most = -__builtin_inff();
-        uint32_t bits = 0u;
-        for (int g = l; g < a.groups; g += LPR) {
-          const float mine = group_value[at_row][g];
-          int rank = 0;
-          for (int h = 0; h < a.groups; ++h) {
-            const float y = group_value[at_row][h];
-            rank += y > mine || (y == mine && h < g) ? 1 : 0;
-          }
-          const bool is_open = rank < a.open && mine > -__builtin_inff();
-          bits |= is_open ? 1u << g : 0u;
-          if (is_open) least = __builtin_fminf(least, mine);
-          else most = __builtin_fmaxf(most, mine);
-        }
-        open = reduce_u32<LPR>(bits, [](uint32_t p, uint32_t q) { return p | q; });
-        least = reduce_f32<LPR>(least, [](float p, float q) { return __builtin_fminf(p, q); });
-        most = max_lanes<LPR>(most);
-        // (two values a side, each off by 5.5 2^-24 of m at most, and their sums' rounding)
-        redo = redo || (most > -__builtin_inff() && !(least - most > m * 0x1p-19f));
-        wave_sync();
+        m = max_lanes<LPR>(m);
       }
-      const float to_units = (float)(1u << (31 - BITS)) / m;
-      uint32_t key[VPT];
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int e = L::at(v, l);
-        const bool may = val[v] > -__builtin_inff() && (open >> (a.open < a.groups ? e / a.size : 0) & 1u);
-        const uint32_t u = min((uint32_t)((val[v] + m) * to_units) + 1u, (1u << (32 - BITS)) - 1u);
-        key[v] = may ? u << BITS | (LOW - (uint32_t)e) : 0u;
-      }
-      // the largest keys one after the other: the next one is the largest below the last, and
-      // with d = key - last in wrapping arithmetic every key below it has a larger d than
-      // every key from it on
-      const auto umax = [](uint32_t p, uint32_t q) { return p > q ? p : q; };
-      uint32_t last = 0u, mine = 0u;
-      const auto next = [&]() __attribute__((always_inline)) {
-        uint32_t d = key[0] - last;
+      for (int v = 0; v < VPT; ++v) top = __builtin_fmaxf(top, val[v]);
+      top = max_lanes<LPR>(top);
+      // (a token that chooses nothing is not in the sums, unless it is NaN)
+      const bool bad = sum.share != sum.share;
+      const bool little = a.score == SCORE_SIGMOID && top > -__builtin_inff() && !bad &&
+                          !(sum.share <= 1.0f / LITTLE && sum.share > 0.0f);
+      const float share = (top > -__builtin_inff() && !little) || bad ? sum.share : 0.0f;
 #pragma unroll
-        for (int v = 1; v < VPT; ++v) d = umax(d, key[v] - last);
-        d = reduce_u32<LPR>(d, umax);
-        const uint32_t n = last + d;
-        const bool none = n == 0u || (last != 0u && n >= last);
-        last = none ? last : n;
-        return none ? 0u : n;
-      };
-      for (int j = 0; j < k; ++j) {
-        const uint32_t n = next();
-        if (l == j) mine = n;
+      for (int v = 0; v < VPT; ++v) acc[v] = __builtin_fmaf(s[v], share, acc[v]);  // (s is NaN in NaN rows alone)
+      if (__ballot(little)) {                          // (uniform over the wave)
+        float e[VPT], most;
+        const float norm = row_softmax<LPR, VPT>(x, most, e);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) acc[v] += little ? e[v] * norm : 0.0f;
       }
-      const uint32_t extra = next();
-      id = mine ? (int)(LOW - (mine & LOW)) : -1;
-      const int ie = extra ? (int)(LOW - (extra & LOW)) : -1;
-      xj = id >= 0 ? to_f32(row[id]) : 0.0f;
-      const float bj = id >= 0 && a.bias ? a.bias[id] : 0.0f;
-      const float xe = ie >= 0 ? to_f32(row[ie]) : 0.0f, be = ie >= 0 && a.bias ? a.bias[ie] : 0.0f;
-      // (LPR lanes: the one behind the k-th takes the next candidate)
-      uint32_t kn = (uint32_t)__shfl_down((int)mine, 1, LPR);
-      float xn = __shfl_down(xj, 1, LPR), bn = __shfl_down(bj, 1, LPR);
-      if (l == k - 1) {
-        kn = extra;
-        xn = xe;
-        bn = be;
-      }
-      const bool close = l < k && kn && (mine >> BITS) - (kn >> BITS) <= NEAR && !(xj == xn && bj == bn);
-      redo = redo || reduce_u32<LPR>(close ? 1u : 0u, umax) != 0u;
     }
-    const bool routed = __shfl(id, 0, LPR) >= 0;
+    // (the next rows' logits are on their way while these choose)
+    if (r0 + AT_ONCE < ROWS) fetch(t + AT_ONCE);
+    // (no range to count in)
+    bool redo = top > -__builtin_inff() && !(m > 1e-30f && m < 1e30f);
+    uint32_t open = 0xFFFFFFFFu;
+    if (a.open < a.groups) {
+      // the values, or where groups are whole quads of experts each quad's two largest
+      if (quads) {
+        if constexpr (VPT % 4 == 0) {
+#pragma unroll
+          for (int v = 0; v < VPT; v += 4) {
+            float c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = __builtin_fmaxf(val[v + i], -__builtin_inff());       // (NaN)
+            const float p = __builtin_fmaxf(c[0], c[1]), q = __builtin_fminf(c[0], c[1]);
+            const float u = __builtin_fmaxf(c[2], c[3]), w = __builtin_fminf(c[2], c[3]);
+            Pack<float, 2> y;
+            y.v[0] = __builtin_fmaxf(p, u);
+            y.v[1] = __builtin_fmaxf(__builtin_fminf(p, u), __builtin_fmaxf(q, w));
+            *reinterpret_cast<Pack<float, 2>*>(&values[at_row][L::at(v, l) / 2]) = y;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) values[at_row][L::at(v, l)] = __builtin_fmaxf(val[v], -__builtin_inff());
+      }
+      wave_sync();
+      // 1 << part_bits lanes a group, each with every so manyeth of its values
+      const int parts = 1 << a.part_bits, part = l & (parts - 1);
+      float least = __builtin_inff(), most = -__builtin_inff();
+      uint32_t bits = 0u;
+      for (int g0 = 0; g0 < a.groups; g0 += LPR >> a.part_bits) {
+        const int g = g0 + (l >> a.part_bits);
+        float t1 = -__builtin_inff(), t2 = -__builtin_inff();
+        if (g < a.groups) {
+          if (quads) {
+            const Pack<float, 2>* const from = reinterpret_cast<const Pack<float, 2>*>(&values[at_row][2 * g * n_quads]);
+            for (int i = part; i < n_quads; i += parts) {
+              const Pack<float, 2> y = from[i];
+              t2 = __builtin_fmaxf(__builtin_fmaxf(t2, y.v[1]), __builtin_fminf(t1, y.v[0]));
+              t1 = __builtin_fmaxf(t1, y.v[0]);
+            }
+          } else {
+            for (int i = part; i < a.size; i += parts) {
+              const float y = values[at_row][g * a.size + i];
+              t2 = __builtin_fmaxf(t2, __builtin_fminf(t1, y));
+              t1 = __builtin_fmaxf(t1, y);
+            }
+          }
+        }
+        for (int o = 1; o < parts; o <<= 1) {
+          const float u1 = __shfl_xor(t1, o, LPR), u2 = __shfl_xor(t2, o, LPR);
+          t2 = __builtin_fmaxf(__builtin_fmaxf(t2, u2), __builtin_fminf(t1, u1));
+          t1 = __builtin_fmaxf(t1, u1);
+        }
+        const float value = a.best > 1 && t2 > -__builtin_inff() ? t1 + t2 : t1;
+        // its order among the groups' values: as a whole number, the lower group first where the five bits
+        // that give way to its number decide (nearer than what is done again); 0: nothing to choose
+        if (part == 0 && g < a.groups) {
+          group_value[at_row][g] = value;
+          group_key[at_row][g] = order_key(value) < 32u ? 0u : (order_key(value) & ~31u) | (31u - (uint32_t)g);
+        }
+      }
+      wave_sync();
+      // a group's rank among all; the least open and the largest closed value
+      for (int g = l; g < a.groups; g += LPR) {
+        const uint32_t mine = group_key[at_row][g];
+        int rank = 0;
+        for (int h = 0; h < a.groups; h += 4) {
+          const Pack<uint32_t, 4> y = *reinterpret_cast<const Pack<uint32_t, 4>*>(&group_key[at_row][h]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) rank += y.v[i] > mine ? 1 : 0;
+        }
+        const bool is_open = rank < a.open && mine != 0u;
+        const float value = group_value[at_row][g];
+        bits |= is_open ? 1u << g : 0u;
+        if (is_open) least = __builtin_fminf(least, value);
+        else most = __builtin_fmaxf(most, value);
+      }
+      open = reduce_u32<LPR>(bits, [](uint32_t p, uint32_t q) { return p | q; });
+      least = reduce_f32<LPR>(least, [](float p, float q) { return __builtin_fminf(p, q); });
+      most = max_lanes<LPR>(most);
+      // (two values a side, each off by 5.5 2^-24 of m at most, their sums' rounding and the keys' five bits)
+      redo = redo || (most > -__builtin_inff() && !(least - most > m * 0x1p-17f));
+      wave_sync();
+    }
+    // keys: the value in units of the range's 2^(32 - BITS)th part, from 4 to below all; a -inf gives 0
+    // units, and a key below FIRST is never chosen
+    constexpr uint32_t FIRST = 1u << BITS;
+    const float units = (float)((1u << (31 - BITS)) - 16u) * __builtin_amdgcn_rcpf(__builtin_fmaxf(m, 1e-30f));
+    const float least_units = __builtin_fmaf(m, units, 4.0f);
+    const uint32_t number = LOW - (uint32_t)L::at(0, l);
+    uint32_t key[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const uint32_t u = (uint32_t)__builtin_fmaf(val[v], units, least_units);
+      key[v] = (u << BITS) + number - (uint32_t)L::at(v, 0);
+    }
+    if (a.open < a.groups) {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const uint32_t g = group_of[v / 4] >> (8 * (v % 4)) & 0x1Fu;
+        key[v] &= (uint32_t)__builtin_amdgcn_sbfe((int)open, g, 1u);
+      }
+    }
+    // the largest keys one after the other: the next one is the largest below the last, and
+    // with d = key - last in wrapping arithmetic every key below it has a larger d than
+    // every key from it on
+    const auto umax = [](uint32_t p, uint32_t q) { return p > q ? p : q; };
+    uint32_t last = 0u, mine = 0u;
+    const auto next = [&]() __attribute__((always_inline)) {
+      uint32_t d = key[0] - last;
+#pragma unroll
+      for (int v = 1; v < VPT; ++v) d = umax(d, key[v] - last);
+      d = reduce_u32<LPR>(d, umax);
+      const uint32_t n = last + d;
+      const bool none = n < FIRST || (last != 0u && n >= last);
+      last = none ? last : n;
+      return none ? 0u : n;
+    };
+    for (int j = 0; j < k; ++j) {
+      const uint32_t n = next();
+      if (l == j) mine = n;
+    }
+    const uint32_t extra = next();
+    const int id = mine ? (int)(LOW - (mine & LOW)) : -1;
+    const int ie = extra ? (int)(LOW - (extra & LOW)) : -1;
+    const float xj = id >= 0 ? to_f32(this_row[id]) : 0.0f;
+    const float bj = id >= 0 && a.bias ? a.bias[id] : 0.0f;
+    const float xe = ie >= 0 ? to_f32(this_row[ie]) : 0.0f, be = ie >= 0 && a.bias ? a.bias[ie] : 0.0f;
+    // (LPR lanes: the one behind the k-th takes the next candidate)
+    uint32_t kn = (uint32_t)__shfl_down((int)mine, 1, LPR);
+    float xn = __shfl_down(xj, 1, LPR), bn = __shfl_down(bj, 1, LPR);
+    if (l == k - 1) {
+      kn = extra;
+      xn = xe;
+      bn = be;
+    }
+    const bool close = l < k && kn && (mine >> BITS) - (kn >> BITS) <= NEAR && !(xj == xn && bj == bn);
+    redo = redo || reduce_u32<LPR>(close ? 1u : 0u, umax) != 0u;
     float w = id >= 0 ? score_of(xj, a.score, sum) : 0.0f;
     if (a.r.renorm) w = chosen_share<LPR>(w, xj, id >= 0);
     const bool bad = sum.share != sum.share;
     w = bad ? sum.share : w * a.scale;
-    // (a token that chooses nothing is not in the sums, unless it is NaN)
-    float share = routed || bad ? sum.share : 0.0f;
-    if (a.score == SCORE_SIGMOID)
-      little_scores<LPR, VPT>(x, routed && !(sum.share <= 1.0f / LITTLE && sum.share > 0.0f) && !bad, s, share);
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) acc[v] += share != 0.0f ? s[v] * share : 0.0f;
-    if (in && l == 0 && routed) atomicAdd(&n_routed, 1);
-    if (in && l < k && !redo) take(t, r, id, w);
+    if (in && l < k && !redo) {
+      take(t, r, id, w);
+      if (l == 0 && id >= 0) atomicAdd(&n_routed, 1);
+    }
     if (in && l == 0 && redo) again[atomicAdd(&n_again, 1)] = (short)r;
   }
   __syncthreads();
@@ -402,6 +507,7 @@ route_scored_rows_kernel(ScoredArgs a) {
       a.r.weights[t * k + lane] = w;
       chosen[r][lane] = (short)id;
       if (id >= 0) atomicOr(&took[r >> 5][id], 1u << (r & 31));
+      if (lane == 0 && id >= 0) atomicAdd(&n_routed, 1);
     }
   }
   finish_block<T, LPR, VPT, NT>(a.r, block, acc, took, chosen, psum, count, off, wave_sum, n_routed);
@@ -539,7 +645,7 @@ struct Pick {
   RowsFn rows;
   int rows_threads;
   BwdFn bwd;
-  int rows_at_once;
+  int rows_at_once, lanes;
 };
 template <typename T, int NT>
 Pick pick_for(int E) {
@@ -548,7 +654,7 @@ Pick pick_for(int E) {
 #define FP8G_PICK(LPR_, VPT_)                                                                    \
   Pick { route_scored_rows_kernel<T, LPR_, VPT_, LPR_ == 16 && VPT_ >= 12 ? WIDE : NT>,          \
          LPR_ == 16 && VPT_ >= 12 ? WIDE : NT, route_scored_backward_kernel<T, LPR_, VPT_>,      \
-         THREADS / LPR_ }
+         THREADS / LPR_, LPR_ }
   if (E <= 16) return FP8G_PICK(16, 1);
   if (E <= 32) return FP8G_PICK(16, 2);
   if (E <= 64) return FP8G_PICK(16, 4);
@@ -584,10 +690,14 @@ hipError_t launch_route_scored(const ScoredCall& c, hipStream_t stream) {
   a.open = c.open;
   a.best = c.best;
   a.size = c.route.E / c.groups;
+  a.per_size = (1u << 20) / (uint32_t)a.size + 1u;     // (exact for e below 1024: e size < 2^20)
+  a.vec_bias = (uintptr_t)c.bias % 16 == 0;
   a.scale = c.scale;
   const int64_t nblk = (c.route.T + ROWS - 1) / ROWS;
   if (nblk == 0) return launch_route_places(c.route, stream);
   const Pick p = pick(c.route.type, c.route.E, c.route.T);
+  a.part_bits = 0;
+  while (c.groups << (a.part_bits + 1) <= p.lanes) ++a.part_bits;
   const int64_t most = rows_blocks_max(p.rows_threads);
   for (int64_t b = 0; b < nblk; b += most) {
     a.r.block0 = (int)b;
