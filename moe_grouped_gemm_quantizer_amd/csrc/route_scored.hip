@@ -29,7 +29,8 @@ struct ScoredArgs {
   const float* bias;
   int score, groups, open, best, size;                 // size: experts of a group
   uint32_t per_size;                                   // e / size = e per_size >> 20
-  int vec_bias, part_bits;
+  int vec_bias;
+  int part_bits, part_bits64;                          // 1 << these lanes a group, of a row's and of a wave's
   float scale;
 };
 
@@ -102,113 +103,131 @@ __device__ __forceinline__ float chosen_share(float s, float x, bool on) {
   return on ? s / z : 0.0f;
 }
 
+// Largest of a wave's values in 64 bits, in all lanes (by lane exchanges that do not go through LDS:
+// a row that is done again is one chain of these, and its workgroup waits for it).
+template <class F>
+__device__ __forceinline__ double both_words(double x, F f) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  return __builtin_bit_cast(double, (uint64_t)f((uint32_t)u) | (uint64_t)f((uint32_t)(u >> 32)) << 32);
+}
+__device__ __forceinline__ double max_wave(double x) {
+  x = fmax(x, both_words(x, [](uint32_t w) { return ring16<8>(w); }));
+  x = fmax(x, both_words(x, [](uint32_t w) { return ring16<4>(w); }));
+  x = fmax(x, both_words(x, [](uint32_t w) { return ring16<2>(w); }));
+  x = fmax(x, both_words(x, [](uint32_t w) { return ring16<1>(w); }));
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const auto words = [](uint32_t lo, uint32_t hi) { return __builtin_bit_cast(double, (uint64_t)lo | (uint64_t)hi << 32); };
+  const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+  x = fmax(words(lo[0], hi[0]), words(lo[1], hi[1]));
+  const uint64_t w = __builtin_bit_cast(uint64_t, x);
+  const auto lo2 = __builtin_amdgcn_permlane32_swap((uint32_t)w, (uint32_t)w, false, false);
+  const auto hi2 = __builtin_amdgcn_permlane32_swap((uint32_t)(w >> 32), (uint32_t)(w >> 32), false, false);
+  return fmax(words(lo2[0], hi2[0]), words(lo2[1], hi2[1]));
+}
+
 // One row by a wave in 64 bits: lane l holds experts l, l + 64, ... Lane j gets the j-th choice
-// (-1: none) and its score.
+// (-1: none) and its score. high, low: LDS of the wave's own, a word each for every expert; 1 <<
+// part_bits lanes a group.
 template <typename T, int PER>
-__device__ __forceinline__ int choose64(const T* __restrict__ row, const ScoredArgs& a, int l, double& score) {
+__device__ __forceinline__ int choose64(const T* __restrict__ row, const ScoredArgs& a, int l, uint32_t* high,
+                                        uint32_t* low, int part_bits, double& score) {
   const int E = a.r.E, k = a.r.k;
   const double none = -__builtin_inf();
-  double s[PER], v[PER];
-  double top = none;
+  double v[PER], top = none, z = 1.0;
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     const int e = l + 64 * q;
-    s[q] = e < E ? (double)to_f32(row[e]) : none;
-    top = fmax(top, s[q]);
+    v[q] = e < E ? (double)to_f32(row[e]) : none;
+    top = fmax(top, v[q]);
   }
-  uint32_t may = 0;
-#pragma unroll
-  for (int q = 0; q < PER; ++q) may |= (s[q] > none ? 1u : 0u) << q;
   if (a.score == SCORE_SOFTMAX) {
+    top = max_wave(top);
+    top = top > none ? top : 0.0;
+    z = 0.0;
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) top = fmax(top, __shfl_xor(top, o));
-    double z = 0.0;
-#pragma unroll
-    for (int q = 0; q < PER; ++q) {
-      s[q] = l + 64 * q < E ? exp(s[q] - (top > none ? top : 0.0)) : 0.0;
-      z += s[q];
-    }
+    for (int q = 0; q < PER; ++q) z += l + 64 * q < E ? exp(v[q] - top) : 0.0;
     z = sum_wave(z);
-#pragma unroll
-    for (int q = 0; q < PER; ++q) s[q] = s[q] / z;
-  } else {
-#pragma unroll
-    for (int q = 0; q < PER; ++q) s[q] = 1.0 / (1.0 + exp(-s[q]));
   }
-#pragma unroll
-  for (int q = 0; q < PER; ++q) {
-    const int e = l + 64 * q;
-    v[q] = (may >> q & 1) ? (a.bias ? s[q] + (double)a.bias[e] : (a.open < a.groups ? s[q] : 0.0)) : none;
-    if (!(v[q] > none)) v[q] = none;                   // (NaN)
-  }
-  if (a.open < a.groups) {
-    double mine = none;                                // lane g: group g's value
-    for (int g = 0; g < a.groups; ++g) {
-      double t1 = none, t2 = none;
-#pragma unroll
-      for (int q = 0; q < PER; ++q) {
-        const int e = l + 64 * q;
-        const double x = e >= g * a.size && e < (g + 1) * a.size ? v[q] : none;
-        t2 = fmax(t2, fmin(t1, x));
-        t1 = fmax(t1, x);
-      }
-#pragma unroll
-      for (int o = 32; o >= 1; o >>= 1) {
-        const double u1 = __shfl_xor(t1, o), u2 = __shfl_xor(t2, o);
-        t2 = fmax(fmax(t2, u2), fmin(t1, u1));
-        t1 = fmax(t1, u1);
-      }
-      const double value = a.best > 1 && t2 > none ? t1 + t2 : t1;
-      mine = l == g ? value : mine;
-    }
-    int rank = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const double x = __shfl(mine, g);
-      rank += x > mine || (x == mine && g < l) ? 1 : 0;
-    }
-    const uint64_t open = __ballot(l < a.groups && rank < a.open && mine > none);
+  const auto score64 = [&](double x) __attribute__((always_inline)) {
+    return a.score == SCORE_SOFTMAX ? exp(x - top) / z : 1.0 / (1.0 + exp(-x));
+  };
+  const bool by_value = a.bias || a.open < a.groups;
+  if (by_value) {
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const int e = l + 64 * q;
-      if (e < E && !(open >> (e / a.size) & 1)) v[q] = none;
+      const double y = score64(v[q]) + (a.bias && e < E ? (double)a.bias[e] : 0.0);
+      v[q] = v[q] > none && y > none ? y : none;       // (NaN: neither)
     }
-  }
-  if (!a.bias) {                                       // (the logits tell more of what is near 0 or 1)
+  } else {
 #pragma unroll
-    for (int q = 0; q < PER; ++q)
-      if (v[q] > none) v[q] = (double)to_f32(row[l + 64 * q]);
+    for (int q = 0; q < PER; ++q) v[q] = v[q] > none ? v[q] : none;
+  }
+  if (a.open < a.groups) {
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const int e = l + 64 * q;
+      const uint64_t u = __builtin_bit_cast(uint64_t, v[q]);
+      if (e < E) {
+        high[e] = (uint32_t)(u >> 32);
+        low[e] = (uint32_t)u;
+      }
+    }
+    wave_sync();
+    const int g = l >> part_bits;
+    double t1 = none, t2 = none;
+    if (g < a.groups)
+      for (int i = l & ((1 << part_bits) - 1); i < a.size; i += 1 << part_bits) {
+        const int e = g * a.size + i;
+        const double x = __builtin_bit_cast(double, (uint64_t)low[e] | (uint64_t)high[e] << 32);
+        t2 = fmax(t2, fmin(t1, x));
+        t1 = fmax(t1, x);
+      }
+    for (int o = 1; o < 1 << part_bits; o <<= 1) {
+      const double u1 = __shfl_xor(t1, o), u2 = __shfl_xor(t2, o);
+      t2 = fmax(fmax(t2, u2), fmin(t1, u1));
+      t1 = fmax(t1, u1);
+    }
+    const double mine = a.best > 1 && t2 > none ? t1 + t2 : t1;
+    const uint64_t words = __builtin_bit_cast(uint64_t, mine);
+    int rank = 0;
+    for (int h = 0; h < a.groups; ++h) {
+      const double x = __builtin_bit_cast(
+          double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)words, h << part_bits) |
+                      (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(words >> 32), h << part_bits) << 32);
+      rank += x > mine || (x == mine && h < g) ? 1 : 0;
+    }
+    const uint64_t open = __ballot(g < a.groups && rank < a.open && mine > none);
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const int e = l + 64 * q;
+      const uint32_t of = min((uint32_t)e * a.per_size >> 20, (uint32_t)a.groups - 1u);
+      if (!(open >> (of << part_bits) & 1u)) v[q] = none;
+    }
+    if (!a.bias) {                                     // (the logits tell more of what is near 0 or 1)
+#pragma unroll
+      for (int q = 0; q < PER; ++q)
+        if (v[q] > none) v[q] = (double)to_f32(row[l + 64 * q]);
+    }
+    wave_sync();
   }
   int id = -1;
-  score = 0.0;
   for (int j = 0; j < k; ++j) {
-    double best = none, at = 0.0;
-    int e = 1 << 30;
+    double best = v[0];
 #pragma unroll
-    for (int q = PER - 1; q >= 0; --q)
-      if (v[q] > none && v[q] >= best) {
-        best = v[q];
-        at = s[q];
-        e = l + 64 * q;
-      }
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) {
-      const double ob = __shfl_xor(best, o), oa = __shfl_xor(at, o);
-      const int oe = __shfl_xor(e, o);
-      if (ob > best || (ob == best && oe < e)) {
-        best = ob;
-        at = oa;
-        e = oe;
-      }
-    }
+    for (int q = 1; q < PER; ++q) best = fmax(best, v[q]);
+    best = max_wave(best);
     if (!(best > none)) break;                         // (the same in all lanes)
-    if (l == j) {
-      id = e;
-      score = at;
-    }
+    uint32_t e = 0xFFFFFFFFu;
 #pragma unroll
-    for (int q = 0; q < PER; ++q)
-      if (l + 64 * q == e) v[q] = none;
+    for (int q = PER - 1; q >= 0; --q) e = v[q] == best ? (uint32_t)(l + 64 * q) : e;
+    e = reduce_u32<64>(e, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
+    if (l == j) id = (int)e;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) v[q] = (uint32_t)(l + 64 * q) == e ? none : v[q];
   }
+  score = id >= 0 ? score64((double)to_f32(row[id])) : 0.0;
   return id;
 }
 
@@ -488,12 +507,14 @@ route_scored_rows_kernel(ScoredArgs a) {
   __syncthreads();
   // rows whose values are too near: a wave each
   constexpr int PER = (LPR * VPT + 63) / 64;
-  for (int i = threadIdx.x >> 6; i < n_again; i += WAVES) {
+  const int wave = threadIdx.x >> 6;
+  for (int i = wave; i < n_again; i += WAVES) {
     const int r = again[i];
     const int64_t t = t0 + r;
     const T* const row = (const T*)a.r.logits + t * a.r.ld;
     double score;
-    const int id = choose64<T, PER>(row, a, lane, score);
+    const int id = choose64<T, PER>(row, a, lane, reinterpret_cast<uint32_t*>(&values[0][0]) + wave * (64 * VPT),
+                                    reinterpret_cast<uint32_t*>(&psum[wave][0]), a.part_bits64, score);
     bool bad = false;
     for (int e = lane; e < E; e += 64) {
       const float x = to_f32(row[e]);
@@ -696,8 +717,9 @@ hipError_t launch_route_scored(const ScoredCall& c, hipStream_t stream) {
   const int64_t nblk = (c.route.T + ROWS - 1) / ROWS;
   if (nblk == 0) return launch_route_places(c.route, stream);
   const Pick p = pick(c.route.type, c.route.E, c.route.T);
-  a.part_bits = 0;
+  a.part_bits = a.part_bits64 = 0;
   while (c.groups << (a.part_bits + 1) <= p.lanes) ++a.part_bits;
+  while (c.groups << (a.part_bits64 + 1) <= 64) ++a.part_bits64;
   const int64_t most = rows_blocks_max(p.rows_threads);
   for (int64_t b = 0; b < nblk; b += most) {
     a.r.block0 = (int)b;
