@@ -127,11 +127,12 @@ __device__ __forceinline__ double max_wave(double x) {
 }
 
 // One row by a wave in 64 bits: lane l holds experts l, l + 64, ... Lane j gets the j-th choice
-// (-1: none) and its score. high, low: LDS of the wave's own, a word each for every expert; 1 <<
-// part_bits lanes a group.
+// (-1: none) and its score. few: the k + 1 experts among which the choice surely is, or all are looked
+// at (null). high, low: LDS of the wave's own, a word each for every expert; 1 << part_bits
+// lanes a group.
 template <typename T, int PER>
-__device__ __forceinline__ int choose64(const T* __restrict__ row, const ScoredArgs& a, int l, uint32_t* high,
-                                        uint32_t* low, int part_bits, double& score) {
+__device__ __forceinline__ int choose64(const T* __restrict__ row, const ScoredArgs& a, int l, const short* few,
+                                        uint32_t* high, uint32_t* low, int part_bits, double& score) {
   const int E = a.r.E, k = a.r.k;
   const double none = -__builtin_inf();
   double v[PER], top = none, z = 1.0;
@@ -153,6 +154,28 @@ __device__ __forceinline__ int choose64(const T* __restrict__ row, const ScoredA
     return a.score == SCORE_SOFTMAX ? exp(x - top) / z : 1.0 / (1.0 + exp(-x));
   };
   const bool by_value = a.bias || a.open < a.groups;
+  if (few) {
+    const int e = l <= k ? few[l] : -1;
+    const float x = e >= 0 ? to_f32(row[e]) : 0.0f;
+    const double y = e < 0 ? none : (a.bias ? score64((double)x) + (double)a.bias[e] : (double)x);
+    const uint64_t words = __builtin_bit_cast(uint64_t, y);
+    int rank = 0;
+    for (int i = 0; i <= k; ++i) {
+      const double o = __builtin_bit_cast(
+          double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)words, i) |
+                      (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(words >> 32), i) << 32);
+      const int oe = __builtin_amdgcn_readlane(e, i);
+      rank += o > y || (o == y && oe < e) ? 1 : 0;
+    }
+    if (l < k) low[l] = 0xFFFFFFFFu;
+    wave_sync();
+    if (e >= 0 && rank < k) low[rank] = (uint32_t)e;
+    wave_sync();
+    const int id = l < k ? (int)low[l] : -1;
+    wave_sync();
+    score = id >= 0 ? score64((double)to_f32(row[id])) : 0.0;
+    return id;
+  }
   if (by_value) {
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
@@ -249,7 +272,8 @@ route_scored_rows_kernel(ScoredArgs a) {
   __shared__ int count[MAX_E], off[MAX_E + 1];
   __shared__ int wave_sum[WAVES];
   __shared__ int n_routed, n_again;
-  __shared__ short again[ROWS];                        // rows that are done again in 64 bits
+  __shared__ short again[ROWS];                        // rows that are done again in 64 bits (~: among all experts)
+  __shared__ short few[ROWS][MAX_K + 1];               // or among these
   __shared__ __attribute__((aligned(8))) float values[AT_ONCE][LPR * VPT];     // where groups are chosen
   __shared__ float group_value[AT_ONCE][MAX_GROUPS];
   __shared__ __attribute__((aligned(16))) uint32_t group_key[AT_ONCE][MAX_GROUPS];
@@ -483,37 +507,41 @@ route_scored_rows_kernel(ScoredArgs a) {
     const int ie = extra ? (int)(LOW - (extra & LOW)) : -1;
     const float xj = id >= 0 ? to_f32(this_row[id]) : 0.0f;
     const float bj = id >= 0 && a.bias ? a.bias[id] : 0.0f;
-    const float xe = ie >= 0 ? to_f32(this_row[ie]) : 0.0f, be = ie >= 0 && a.bias ? a.bias[ie] : 0.0f;
-    // (LPR lanes: the one behind the k-th takes the next candidate)
-    uint32_t kn = (uint32_t)__shfl_down((int)mine, 1, LPR);
-    float xn = __shfl_down(xj, 1, LPR), bn = __shfl_down(bj, 1, LPR);
-    if (l == k - 1) {
-      kn = extra;
-      xn = xe;
-      bn = be;
+    // neighbours among the chosen that are near and not alike; the k-th and the next may be
+    // alike and a third near them
+    const uint32_t kn = l == k - 1 ? extra : (uint32_t)__shfl_down((int)mine, 1, LPR);
+    const float xn = __shfl_down(xj, 1, LPR), bn = __shfl_down(bj, 1, LPR);
+    const bool close = l < k && kn && (mine >> BITS) - (kn >> BITS) <= NEAR && (l == k - 1 || xj != xn || bj != bn);
+    const bool near = reduce_u32<LPR>(close ? 1u : 0u, umax) != 0u && !redo;
+    bool sure = false;
+    if (__ballot(near)) {                              // (uniform over the wave)
+      // the choice is among these and the next, if no other expert is near the k-th
+      const uint32_t beyond = next(), kth = (uint32_t)__shfl((int)mine, k - 1, LPR);
+      sure = near && (beyond == 0u || (kth >> BITS) - (beyond >> BITS) > NEAR);
+      if (in && sure && l < k) few[r][l] = (short)id;
+      if (in && sure && l == 0) few[r][k] = (short)ie;
     }
-    const bool close = l < k && kn && (mine >> BITS) - (kn >> BITS) <= NEAR && !(xj == xn && bj == bn);
-    redo = redo || reduce_u32<LPR>(close ? 1u : 0u, umax) != 0u;
     float w = id >= 0 ? score_of(xj, a.score, sum) : 0.0f;
     if (a.r.renorm) w = chosen_share<LPR>(w, xj, id >= 0);
     const bool bad = sum.share != sum.share;
     w = bad ? sum.share : w * a.scale;
-    if (in && l < k && !redo) {
+    if (in && l < k && !redo && !near) {
       take(t, r, id, w);
       if (l == 0 && id >= 0) atomicAdd(&n_routed, 1);
     }
-    if (in && l == 0 && redo) again[atomicAdd(&n_again, 1)] = (short)r;
+    if (in && l == 0 && (redo || near)) again[atomicAdd(&n_again, 1)] = (short)(sure ? r : ~r);
   }
   __syncthreads();
   // rows whose values are too near: a wave each
   constexpr int PER = (LPR * VPT + 63) / 64;
   const int wave = threadIdx.x >> 6;
   for (int i = wave; i < n_again; i += WAVES) {
-    const int r = again[i];
+    const bool sure = again[i] >= 0;
+    const int r = sure ? again[i] : ~again[i];
     const int64_t t = t0 + r;
     const T* const row = (const T*)a.r.logits + t * a.r.ld;
     double score;
-    const int id = choose64<T, PER>(row, a, lane, reinterpret_cast<uint32_t*>(&values[0][0]) + wave * (64 * VPT),
+    const int id = choose64<T, PER>(row, a, lane, sure ? few[r] : nullptr, reinterpret_cast<uint32_t*>(&values[wave * (64 / LPR)][0]),
                                     reinterpret_cast<uint32_t*>(&psum[wave][0]), a.part_bits64, score);
     bool bad = false;
     for (int e = lane; e < E; e += 64) {
