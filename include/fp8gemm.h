@@ -801,8 +801,8 @@ fp8g_status gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const f
  * group_offsets  DEVICE int32 [G + 1], non-decreasing, in [0, M_total]. They
  *    need not be multiples of 128, nor must M_total (unlike for the FP8 call,
  *    the scales have no blocks). Entries are clamped into [0, M_total] and an
- *    expert whose end lies before its start has no rows: whatever they hold,
- *    no access leaves the arrays.
+ *    entry below an earlier one counts as that one: whatever they hold, no
+ *    access leaves the arrays and no row has two experts.
  * N, K and errors as for gemm_int8; FP8G_ERR_UNSUPPORTED for G > 1024.
  * G == 0 and M_total == 0 are no-ops.
  */

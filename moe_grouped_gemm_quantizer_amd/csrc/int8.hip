@@ -216,24 +216,25 @@ struct Experts {
 
 // By one wave; `side`: rows of a block.
 __device__ __forceinline__ void list_experts(const Int8Args& a, Experts& ex, int side, int lane) {
-  int n = 0, blocks = 0;
+  const int R = (int)a.rows;
+  int n = 0, blocks = 0, past = 0;                     // past: where the experts before end at the latest
   for (int g0 = 0; g0 < a.G; g0 += 64) {
     const int g = g0 + lane;
-    int64_t lo = 0, cnt = 0;
-    if (g < a.G) {
-      if (a.mode == MODE_DENSE) {
-        cnt = a.rows;
-      } else if (a.mode == MODE_CONTIGUOUS) {
-        lo = min(max((int64_t)a.group[g], (int64_t)0), a.rows);
-        cnt = min(max((int64_t)a.group[g + 1], lo), a.rows) - lo;
-      } else {
-        lo = (int64_t)g * a.rows;
-        cnt = min(max((int64_t)a.group[g], (int64_t)0), a.rows);
-      }
+    int lo = 0, cnt = 0;
+    if (a.mode == MODE_CONTIGUOUS) {
+      // an offset below an earlier one counts as that one: no row has two experts, whatever they are
+      lo = g < a.G ? min(max(a.group[g], past), R) : 0;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) lo = max(lo, __shfl_up(lo, o));
+      const int hi = g < a.G ? min(max(a.group[g + 1], lo), R) : lo;
+      cnt = hi - lo;
+      past = __shfl(hi, 63);
+    } else if (g < a.G) {
+      cnt = a.mode == MODE_DENSE ? R : min(max(a.group[g], 0), R);
     }
     const uint64_t has = __ballot(cnt > 0);
     const int i = n + __popcll(has & ((1ull << lane) - 1));
-    int sum = (int)((cnt + side - 1) / side);
+    int sum = (int)(((unsigned)cnt + side - 1) / side);
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const int y = __shfl_up(sum, o);
@@ -241,8 +242,8 @@ __device__ __forceinline__ void list_experts(const Int8Args& a, Experts& ex, int
     }
     if (cnt > 0) {
       ex.id[i] = g;
-      ex.row0[i] = a.mode == MODE_MASKED ? 0 : (int)lo;
-      ex.rows[i] = (int)cnt;
+      ex.row0[i] = lo;
+      ex.rows[i] = cnt;
       ex.before[i + 1] = blocks + sum;
     }
     n += __popcll(has);
@@ -275,6 +276,16 @@ constexpr int COPIES = 16;                             // a wave's copies of a s
 constexpr int EARLY = 12;                              // those that are read a step ahead,
 constexpr int EARLY_FIRST = 8;                         // of these, issued in a step's first half
 constexpr int STORES = 32;                             // a wave's stores of a full tile
+
+// Of `tiles` on `round` workgroups those that are walked whole: all, but for a last round that would
+// leave half of the workgroups or more without one. Its tiles go to int8_ring_kernel<.., REST> in two
+// halves each, which takes 0.6 of a round (512 rows over 8 experts 4096x7168, all of it such a
+// round, 78 -> 54 us; 4096x6144x7168, 1.5 rounds, 195 -> 165; 4096 rows over 8 experts, 1.4 rounds,
+// 174 -> 161; where weights from memory bound the launch, as 8192x7168x2048 with 3.5, 147 -> 149).
+__host__ __device__ __forceinline__ uint32_t full_rounds(uint32_t tiles, uint32_t round) {
+  const uint32_t rest = tiles % round;
+  return rest <= round / 2 ? tiles - rest : tiles;
+}
 
 struct Tile {
   const int8_t *a, *b;                                 // first row
@@ -359,7 +370,7 @@ int8_tile_kernel(Int8Args a, int nblocks, int xcd_remap) {
   if (wave == 0) list_experts(a, ex, TS, lane);
   __syncthreads();
   const int n_ex = __builtin_amdgcn_readfirstlane(ex.n);
-  const int tiles = __builtin_amdgcn_readfirstlane(ex.before[n_ex]) * nblocks;
+  const int tiles = (int)full_rounds(__builtin_amdgcn_readfirstlane(ex.before[n_ex]) * nblocks, a.round);
   const int first = xcd_remap ? (w & 7) * (grid >> 3) + (w >> 3) : w;
   if (first >= tiles) return;
   const int steps = (int)(a.K / 128);
@@ -562,7 +573,8 @@ __device__ __forceinline__ int xcd_run(int w, int tiles) {
   return x * most + min(x, more) + (w >> 3);
 }
 
-template <int FM, int FN, int RING, bool KTAIL>
+// REST: the tiles that int8_tile_kernel leaves, in halves of 128 columns.
+template <int FM, int FN, int RING, bool KTAIL, bool REST>
 __global__ void __launch_bounds__(256, 1)
 int8_ring_kernel(Int8Args a, int nblocks) {
   constexpr int TM = 64 * FM, TN = 64 * FN;
@@ -577,16 +589,25 @@ int8_ring_kernel(Int8Args a, int nblocks) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int64_t g = 0, row = 0;
   int rows = (int)a.rows, before = 0, mblocks = (int)((a.rows + TM - 1) / TM), tiles = mblocks * nblocks, at;
-  if (a.mode == MODE_DENSE) {
-    at = xcd_run(blockIdx.x, tiles);
-  } else {
+  if (a.mode != MODE_DENSE) {
     if (wave == 0) list_experts(a, ex, TM, lane);
     __syncthreads();
-    const int n = __builtin_amdgcn_readfirstlane(ex.n);
-    tiles = __builtin_amdgcn_readfirstlane(ex.before[n]) * nblocks;
+    tiles = __builtin_amdgcn_readfirstlane(ex.before[ex.n]) * nblocks;
+  }
+  int half = 0;                                        // REST: of its tile's
+  if constexpr (REST) {
+    static_assert(TM == TS && 2 * TN == TS, "halves of the tiles");
+    const int done = (int)full_rounds(tiles, a.round), halves = 2 * (tiles - done);
+    if ((int)blockIdx.x >= halves) return;
+    const int h = xcd_run(blockIdx.x, halves);
+    at = done + h / 2;
+    half = h % 2;
+  } else {
     if ((int)blockIdx.x >= tiles) return;
     at = xcd_run(blockIdx.x, tiles);
-    int lo = 0, hi = n - 1;
+  }
+  if (a.mode != MODE_DENSE) {
+    int lo = 0, hi = __builtin_amdgcn_readfirstlane(ex.n) - 1;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (at / nblocks < __builtin_amdgcn_readfirstlane(ex.before[mid + 1])) hi = mid;
@@ -600,7 +621,11 @@ int8_ring_kernel(Int8Args a, int nblocks) {
     __syncthreads();                                   // (read by all: the copies may come)
   }
   int mb, nb;
-  gidx::swizzle_tile(at - before * nblocks, mblocks, nblocks, 8, mb, nb);
+  gidx::swizzle_tile(at - before * nblocks, mblocks, nblocks, REST ? 4 : 8, mb, nb);
+  if constexpr (REST) {
+    nb = 2 * nb + half;
+    if ((int64_t)nb * TN >= a.N) return;               // (uniform over the workgroup)
+  }
   const int64_t m0 = (int64_t)mb * TM, n0 = (int64_t)nb * TN;
   const int mv = (int)min((int64_t)TM, rows - m0), nv = (int)min((int64_t)TN, a.N - n0);
   row += m0;
@@ -873,7 +898,8 @@ int8_skinny_kernel(Int8Args a) {
 // not a multiple of 128 (rows then start inside a 128-byte line, and a copy touches two lines for
 // one), in 1/100 us: fitted to 200 products of M 8 to 9000, N 256 to 12,800, K 256 to 8960,
 // weights cold (each kernel within 8 to 13% rms). The smallest estimate picks within 0.4% of the
-// fastest on the geometric mean and within 19% at most.
+// fastest on the geometric mean and within 19% at most. A TILE256 launch's short last round is
+// RING256's (60 further products of 300 to 9000 rows: within 2% of the fastest, all of them).
 enum Kernel { SKINNY16, SKINNY32, SKINNY64, RING128, RING256, TILE256, KERNELS };
 struct Cost {
   int tm, tn;
@@ -908,7 +934,9 @@ Kernel choose(const Int8Args& a, int expected_m, int cus) {
   for (int k = 0; k < (a.K % 128 ? TILE256 : KERNELS); ++k) {
     const Cost& c = kCost[k];
     const int64_t tiles = blocks(a.rows, c.tm) * blocks(a.N, c.tn);
-    const int64_t t = c.start + blocks(tiles, cus) * (c.round + (a.K % 128 ? c.odd : c.block) * blocks(a.K, 128));
+    const int64_t kb = blocks(a.K, 128), last = k == TILE256 ? tiles - full_rounds(tiles, cus) : 0;
+    int64_t t = c.start + blocks(tiles - last, cus) * (c.round + (a.K % 128 ? c.odd : c.block) * kb);
+    if (last) t += kCost[RING256].start + kCost[RING256].round + kCost[RING256].block * kb;
     if (t < least) {
       least = t;
       best = k;
@@ -925,8 +953,8 @@ SkinnyFn skinny_pick(Kernel k, bool tail) {
   return tail ? int8_skinny_kernel<4, 4, 2, true> : int8_skinny_kernel<4, 4, 2, false>;
 }
 TilesFn ring_pick(Kernel k, bool tail) {
-  if (k == RING128) return tail ? int8_ring_kernel<2, 2, 4, true> : int8_ring_kernel<2, 2, 4, false>;
-  return tail ? int8_ring_kernel<4, 2, 3, true> : int8_ring_kernel<4, 2, 3, false>;
+  if (k == RING128) return tail ? int8_ring_kernel<2, 2, 4, true, false> : int8_ring_kernel<2, 2, 4, false, false>;
+  return tail ? int8_ring_kernel<4, 2, 3, true, false> : int8_ring_kernel<4, 2, 3, false, false>;
 }
 
 }  // namespace
@@ -947,8 +975,19 @@ hipError_t launch_int8(const Int8Args& args, const DeviceInfo& dev, int expected
   } else if (k != TILE256) {
     ring_pick(k, tail)<<<dim3((unsigned)tiles), dim3(256), 0, stream>>>(args, (int)nb);
   } else {
-    const int64_t grid = tiles < dev.cu_count ? tiles : dev.cu_count;
-    int8_tile_kernel<<<dim3((unsigned)grid), dim3(256), 0, stream>>>(args, (int)nb, grid % 8 == 0 ? 1 : 0);
+    Int8Args all = args;
+    all.round = dev.cu_count;
+    // (grouped: how many tiles there are is known on the device alone; a launch for what may be left)
+    if (args.mode != MODE_DENSE || full_rounds(tiles, all.round) > 0) {
+      const int64_t grid = tiles < dev.cu_count ? tiles : dev.cu_count;
+      int8_tile_kernel<<<dim3((unsigned)grid), dim3(256), 0, stream>>>(all, (int)nb, grid % 8 == 0 ? 1 : 0);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    const int64_t rest = args.mode != MODE_DENSE ? (tiles < all.round / 2 ? tiles : all.round / 2)
+                                                 : tiles - full_rounds(tiles, all.round);
+    if (rest > 0)
+      int8_ring_kernel<4, 2, 3, false, true><<<dim3((unsigned)(2 * rest)), dim3(256), 0, stream>>>(all, (int)nb);
   }
   return hipGetLastError();
 }
@@ -965,6 +1004,7 @@ void int8_kernels(std::vector<const void*>& out) {
     for (Kernel k : {RING128, RING256}) out.push_back((const void*)ring_pick(k, tail));
   }
   out.push_back((const void*)int8_tile_kernel);
+  out.push_back((const void*)int8_ring_kernel<4, 2, 3, false, true>);
 }
 
 }  // namespace fp8g

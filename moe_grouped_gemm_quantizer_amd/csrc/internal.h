@@ -186,6 +186,7 @@ struct Int8Args {
   int64_t rows;            // dense: M; contiguous: M_total; masked: max_m
   int64_t N, K;
   int G, mode;             // MODE_DENSE, MODE_CONTIGUOUS or MODE_MASKED
+  int round = 0;           // set by the launcher: workgroups of a round
 };
 hipError_t launch_int8(const Int8Args& args, const DeviceInfo& dev, int expected_m, hipStream_t stream);
 void int8_kernels(std::vector<const void*>& out);

@@ -196,7 +196,7 @@ def test_masked(counts, max_m, N, K, hint):
 
 
 def test_offsets_that_break_the_rules_stay_inside():
-    """Offsets outside [0, M_total] and an expert that ends before it starts: clamped."""
+    """Offsets outside [0, M_total] and below earlier ones: clamped, to the earlier ones too."""
     rng = np.random.default_rng(8)
     M, G, N, K = 200, 4, 48, 64
     a, sa, b, sb = codes(rng, M, K), scales(rng, M), codes(rng, G, N, K), scales(rng, G, N)
@@ -204,7 +204,7 @@ def test_offsets_that_break_the_rules_stay_inside():
     off = torch.tensor([-50, 30, 20, 2_000_000_000, 100], dtype=torch.int32, device=dev())
     fp8g.grouped_gemm_int8_contiguous(to_dev(a), to_dev(sa), to_dev(b), to_dev(sb), guard[32:32 + M], off)
     got = to_host(guard).view(np.uint16)
-    want = ref.contiguous(a, sa, b, sb, [0, 30, 20, 200, 100], np.full((M, N), STALE, np.uint16))
+    want = ref.contiguous(a, sa, b, sb, [0, 30, 30, 200, 200], np.full((M, N), STALE, np.uint16))
     assert np.array_equal(got[32:32 + M], want) and (got[:32] == STALE).all() and (got[32 + M:] == STALE).all()
 
 
@@ -292,3 +292,50 @@ def test_binding_refuses():
             fp8g.int8_quantize(*bad)
     with pytest.raises(fp8g.Fp8GemmError):
         fp8g.int8_quantize(x[:, :24], torch.zeros(4, 24, **i8), sa)
+
+
+@pytest.mark.parametrize("M,N,K", [(4200, 4368, 128), (8200, 3856, 128), (3200, 4096, 256), (12544, 2704, 128),
+                                   (4096, 6160, 384), (6400, 5904, 128)])
+def test_dense_last_round(M, N, K):
+    """More tiles than CUs: last rounds that are empty, of a few tiles, of half of the CUs, of most."""
+    got, want = run_dense(np.random.default_rng(M + N), M, N, K)
+    assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("counts,N,K", [
+    ((1500, 0, 900, 1, 700, 1300), 4368, 128), ((300, 290, 310, 257, 0, 512, 600, 256), 7184, 128),
+    ((600, 700), 1040, 256), ((4096, 4096), 2048, 128)])
+def test_contiguous_last_round(counts, N, K):
+    got, want = run_contiguous(np.random.default_rng(N), counts, N, K, align=1, lead=3, tail=2)
+    assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("counts,max_m,N,K", [
+    ((200, 130, 256, 0, 180, 7, 255, 140, 256, 300), 256, 7184, 128), ((512, 300, 0, 512), 512, 4368, 256)])
+def test_masked_last_round(counts, max_m, N, K):
+    rng = np.random.default_rng(max_m + N)
+    G = len(counts)
+    a, sa = codes(rng, G, max_m, K), scales(rng, G, max_m)
+    b, sb = codes(rng, G, N, K), scales(rng, G, N)
+    d = torch.full((G, max_m, N), STALE, dtype=torch.int16, device=dev())
+    m = torch.tensor(counts, dtype=torch.int32, device=dev())
+    fp8g.grouped_gemm_int8_masked(to_dev(a), to_dev(sa), to_dev(b), to_dev(sb), d, m)
+    want = ref.masked(a, sa, b, sb, counts, np.full((G, max_m, N), STALE, np.uint16))
+    assert np.array_equal(to_host(d).view(np.uint16), want)
+
+
+@pytest.mark.parametrize("K", [128, 144])
+def test_offsets_in_any_order_stay_inside(K):
+    """More experts than a wave has lanes, offsets at random: as their running maximum says."""
+    rng = np.random.default_rng(K)
+    M, G, N = 700, 150, 272
+    a, sa, b, sb = codes(rng, M, K), scales(rng, M), codes(rng, G, N, K), scales(rng, G, N)
+    off = rng.integers(-2 ** 31, 2 ** 31, G + 1)
+    off[::3] = rng.integers(0, M + 1, len(off[::3]))
+    off[:100] = np.minimum(off[:100], rng.integers(0, 300, 100))
+    d = torch.full((M, N), STALE, dtype=torch.int16, device=dev())
+    fp8g.grouped_gemm_int8_contiguous(to_dev(a), to_dev(sa), to_dev(b), to_dev(sb), d,
+                                      torch.from_numpy(off.astype(np.int32)).to(dev()))
+    starts = np.maximum.accumulate(np.clip(off, 0, M))
+    want = ref.contiguous(a, sa, b, sb, starts, np.full((M, N), STALE, np.uint16))
+    assert np.array_equal(to_host(d).view(np.uint16), want) and len(np.unique(starts)) > 4
