@@ -7,7 +7,12 @@ experts' weight gradients, the router's gradient, and one clipping of all
 gradients together. Gathers, the router's two small products and the update
 are torch's.
 
-    python examples/moe_train_step.py [--steps 30]
+With score="sigmoid" (or "softmax") the router goes by scores plus a bias that
+evens out the experts' loads; with adamw the update is the library's AdamW step,
+which clips by itself, states in 32 or 8 bits; serve() answers through products in
+8-bit integers.
+
+    python examples/moe_train_step.py [--steps 30] [--score sigmoid] [--adamw 8]
 """
 
 import argparse
@@ -27,7 +32,8 @@ def _pad(n):
 class MoELayer:
     """Parameters (fp32) and the buffers that every step uses again."""
 
-    def __init__(self, tokens, width, out, experts, top_k, balance=0.01, device="cuda", seed=0):
+    def __init__(self, tokens, width, out, experts, top_k, balance=0.01, device="cuda", seed=0, score=None,
+                 groups=1, open_groups=1, adamw=0):
         g = torch.Generator(device=device)
         g.manual_seed(seed)
         self.T, self.K, self.N, self.E, self.k, self.balance = tokens, width, out, experts, top_k, balance
@@ -50,13 +56,31 @@ class MoELayer:
         self.d_weight = new(experts, out, width, dtype=bf16)
         self.sumsq, self.norm, self.one = new(1, dtype=torch.float64), new(1), torch.ones(1, device=device)
         self.clip_ws = new(max(8, fp8g.grad_norm_sq_workspace_size([self.d_weight, self.router])), dtype=u8)
+        # routing by scores: what its two calls share, and the choice's bias
+        self.scored = score and dict(score=score, renormalise=True, loss_coef=balance)
+        self.choice = dict(groups=groups, open_groups=open_groups, group_best=min(2, experts // groups))
+        self.bias = torch.zeros(experts, device=device)
+        self.adamw, self.steps = adamw, 0
+        if adamw:
+            params, self.d_router = [self.weight, self.router], new(experts, width)
+            fresh = lambda f: [f(p.numel()) for p in params]  # noqa: E731
+            zeros = lambda n, dtype=torch.float32: torch.zeros(n, dtype=dtype, device=device)  # noqa: E731
+            code, block = (lambda n: zeros(n, u8)), (lambda n: zeros(-(-n // 128), u8))
+            states = [fresh(code if adamw == 8 else zeros) for _ in range(2)]
+            scales = dict(m_scales=fresh(block), v_scales=fresh(block)) if adamw == 8 else {}
+            self.states = states + list(scales.values())
+            self.tensors = fp8g.adamw_tensors(params, [self.d_weight, self.d_router], *states, **scales)
 
-    def forward(self, x, mask=None):
-        """x bf16 [T][K] -> y fp32 [T][N]; keeps what the backward pass needs."""
+    def _route(self, x, mask):
+        """Rows of the experts' operand, filled; each pair's row of it."""
         r = self.route
         self.logits = x.float() @ self.router.t()
-        fp8g.moe_route(self.logits, self.k, *r.values(), self.route_ws, token_mask=mask, renormalise=True,
-                       loss_coef=self.balance)
+        if self.scored:
+            fp8g.moe_route_scored(self.logits, self.k, *r.values(), self.route_ws, bias=self.bias, token_mask=mask,
+                                  **self.scored, **self.choice)
+        else:
+            fp8g.moe_route(self.logits, self.k, *r.values(), self.route_ws, token_mask=mask, renormalise=True,
+                           loss_coef=self.balance)
         live = r["slots"] >= 0
         # (rows that no token fills stay zero; a pair without a slot goes to a
         # spare row past the end)
@@ -64,14 +88,37 @@ class MoELayer:
         self.xr = torch.zeros(self.rows + 1, self.K, dtype=torch.bfloat16, device=x.device)
         self.xr[self.at.reshape(-1)] = x.repeat_interleave(self.k, 0)
         self.xr = self.xr[: self.rows]
+        self.w = torch.where(live, r["weights"], torch.zeros_like(r["weights"]))
+
+    def forward(self, x, mask=None):
+        """x bf16 [T][K] -> y fp32 [T][N]; keeps what the backward pass needs."""
+        self._route(x, mask)
         fp8g.fp8_quantize_bf16(self.xr, 1, self.qx, self.sx, 1, self.rows)
         fp8g.fp8_quantize(self.weight.view(-1, self.K), 128, self.qw.view(-1, self.K),
                           self.sw.view(-1, self.K // 128), self.K // 128, 1)
         self.y.zero_()
         fp8g.grouped_gemm_fp8_contiguous(self.qx, self.sx, self.qw, self.sw, self.y, self._all_rows())
-        self.w = torch.where(live, r["weights"], torch.zeros_like(r["weights"]))
+        return self._combine()
+
+    def _combine(self):
         self.picked = torch.cat([self.y, self.y.new_zeros(1, self.N)])[self.at].float()   # [T][k][N]
         return (self.w[..., None] * self.picked).sum(1)
+
+    def freeze(self):
+        """The weights' int8 codes and scales for serve."""
+        self.iw = torch.empty(self.weight.shape, dtype=torch.int8, device=self.weight.device)
+        self.siw = torch.empty(self.weight.shape[:2], device=self.weight.device)
+        fp8g.int8_quantize(self.weight.view(-1, self.K), self.iw.view(-1, self.K), self.siw.view(-1))
+        self.ix = torch.empty(self.rows, self.K, dtype=torch.int8, device=self.weight.device)
+        self.six = torch.empty(self.rows, device=self.weight.device)
+
+    def serve(self, x, mask=None):
+        """x bf16 [T][K] -> y fp32 [T][N] by products in 8-bit integers."""
+        self._route(x, mask)
+        fp8g.int8_quantize(self.xr, self.ix, self.six)
+        self.y.zero_()
+        fp8g.grouped_gemm_int8_contiguous(self.ix, self.six, self.iw, self.siw, self.y, self.route["group_offsets"])
+        return self._combine()
 
     def _all_rows(self):
         """The offsets as the product wants them: the last expert's rows reach
@@ -91,9 +138,16 @@ class MoELayer:
                                     group_offsets=r["group_offsets"])
         d_w = (self.picked * dy[:, None]).sum(2)
         d_logits = torch.empty_like(self.logits)
-        fp8g.moe_route_backward(self.logits, r["expert_ids"], d_w, self.one, r["counts"], r["routed"], d_logits,
-                                renormalise=True, loss_coef=self.balance)
-        self.d_router = d_logits.t() @ x.float()
+        if self.scored:
+            fp8g.moe_route_scored_backward(self.logits, r["expert_ids"], d_w, self.one, r["counts"], r["routed"],
+                                           d_logits, **self.scored)
+        else:
+            fp8g.moe_route_backward(self.logits, r["expert_ids"], d_w, self.one, r["counts"], r["routed"], d_logits,
+                                    renormalise=True, loss_coef=self.balance)
+        if self.adamw:
+            self.d_router.copy_(d_logits.t() @ x.float())   # (the step's list holds its address)
+        else:
+            self.d_router = d_logits.t() @ x.float()
         return self.d_weight, self.d_router
 
     def step(self, x, target, lr, max_norm=1.0, mask=None):
@@ -105,17 +159,24 @@ class MoELayer:
         loss = err.square().mean() + self.route["loss"][0]
         grads = list(self.backward(x, 2.0 * err / err.numel()))
         fp8g.grad_norm_sq(grads, self.sumsq, self.clip_ws)
+        if self.scored:
+            counts = self.route["counts"].float()
+            self.bias += 1e-3 * torch.sign(counts.mean() - counts)
+        if self.adamw:
+            self.steps += 1
+            fp8g.adamw_step(self.tensors, self.steps, lr, sumsq=self.sumsq, max_norm=max_norm, norm=self.norm)
+            return loss
         fp8g.grad_clip(grads, grads, self.sumsq, max_norm, self.norm)
         self.weight -= lr * grads[0].float()
         self.router -= lr * grads[1]
         return loss
 
 
-def train(steps=30, tokens=1024, width=512, out=256, experts=8, top_k=2, lr=20.0, seed=0):
+def train(steps=30, tokens=1024, width=512, out=256, experts=8, top_k=2, lr=20.0, seed=0, **options):
     """Losses of `steps` steps."""
     g = torch.Generator(device="cuda")
     g.manual_seed(seed + 1)
-    layer = MoELayer(tokens, width, out, experts, top_k, seed=seed)
+    layer = MoELayer(tokens, width, out, experts, top_k, seed=seed, **options)
     teacher = torch.randn(out, width, device="cuda", generator=g) * width ** -0.5
     losses = []
     for _ in range(steps):
@@ -127,5 +188,8 @@ def train(steps=30, tokens=1024, width=512, out=256, experts=8, top_k=2, lr=20.0
 if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=30)
-    for i, v in enumerate(train(ap.parse_args().steps)):
+    ap.add_argument("--score", choices=["sigmoid", "softmax"])
+    ap.add_argument("--adamw", type=int, choices=[32, 8], default=0, help="bits of the states")
+    args = ap.parse_args()
+    for i, v in enumerate(train(args.steps, lr=3e-3 if args.adamw else 20.0, score=args.score, adamw=args.adamw)):
         print(f"step {i:3d}  loss {v:.4f}", flush=True)

@@ -777,6 +777,8 @@ def adamw_tensors(params, grads, exp_avgs, exp_avg_sqs, copies=None, m_scales=No
     written = [p for ps in ptr[:1] + ptr[2:] for p in ps if p]
     if len(set(written)) != len(written):
         _fail("a tensor that the step writes is in the list twice")
+    if not set(written).isdisjoint(ptr[1]):
+        _fail("a gradient must not be a tensor that the step writes")
     out = AdamwTensors()
     # (the memory, whatever becomes of the tensors)
     out.held = [[t.untyped_storage() for t in ts if t is not None] for ts in lists]

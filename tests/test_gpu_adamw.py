@@ -335,7 +335,7 @@ def test_binding_refuses():
                 dict(ok, exp_avg_sqs=[z().bfloat16()]), dict(ok, params=[torch.zeros(8)]), dict(ok, grads=[None]),
                 dict(ok, params=[z(16)[::2]]), dict(ok, copies=[z()]), dict(ok, copies=[z(7).bfloat16()]),
                 dict(eight, v_scales=None), dict(eight, m_scales=[z(2, u8)]), dict(eight, exp_avgs=[z()]),
-                dict(ok, exp_avgs=[same], exp_avg_sqs=[same]),
+                dict(ok, exp_avgs=[same], exp_avg_sqs=[same]), dict(ok, params=[same], grads=[same]),
                 dict(params=[same, same], grads=[z(), z()], exp_avgs=[z(), z()], exp_avg_sqs=[z(), z()])]:
         with pytest.raises(ValueError):
             fp8g.adamw_tensors(**bad)
