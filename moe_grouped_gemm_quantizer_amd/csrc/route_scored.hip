@@ -256,7 +256,7 @@ __device__ __forceinline__ int choose64(const T* __restrict__ row, const ScoredA
 
 // One block of 64 tokens per workgroup, LPR lanes a row, as in route.hip.
 template <typename T, int LPR, int VPT, int NT>
-__global__ void __launch_bounds__(NT, NT == 512 ? 4 : 1)
+__global__ void __launch_bounds__(NT, NT == 512 ? (LPR == 16 ? 4 : 2) : 1)
 route_scored_rows_kernel(ScoredArgs a) {
   using L = Lay<T, LPR, VPT>;
   constexpr int AT_ONCE = NT / LPR, WAVES = NT / 64;
@@ -701,8 +701,8 @@ Pick pick_for(int E) {
   constexpr bool few = NT == THREADS;
   constexpr int WIDE = NT > 512 ? 512 : NT;
 #define FP8G_PICK(LPR_, VPT_)                                                                    \
-  Pick { route_scored_rows_kernel<T, LPR_, VPT_, LPR_ == 16 && VPT_ >= 12 ? WIDE : NT>,          \
-         LPR_ == 16 && VPT_ >= 12 ? WIDE : NT, route_scored_backward_kernel<T, LPR_, VPT_>,      \
+  Pick { route_scored_rows_kernel<T, LPR_, VPT_, VPT_ >= 12 ? WIDE : NT>,                        \
+         VPT_ >= 12 ? WIDE : NT, route_scored_backward_kernel<T, LPR_, VPT_>,      \
          THREADS / LPR_, LPR_ }
   if (E <= 16) return FP8G_PICK(16, 1);
   if (E <= 32) return FP8G_PICK(16, 2);
