@@ -734,6 +734,10 @@ fp8g_status grad_clip(const void* const* grads, void* const* outs, const int64_t
  *                    taken as 1.
  * sumsq, norm        DEVICE double [1] (grad_norm_sq's, sums over processes
  *                    added) or NULL, and DEVICE float [1] or NULL: the norm.
+ * table              NULL, or the DEVICE copy of what adamw_table wrote for
+ *                    these lists, 8-byte aligned: a long list is then one
+ *                    launch, for one of each 52 tensors without it. Not
+ *                    read by steps that are captured into a graph.
  * Errors (nothing is launched): FP8G_ERR_SHAPE (negative sizes, step_value < 1,
  * a beta outside [0, 1), eps negative, a hyperparameter that is not finite,
  * max_norm not > 0 with sumsq), _NULL_PTR (also norm without sumsq), _ALIGN,
@@ -745,7 +749,20 @@ fp8g_status adamw_step(void* const* params, const int* param_types, const void* 
                        const int* copy_types, const int64_t* numels, int n, const int64_t* step,
                        int64_t step_value, const float* lr, double lr_value, double beta1, double beta2,
                        double eps, double weight_decay, const double* sumsq, float max_norm, float* norm,
-                       uint32_t seed, hipStream_t stream);
+                       uint32_t seed, const void* table, hipStream_t stream);
+
+/*
+ * adamw_table, adamw_table_size -- the list of an adamw_step as a table, for lists
+ * that are used again: writes adamw_table_size(n) bytes to HOST memory at table
+ * (8-byte aligned), which the caller copies to the device and gives to the
+ * steps over the same list (the arguments as there). Errors as for adamw_step's
+ * lists; _UNSUPPORTED for more than 2^42 elements.
+ */
+fp8g_status adamw_table_size(int n, size_t* bytes);
+fp8g_status adamw_table(void* const* params, const int* param_types, const void* const* grads,
+                        const int* grad_types, void* const* exp_avgs, void* const* exp_avg_sqs,
+                        uint8_t* const* avg_scales, uint8_t* const* sq_scales, void* const* copies,
+                        const int* copy_types, const int64_t* numels, int n, void* table);
 
 /* ---- Products in 8-bit integers ---------------------------------------------
  * The other common 8-bit form of a served layer: whole numbers -127 .. 127

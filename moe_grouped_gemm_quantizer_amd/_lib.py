@@ -26,7 +26,7 @@ ENTRY_POINTS = ("fp8_quantize", "fp8_quantize_bf16", "fp8_quantize_tensor", "gem
                 "fp8_quantize_transpose", "grouped_gemm_fp8_wgrad", "grad_norm_sq",
                 "grad_norm_sq_workspace_size", "grad_clip",
                 "moe_route_scored", "moe_route_scored_backward",
-                "adamw_step", "int8_quantize", "gemm_int8", "grouped_gemm_int8_contiguous",
+                "adamw_step", "adamw_table", "adamw_table_size", "int8_quantize", "gemm_int8", "grouped_gemm_int8_contiguous",
                 "grouped_gemm_int8_masked",
                 "fp8g_status_string", "fp8g_abi_version")
 
@@ -83,7 +83,9 @@ _SIGS = {
     "moe_route_scored_backward": [_c_vp, _c_int, _c_i64, _c_int, _c_i64, _c_int, _c_vp, _c_int, _c_int, _c_f,
                                   _c_f, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp],
     "adamw_step": [_c_vp] * 11 + [_c_int, _c_vp, _c_i64, _c_vp, _c_d, _c_d, _c_d, _c_d, _c_d, _c_vp, _c_f,
-                                  _c_vp, ctypes.c_uint32, _c_vp],
+                                  _c_vp, ctypes.c_uint32, _c_vp, _c_vp],
+    "adamw_table": [_c_vp] * 11 + [_c_int, _c_vp],
+    "adamw_table_size": [_c_int, ctypes.POINTER(ctypes.c_size_t)],
     "int8_quantize": [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp],
     "gemm_int8": [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp],
     "grouped_gemm_int8_contiguous": [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_i64, _c_i64,
@@ -726,10 +728,10 @@ def grad_clip(grads, outs, sumsq, max_norm, norm, stream=None):
 
 class AdamwTensors:
     """The tensors of an AdamW step (made by adamw_tensors): their pointers,
-    sizes and types as HOST arrays, and their storages, which keeps the memory
-    alive."""
+    sizes and types as HOST arrays, for a long list as a table in device memory
+    too, and their storages, which keeps the memory alive."""
 
-    __slots__ = ("held", "lists", "n", "device")
+    __slots__ = ("held", "lists", "n", "device", "table", "streams")
 
 
 def adamw_tensors(params, grads, exp_avgs, exp_avg_sqs, copies=None, m_scales=None, v_scales=None):
@@ -787,6 +789,16 @@ def adamw_tensors(params, grads, exp_avgs, exp_avg_sqs, copies=None, m_scales=No
                  ptr[6] if copies is not None else (), typ[2], array.array("q", numels))
     out.n = n
     out.device = at
+    out.table, out.streams = None, None
+    # (a list that one launch takes by value has no use for it; a step that is captured takes that way)
+    if n > 52 and not torch.cuda.is_current_stream_capturing():
+        size = ctypes.c_size_t(0)
+        _check(load().adamw_table_size(n, ctypes.byref(size)), "adamw_table_size")
+        table = torch.empty(size.value, dtype=torch.uint8)
+        st = load().adamw_table(*map(_at, out.lists), n, table.data_ptr())
+        if st == 0:                          # (refused here: the step refuses it too, or does without)
+            out.table = table.to(f"cuda:{at}")
+            out.streams = {_current_stream()}
     return out
 
 
@@ -810,8 +822,14 @@ def adamw_step(tensors, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay
         lp, lr = _out(lr, (1,) if lr.dim() else (), torch.float32, "lr"), 0.0
     total = None if sumsq is None else _out(sumsq, (1,), torch.float64, "sumsq")
     nrm = None if norm is None else _out(norm, (1,), torch.float32, "norm")
+    on, table = _stream(stream), tensors.table
+    if table is not None:
+        if on not in tensors.streams:        # (its memory is not used again before the steps there are done)
+            table.record_stream(torch.cuda.ExternalStream(on))
+            tensors.streams.add(on)
+        table = table.data_ptr()
     st = load().adamw_step(*map(_at, tensors.lists), tensors.n, sp, step, lp, lr, beta1, beta2, eps, weight_decay,
-                           total, max_norm, nrm, seed & 0xFFFFFFFF, _stream(stream))
+                           total, max_norm, nrm, seed & 0xFFFFFFFF, table, on)
     if st:
         _check(st, "adamw_step")
 

@@ -12,8 +12,8 @@
 // that is cut off, by 16 bits of a hash of (seed, step, tensor, element). r is never rounded to
 // 0 unless it is 0: m / (r + eps) would then be as large as eps is small.
 //
-// An HBM stream: every tensor is read and written once. The list travels in the kernel's
-// arguments (MAX_T tensors a launch): nothing of it stays on the device or in the library.
+// An HBM stream: every tensor is read and written once. The list travels in the kernel's arguments,
+// MAX_T tensors a launch, or lies in device memory for a launch over all of them.
 
 #include <math.h>
 #include <vector>
@@ -34,22 +34,22 @@ constexpr int BLOCK = 128;                             // elements of an 8-bit s
 constexpr int64_t CHUNK_MIN = 2048, CHUNK_MAX = 8192;  // elements of a chunk, multiples of 2048
 constexpr int64_t LONG = int64_t(1) << 24;             // elements of a list that takes large chunks
 constexpr int64_t CHUNKS = (1 << 24) - 1;              // of a launch: fewer than 2^32 threads
+constexpr int64_t TABLE_CHUNKS = (int64_t(1) << 31) - 1;
 
-struct Table {
-  void* p[MAX_T];
-  const void* g[MAX_T];
-  void* m[MAX_T];
-  void* v[MAX_T];
-  void* copy[MAX_T];
-  uint8_t* ms[MAX_T];
-  uint8_t* vs[MAX_T];
-  int64_t numel[MAX_T];
-  int end[MAX_T];                                      // chunks of this tensor and those before it
-  int index[MAX_T];                                    // its number in the caller's list
-  uint8_t types[MAX_T];                                // of p + 3 of g
-  uint8_t ctype[MAX_T];
-  int n, chunk;
+struct Entry {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  void* copy;
+  uint8_t* ms;
+  uint8_t* vs;
+  int64_t numel;
+  int first;                                           // the tensor's first chunk
+  uint8_t types;                                       // of p + 3 of g
+  uint8_t ctype;
 };
+static_assert(sizeof(Entry) == 72, "whole dwords");
 
 struct Hyper {
   const double* sumsq;
@@ -62,11 +62,61 @@ struct Hyper {
   uint32_t seed, key;
   float size, inv, keep;                               // Factors', where the host knows step and lr
 };
-struct Args {
-  Table t;
+// Tensors by value, from number `base` of the caller's list on; end: chunks of a tensor and those
+// before it.
+struct Some {
   Hyper h;
+  int n, chunk, base;
+  int end[MAX_T];
+  Entry list[MAX_T];
+  // (c: this workgroup's chunk, the same in all lanes)
+  __device__ __forceinline__ int find(int c) const {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (c < end[mid]) hi = mid;
+      else lo = mid + 1;
+    }
+    return lo;
+  }
+  __device__ __forceinline__ Entry at(int i) const { return list[i]; }
 };
-static_assert(sizeof(Args) <= 4096, "a kernel's arguments");
+static_assert(sizeof(Some) <= 4096, "a kernel's arguments");
+
+// All of them in device memory, a launch's chunks from number chunk0 on. 64 ends are looked at at
+// once, and a tensor's entry is loaded by a lane each dword.
+struct All {
+  Hyper h;
+  int n, chunk, base, chunk0;
+  const int* end;
+  const Entry* list;
+  __device__ __forceinline__ int find(int c) const {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, len = n;
+    while (len > 64) {
+      const int stride = (len + 63) >> 6;
+      const int last = min((lane + 1) * stride, len) - 1;
+      const int before = __popcll(__ballot(c >= end[lo + last]));     // (past the list: its last, after c)
+      lo += before * stride;
+      len = min(stride, len - before * stride);
+    }
+    return lo + __popcll(__ballot(lane < len && c >= end[lo + min(lane, len - 1)]));
+  }
+  __device__ __forceinline__ Entry at(int i) const {
+    constexpr int W = sizeof(Entry) / 4;
+    const int lane = threadIdx.x & 63;
+    const uint32_t mine = reinterpret_cast<const uint32_t*>(list + i)[min(lane, W - 1)];
+    uint32_t w[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k] = (uint32_t)__builtin_amdgcn_readlane((int)mine, k);
+    Entry e;
+    __builtin_memcpy(&e, w, sizeof(e));
+    return e;
+  }
+};
+template <typename A>
+constexpr bool is_all = __is_same(A, All);
+int64_t ends_bytes(int n) { return (n + 1) / 2 * 8; }
 
 // What a step multiplies with, the same in every thread.
 struct Factors {
@@ -196,12 +246,12 @@ __device__ __forceinline__ void store_copy(void* c, int64_t at, int type, bool v
 
 // A chunk with fp32 states: four elements a lane.
 template <typename P, typename G>
-__device__ __forceinline__ void chunk32(const Table& t, int i, int64_t at, int n, const Factors& f) {
-  P* const p = (P*)t.p[i] + at;
-  const G* const g = (const G*)t.g[i] + at;
-  float* const m = (float*)t.m[i] + at;
-  float* const v = (float*)t.v[i] + at;
-  void* const c = t.copy[i];
+__device__ __forceinline__ void chunk32(const Entry& t, int64_t at, int n, const Factors& f) {
+  P* const p = (P*)t.p + at;
+  const G* const g = (const G*)t.g + at;
+  float* const m = (float*)t.m + at;
+  float* const v = (float*)t.v + at;
+  void* const c = t.copy;
   constexpr int N = 4;
   const bool vec = (((uintptr_t)p % (N * sizeof(P))) | ((uintptr_t)g % (N * sizeof(G))) |
                     (((uintptr_t)m | (uintptr_t)v) % 16) | ((uintptr_t)c % 8)) == 0;
@@ -247,7 +297,7 @@ __device__ __forceinline__ void chunk32(const Table& t, int i, int64_t at, int n
       store_few<float, N>(m + e, left, xm);
       store_few<float, N>(v + e, left, xv);
     }
-    if (c) store_copy<N>(c, at + e, t.ctype[i], whole, left, xp);
+    if (c) store_copy<N>(c, at + e, t.ctype, whole, left, xp);
   }
 }
 
@@ -272,17 +322,17 @@ __device__ __forceinline__ uint32_t code7(float x, float scale, uint32_t cut) {
 
 // A chunk with states in 8 bits: eight elements a lane, 16 lanes a block.
 template <typename P, typename G>
-__device__ __forceinline__ void chunk8(const Table& t, int i, int64_t at, int n, const Factors& f) {
-  P* const p = (P*)t.p[i] + at;
-  const G* const g = (const G*)t.g[i] + at;
-  uint8_t* const m = (uint8_t*)t.m[i] + at;
-  uint8_t* const v = (uint8_t*)t.v[i] + at;
-  uint8_t* const ms = t.ms[i] + at / BLOCK;
-  uint8_t* const vs = t.vs[i] + at / BLOCK;
-  void* const c = t.copy[i];
+__device__ __forceinline__ void chunk8(const Entry& t, int index, int64_t at, int n, const Factors& f) {
+  P* const p = (P*)t.p + at;
+  const G* const g = (const G*)t.g + at;
+  uint8_t* const m = (uint8_t*)t.m + at;
+  uint8_t* const v = (uint8_t*)t.v + at;
+  uint8_t* const ms = t.ms + at / BLOCK;
+  uint8_t* const vs = t.vs + at / BLOCK;
+  void* const c = t.copy;
   constexpr int N = 8;
   const bool vec = (((uintptr_t)p | (uintptr_t)g | (uintptr_t)c) % 16 | ((uintptr_t)m | (uintptr_t)v) % 8) == 0;
-  const uint32_t key = mix(f.key + (uint32_t)t.index[i]) + (uint32_t)(at / BLOCK);
+  const uint32_t key = mix(f.key + (uint32_t)index) + (uint32_t)(at / BLOCK);
   const int lane = threadIdx.x & 15;
   // (whole blocks: all 16 lanes of one take part in its maxima)
   for (int e = threadIdx.x * N; e - lane * N < n; e += THREADS * N) {
@@ -406,7 +456,7 @@ __device__ __forceinline__ void chunk8(const Table& t, int i, int64_t at, int n,
           v[e + k] = (uint8_t)(ov[k / 4] >> (8 * (k % 4)));
         }
     }
-    if (c) store_copy<N>(c, at + e, t.ctype[i], whole, left, xp);
+    if (c) store_copy<N>(c, at + e, t.ctype, whole, left, xp);
     if (lane == 0) {
       ms[blk] = (uint8_t)(em + 127);
       vs[blk] = (uint8_t)(er + 127);
@@ -415,28 +465,24 @@ __device__ __forceinline__ void chunk8(const Table& t, int i, int64_t at, int n,
 }
 
 // A workgroup a chunk (n == 0: one writes the norm).
-template <int BITS>
+template <int BITS, typename Args>
 __global__ void __launch_bounds__(THREADS)
 adamw_kernel(Args a) {
-  const Table& t = a.t;
   Factors f;
   if (!factors(a.h, f)) return;
-  const int c = (int)blockIdx.x;
-  if (t.n == 0) return;
-  int lo = 0, hi = t.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (c < t.end[mid]) hi = mid;
-    else lo = mid + 1;
-  }
-  const int64_t at = (int64_t)(c - (lo ? t.end[lo - 1] : 0)) * t.chunk;
-  const int64_t left = t.numel[lo] - at;
-  const int n = (int)(left < t.chunk ? left : t.chunk);
+  if (a.n == 0) return;
+  int c = (int)blockIdx.x;
+  if constexpr (is_all<Args>) c += a.chunk0;
+  const int i = a.find(c);
+  const Entry t = a.at(i);
+  const int64_t at = (int64_t)(c - t.first) * a.chunk;
+  const int64_t left = t.numel - at;
+  const int n = (int)(left < a.chunk ? left : a.chunk);
   const auto run = [&](auto p, auto g) __attribute__((always_inline)) {
-    if constexpr (BITS == 8) chunk8<decltype(p), decltype(g)>(t, lo, at, n, f);
-    else chunk32<decltype(p), decltype(g)>(t, lo, at, n, f);
+    if constexpr (BITS == 8) chunk8<decltype(p), decltype(g)>(t, a.base + i, at, n, f);
+    else chunk32<decltype(p), decltype(g)>(t, at, n, f);
   };
-  switch (t.types[lo]) {
+  switch (t.types) {
     case 0: run(0.0f, 0.0f); break;
     case 1: run(bf16_t(), 0.0f); break;
     case 2: run(f16_t(), 0.0f); break;
@@ -464,12 +510,27 @@ int chunk_for(const AdamwCall& c) {
   return (int)(total >= LONG && narrow > total / 2 ? CHUNK_MAX : CHUNK_MIN);
 }
 
-}  // namespace
+int64_t chunks_of(int64_t numel, int chunk) { return (numel + chunk - 1) / chunk; }
 
-hipError_t launch_adamw(const AdamwCall& c, hipStream_t stream) {
-  Args a;
-  Table& t = a.t;
-  Hyper& h = a.h;
+// Tensor i's entry, its chunks from `first` on.
+Entry entry(const AdamwCall& c, int i, int64_t first) {
+  Entry e = {};
+  e.p = c.params[i];
+  e.g = c.grads[i];
+  e.m = c.m[i];
+  e.v = c.v[i];
+  e.copy = c.copies ? c.copies[i] : nullptr;
+  e.ms = c.ms ? c.ms[i] : nullptr;
+  e.vs = c.ms ? c.vs[i] : nullptr;
+  e.numel = c.numels[i];
+  e.first = (int)first;
+  e.types = (uint8_t)(c.param_types[i] + 3 * c.grad_types[i]);
+  e.ctype = (uint8_t)(c.copies ? c.copy_types[i] : 0);
+  return e;
+}
+
+Hyper hyper(const AdamwCall& c) {
+  Hyper h = {};
   h.sumsq = c.sumsq;
   h.norm = c.norm;
   h.step_at = c.step_at;
@@ -487,47 +548,100 @@ hipError_t launch_adamw(const AdamwCall& c, hipStream_t stream) {
   h.step = c.step;
   h.seed = c.seed;
   if (!c.step_at && !c.lr_at) of_step(h, c.step, c.lr, h);
-  t.chunk = chunk_for(c);
-  const auto kernel = c.ms ? adamw_kernel<8> : adamw_kernel<32>;
-  int i = 0;
-  bool first = true;
-  for (;;) {
-    t.n = 0;
-    int64_t chunks = 0;
-    for (; i < c.n && t.n < MAX_T; ++i) {
-      if (c.numels[i] == 0) continue;
-      const int64_t k = (c.numels[i] + t.chunk - 1) / t.chunk;
-      if (chunks + k > CHUNKS && t.n > 0) break;       // (each tensor fits by itself: checked before)
-      chunks += k;
-      t.p[t.n] = c.params[i];
-      t.g[t.n] = c.grads[i];
-      t.m[t.n] = c.m[i];
-      t.v[t.n] = c.v[i];
-      t.copy[t.n] = c.copies ? c.copies[i] : nullptr;
-      t.ctype[t.n] = (uint8_t)(c.copies ? c.copy_types[i] : 0);
-      t.ms[t.n] = c.ms ? c.ms[i] : nullptr;
-      t.vs[t.n] = c.vs ? c.vs[i] : nullptr;
-      t.numel[t.n] = c.numels[i];
-      t.types[t.n] = (uint8_t)(c.param_types[i] + 3 * c.grad_types[i]);
-      t.index[t.n] = i;
-      t.end[t.n] = (int)chunks;
-      ++t.n;
-    }
-    // (nothing to do, but a norm to write)
-    if (chunks == 0 && !(first && c.norm)) break;
-    kernel<<<dim3((unsigned)(chunks ? chunks : 1)), dim3(THREADS), 0, stream>>>(a);
+  return h;
+}
+
+hipError_t launch_all(const AdamwCall& c, hipStream_t stream) {
+  All a;
+  a.h = hyper(c);
+  a.n = c.n;
+  a.chunk = chunk_for(c);
+  a.base = 0;
+  a.end = (const int*)c.table;
+  a.list = (const Entry*)((const char*)c.table + ends_bytes(c.n));
+  int64_t chunks = 0;
+  for (int i = 0; i < c.n; ++i) chunks += chunks_of(c.numels[i], a.chunk);
+  const auto kernel = c.ms ? adamw_kernel<8, All> : adamw_kernel<32, All>;
+  for (int64_t at = 0; at < chunks; at += CHUNKS) {
+    a.chunk0 = (int)at;
+    kernel<<<dim3((unsigned)(chunks - at < CHUNKS ? chunks - at : CHUNKS)), dim3(THREADS), 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    h.norm = nullptr;
-    first = false;
-    if (chunks == 0) break;
+    a.h.norm = nullptr;
   }
   return hipSuccess;
 }
 
+hipError_t launch_some(const AdamwCall& c, hipStream_t stream) {
+  Some a;
+  a.h = hyper(c);
+  a.chunk = chunk_for(c);
+  const auto kernel = c.ms ? adamw_kernel<8, Some> : adamw_kernel<32, Some>;
+  int i = 0;
+  bool first = true;
+  for (;;) {
+    a.n = 0;
+    a.base = i;
+    int64_t chunks = 0;
+    for (; i < c.n && a.n < MAX_T; ++i) {
+      const int64_t k = chunks_of(c.numels[i], a.chunk);
+      if (chunks + k > CHUNKS && a.n > 0) break;       // (each tensor fits by itself: checked before)
+      a.list[a.n] = entry(c, i, chunks);
+      chunks += k;
+      a.end[a.n] = (int)chunks;
+      ++a.n;
+    }
+    if (chunks == 0) a.n = 0;
+    // (nothing to do, but a norm to write)
+    if (chunks > 0 || (first && c.norm)) {
+      kernel<<<dim3((unsigned)(chunks ? chunks : 1)), dim3(THREADS), 0, stream>>>(a);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      a.h.norm = nullptr;
+      first = false;
+    }
+    if (i >= c.n) break;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t adamw_table_bytes(int n) { return (size_t)ends_bytes(n) + (size_t)n * sizeof(Entry); }
+
+bool adamw_table_fill(const AdamwCall& c, void* table) {
+  int* const end = (int*)table;
+  Entry* const list = (Entry*)((char*)table + ends_bytes(c.n));
+  const int chunk = chunk_for(c);
+  int64_t chunks = 0;
+  for (int i = 0; i < c.n; ++i) {
+    list[i] = entry(c, i, chunks);
+    chunks += chunks_of(c.numels[i], chunk);
+    if (chunks > TABLE_CHUNKS) return false;
+    end[i] = (int)chunks;
+  }
+  if (c.n % 2) end[c.n] = 0;
+  return true;
+}
+
+hipError_t launch_adamw(const AdamwCall& c, hipStream_t stream) {
+  // (a graph holds what its launches were given: a list by value outlives the caller's table)
+  if (c.table && c.n > MAX_T) {
+    hipStreamCaptureStatus status;
+    const hipError_t e = hipStreamIsCapturing(stream, &status);
+    if (e != hipSuccess) return e;
+    int64_t total = 0;
+    for (int i = 0; i < c.n; ++i) total += c.numels[i];
+    if (status == hipStreamCaptureStatusNone && total > 0) return launch_all(c, stream);
+  }
+  return launch_some(c, stream);
+}
+
 void adamw_kernels(std::vector<const void*>& out) {
-  out.push_back((const void*)adamw_kernel<8>);
-  out.push_back((const void*)adamw_kernel<32>);
+  out.push_back((const void*)adamw_kernel<8, Some>);
+  out.push_back((const void*)adamw_kernel<32, Some>);
+  out.push_back((const void*)adamw_kernel<8, All>);
+  out.push_back((const void*)adamw_kernel<32, All>);
 }
 
 }  // namespace fp8g

@@ -213,8 +213,11 @@ struct AdamwCall {
   float max_norm;
   float* norm;
   uint32_t seed;
+  const void* table;       // null, or what adamw_table_fill wrote, in device memory
 };
 hipError_t launch_adamw(const AdamwCall& c, hipStream_t stream);
+size_t adamw_table_bytes(int n);
+bool adamw_table_fill(const AdamwCall& c, void* table);  // (false: too many chunks for a table)
 void adamw_kernels(std::vector<const void*>& out);
 
 // The allocation-free contiguous entry point's scratch: its size, and its

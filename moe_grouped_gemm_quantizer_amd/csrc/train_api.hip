@@ -329,13 +329,45 @@ fp8g_status grad_clip(const void* const* grads, void* const* outs, const int64_t
       launch_grad_clip(grads, outs, numels, types, n, sumsq, max_norm, norm, stream));
 }
 
+fp8g_status adamw_table_size(int n, size_t* bytes) {
+  if (!bytes) return FP8G_ERR_NULL_PTR;
+  *bytes = 0;
+  if (n < 0) return FP8G_ERR_SHAPE;
+  *bytes = adamw_table_bytes(n);
+  return FP8G_OK;
+}
+
+fp8g_status adamw_table(void* const* params, const int* param_types, const void* const* grads,
+                        const int* grad_types, void* const* exp_avgs, void* const* exp_avg_sqs,
+                        uint8_t* const* avg_scales, uint8_t* const* sq_scales, void* const* copies,
+                        const int* copy_types, const int64_t* numels, int n, void* table) {
+  AdamwCall c = {};
+  c.params = params;
+  c.param_types = param_types;
+  c.grads = grads;
+  c.grad_types = grad_types;
+  c.m = exp_avgs;
+  c.v = exp_avg_sqs;
+  c.ms = avg_scales;
+  c.vs = sq_scales;
+  c.copies = copies;
+  c.copy_types = copy_types;
+  c.numels = numels;
+  c.n = n;
+  const fp8g_status s = adamw_list_ok(c);
+  if (s != FP8G_OK || n == 0) return s;
+  if (!table) return FP8G_ERR_NULL_PTR;
+  if (!aligned(table, 8)) return FP8G_ERR_ALIGN;
+  return adamw_table_fill(c, table) ? FP8G_OK : FP8G_ERR_UNSUPPORTED;
+}
+
 fp8g_status adamw_step(void* const* params, const int* param_types, const void* const* grads,
                        const int* grad_types, void* const* exp_avgs, void* const* exp_avg_sqs,
                        uint8_t* const* avg_scales, uint8_t* const* sq_scales, void* const* copies,
                        const int* copy_types, const int64_t* numels, int n, const int64_t* step,
                        int64_t step_value, const float* lr, double lr_value, double beta1, double beta2,
                        double eps, double weight_decay, const double* sumsq, float max_norm, float* norm,
-                       uint32_t seed, hipStream_t stream) {
+                       uint32_t seed, const void* table, hipStream_t stream) {
   AdamwCall c;
   c.params = params;
   c.param_types = param_types;
@@ -361,6 +393,7 @@ fp8g_status adamw_step(void* const* params, const int* param_types, const void* 
   c.max_norm = max_norm;
   c.norm = norm;
   c.seed = seed;
+  c.table = table;
   const fp8g_status s = adamw_list_ok(c);
   if (s != FP8G_OK) return s;
   if ((!step && step_value < 1) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) ||
@@ -368,7 +401,8 @@ fp8g_status adamw_step(void* const* params, const int* param_types, const void* 
     return FP8G_ERR_SHAPE;
   if (sumsq && !(max_norm > 0.0f)) return FP8G_ERR_SHAPE;
   if (norm && !sumsq) return FP8G_ERR_NULL_PTR;
-  if (!aligned(step, 8) || !aligned(lr, 4) || !aligned(sumsq, 8) || !aligned(norm, 4)) return FP8G_ERR_ALIGN;
+  if (!aligned(step, 8) || !aligned(lr, 4) || !aligned(sumsq, 8) || !aligned(norm, 4) || !aligned(table, 8))
+    return FP8G_ERR_ALIGN;
   DeviceInfo dev;
   if (current_device_info(&dev) != 0) return FP8G_ERR_DEVICE;
   return launched(launch_adamw(c, stream));

@@ -5,6 +5,7 @@ import ctypes
 import numpy as np
 import pytest
 
+from moe_grouped_gemm_quantizer_amd._lib import load
 from oracle.formats import e4m3_decode_table
 from tests import adamw_ref as ref
 from tests.test_abi_host import STATUS, lib  # noqa: F401  (the library fixture)
@@ -26,7 +27,7 @@ def call(lib, n=2, sizes=(5, 300), eight=False, **kw):  # noqa: F811
     base = dict(p=ptrs(), pt=ints(0), g=ptrs(), gt=ints(1), m=ptrs(), v=ptrs(), ms=ptrs() if eight else None,
                 vs=ptrs() if eight else None, c=None, ct=None, numels=ints(list(sizes), ctypes.c_int64), n=n, step=None,
                 step_value=1, lr=None, lr_value=0.1, b1=0.9, b2=0.99, eps=1e-8, wd=0.0, sumsq=None, max_norm=0.0,
-                norm=None, seed=0, stream=None)
+                norm=None, seed=0, table=None, stream=None)
     for k, v in kw.items():
         if isinstance(v, tuple):
             v = ptrs(v[1]) if v[0] == "ptr" else ints(v[1], ctypes.c_int64 if k == "numels" else ctypes.c_int)
@@ -53,9 +54,40 @@ NAN, INF = float("nan"), float("inf")
     (dict(p=("ptr", P + 2)), "ALIGN"), (dict(g=("ptr", P + 1)), "ALIGN"), (dict(m=("ptr", P + 2)), "ALIGN"),
     (dict(v=("ptr", P + 1)), "ALIGN"), (dict(c=("ptr", P + 1), ct=("int", 1)), "ALIGN"), (dict(step=P + 4), "ALIGN"),
     (dict(lr=P + 2), "ALIGN"), (dict(sumsq=P + 4, max_norm=1.0), "ALIGN"), (dict(sumsq=P, max_norm=1.0, norm=P + 1), "ALIGN"),
+    (dict(table=P + 4), "ALIGN"),
 ])
 def test_refusals(lib, kw, status):  # noqa: F811
     assert call(lib, **kw) == STATUS[status]
+
+
+def test_table():
+    """Ends and entries of a list with an empty tensor, as the header's sizes say; refusals."""
+    lib = load()
+    size = ctypes.c_size_t(7)
+    assert lib.adamw_table_size(-1, ctypes.byref(size)) == STATUS["SHAPE"] and size.value == 0
+    assert lib.adamw_table_size(3, None) == STATUS["NULL"]
+    assert lib.adamw_table_size(0, ctypes.byref(size)) == 0 and size.value == 0
+    assert lib.adamw_table_size(3, ctypes.byref(size)) == 0 and size.value == 16 + 3 * 72
+    numels = [5000, 0, 2048]
+    ptr = [(ctypes.c_uint64 * 3)(*[P + 4096 * (3 * j + i) for i in range(3)]) for j in range(4)]
+    typ = (ctypes.c_int * 3)(0, 1, 2)
+    sizes = (ctypes.c_int64 * 3)(*numels)
+    lists = [ptr[0], typ, ptr[1], typ, ptr[2], ptr[3], None, None, None, None, sizes]
+    at = lambda t: None if t is None else ctypes.addressof(t)  # noqa: E731
+    out = np.full(size.value + 8, 0xAB, np.uint8)
+    call = lambda ls, table=None: lib.adamw_table(*map(at, ls), 3, out.ctypes.data if table is None else table)  # noqa: E731
+    assert out.ctypes.data % 8 == 0 and call(lists) == 0
+    assert (out[-8:] == 0xAB).all()
+    assert list(out[:16].view(np.int32)[:3]) == [3, 3, 4]
+    for i, n in enumerate(numels):
+        e = out[16 + 72 * i:16 + 72 * (i + 1)]
+        assert list(e[:64].view(np.uint64)) == [ptr[j][i] for j in range(4)] + [0, 0, 0, n]
+        assert e[64:68].view(np.int32)[0] == [0, 3, 3][i] and e[68] == 4 * i and e[69] == 0
+    assert call(lists, 0) == STATUS["NULL"] and call(lists, out.ctypes.data + 4) == STATUS["ALIGN"]
+    assert call([None] + lists[1:]) == STATUS["NULL"]
+    assert call(lists[:10] + [(ctypes.c_int64 * 3)(5, -1, 3)]) == STATUS["SHAPE"]
+    lists[10] = (ctypes.c_int64 * 3)(*[(1 << 35) - 2048] * 3)
+    assert call(lists) == 0
 
 
 def test_plain_codes():

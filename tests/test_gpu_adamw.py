@@ -349,3 +349,60 @@ def test_binding_refuses():
                      ((1, 0.1), dict(sumsq=z(1), max_norm=1.0))]:
         with pytest.raises(ValueError):
             fp8g.adamw_step(lst, *args, **kw)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("n", [52, 53, 64, 65, 129, 1000, 4097, 9000])
+def test_long_lists(n, bits):
+    """Lists that lie in device memory, empty tensors among them and at both ends."""
+    rng = np.random.default_rng(n)
+    sizes = list(rng.integers(0, 40, n))
+    for i in rng.integers(0, n, 3):
+        sizes[i] = 4500
+    sizes[0] = sizes[-1] = 0
+    q = Problem([int(k) for k in sizes], "f32", "bf16", bits, copy=["bf16"], seed=n)
+    assert (q.list.table is not None) == (n > 52)
+    q.run()
+    q.run(step=4, max_norm=0.05)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_long_list_by_value_and_by_table(bits):
+    """A captured step takes the list by value, whatever becomes of the list's table: the same bits."""
+    sizes = [1 + 37 * i % 400 for i in range(130)]
+    a, b = (Problem(sizes, "bf16", "f32", bits, seed=3) for _ in range(2))
+    lr, step = torch.full((1,), 1e-2, device=dev()), torch.ones(1, dtype=torch.int64, device=dev())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        fp8g.adamw_step(a.list, step, lr, seed=5)
+    table = a.list.table
+    a.list = None
+    table.fill_(0xFF)
+    torch.cuda.synchronize()
+    for t in (1, 2, 3):
+        step.fill_(t)
+        graph.replay()
+        fp8g.adamw_step(b.list, t, 1e-2, seed=5)
+        torch.cuda.synchronize()
+        for x, y in zip([*a.p, *a.m, *a.v], [*b.p, *b.m, *b.v]):
+            assert torch.equal(x, y)
+
+
+def test_long_list_dropped_after_a_step_on_another_stream():
+    sizes = [3000] * 200
+    a, b = (Problem(sizes, seed=4) for _ in range(2))
+    fp8g.adamw_step(b.list, 1, 1e-2)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        x = torch.randn(4096, 4096, device=dev())
+        for _ in range(20):
+            x = x @ x * 1e-4
+        fp8g.adamw_step(a.list, 1, 1e-2)
+    size = a.list.table.numel()
+    a.list = None
+    junk = [torch.full((size,), 0xFF, dtype=torch.uint8, device=dev()) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert len(junk) == 8 and all(torch.equal(x, y) for x, y in zip(a.p + a.m, b.p + b.m))
