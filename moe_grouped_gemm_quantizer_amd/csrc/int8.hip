@@ -566,69 +566,23 @@ int8_tile_kernel(Int8Args a, int nblocks, int xcd_remap) {
 // RING - 1/2 steps ahead. One barrier a step, half way: it publishes the stage that has landed
 // and frees the one whose fragments are all in registers. Position r of fragment i of a wave's
 // rows is row FM r + i (columns likewise), so that a lane's results are runs of 4 FN columns.
+template <int FM, int FN, int RING>
+struct Ring {
+  static constexpr int TM = 64 * FM, TN = 64 * FN, STAGE_BYTES = (TM + TN) * 128, BYTES = RING * STAGE_BYTES;
+  static_assert(sizeof(Experts) <= BYTES, "the list of experts fits the stages' place");
+};
 
-// Workgroups are dealt to the 8 XCDs in turn: an XCD's get a run of tiles.
-__device__ __forceinline__ int xcd_run(int w, int tiles) {
-  const int x = w & 7, most = tiles >> 3, more = tiles & 7;
-  return x * most + min(x, more) + (w >> 3);
-}
-
-// REST: the tiles that int8_tile_kernel leaves, in halves of 128 columns.
-template <int FM, int FN, int RING, bool KTAIL, bool REST>
-__global__ void __launch_bounds__(256, 1)
-int8_ring_kernel(Int8Args a, int nblocks) {
-  constexpr int TM = 64 * FM, TN = 64 * FN;
-  constexpr int RSTAGE = (TM + TN) * 128;
-  constexpr int PER = (TM + TN) / 32;                  // a wave's copies of a stage, 8 rows each
+// The tile of mv rows from `row` (of a, sa and d) and nv columns from n0 of expert g.
+template <int FM, int FN, int RING, bool KTAIL>
+__device__ __forceinline__ void ring_tile(const Int8Args& a, uint8_t* lds, int64_t g, int64_t row, int mv,
+                                          int64_t n0, int nv) {
+  constexpr int TM = 64 * FM;
+  constexpr int RSTAGE = Ring<FM, FN, RING>::STAGE_BYTES;
+  constexpr int PER = (TM + 64 * FN) / 32;             // a wave's copies of a stage, 8 rows each
   constexpr int PAIRS = FM * FN;                       // pairs of matrix instructions in half a step
   static_assert(PER % 2 == 0 && PER / 2 <= 2 * PAIRS, "copies between matrix instructions");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[RING * RSTAGE];
-  static_assert(sizeof(Experts) <= RING * RSTAGE, "the list of experts fits the stages' place");
-  Experts& ex = *reinterpret_cast<Experts*>(lds);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int64_t g = 0, row = 0;
-  int rows = (int)a.rows, before = 0, mblocks = (int)((a.rows + TM - 1) / TM), tiles = mblocks * nblocks, at;
-  if (a.mode != MODE_DENSE) {
-    if (wave == 0) list_experts(a, ex, TM, lane);
-    __syncthreads();
-    tiles = __builtin_amdgcn_readfirstlane(ex.before[ex.n]) * nblocks;
-  }
-  int half = 0;                                        // REST: of its tile's
-  if constexpr (REST) {
-    static_assert(TM == TS && 2 * TN == TS, "halves of the tiles");
-    const int done = (int)full_rounds(tiles, a.round), halves = 2 * (tiles - done);
-    if ((int)blockIdx.x >= halves) return;
-    const int h = xcd_run(blockIdx.x, halves);
-    at = done + h / 2;
-    half = h % 2;
-  } else {
-    if ((int)blockIdx.x >= tiles) return;
-    at = xcd_run(blockIdx.x, tiles);
-  }
-  if (a.mode != MODE_DENSE) {
-    int lo = 0, hi = __builtin_amdgcn_readfirstlane(ex.n) - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (at / nblocks < __builtin_amdgcn_readfirstlane(ex.before[mid + 1])) hi = mid;
-      else lo = mid + 1;
-    }
-    before = __builtin_amdgcn_readfirstlane(ex.before[lo]);
-    mblocks = __builtin_amdgcn_readfirstlane(ex.before[lo + 1]) - before;
-    g = __builtin_amdgcn_readfirstlane(ex.id[lo]);
-    rows = __builtin_amdgcn_readfirstlane(ex.rows[lo]);
-    row = a.mode == MODE_MASKED ? g * a.rows : __builtin_amdgcn_readfirstlane(ex.row0[lo]);
-    __syncthreads();                                   // (read by all: the copies may come)
-  }
-  int mb, nb;
-  gidx::swizzle_tile(at - before * nblocks, mblocks, nblocks, REST ? 4 : 8, mb, nb);
-  if constexpr (REST) {
-    nb = 2 * nb + half;
-    if ((int64_t)nb * TN >= a.N) return;               // (uniform over the workgroup)
-  }
-  const int64_t m0 = (int64_t)mb * TM, n0 = (int64_t)nb * TN;
-  const int mv = (int)min((int64_t)TM, rows - m0), nv = (int)min((int64_t)TN, a.N - n0);
-  row += m0;
   const int steps = (int)((a.K + 127) / 128), kr = (int)(a.K % 128);
   // copy c: LDS rows 8 q .. +7 of the stage, q = wave PER + c, a's first
   const int8_t* const pa = a.a + row * a.K;
@@ -770,6 +724,80 @@ int8_ring_kernel(Int8Args a, int nblocks) {
       }
     }
   }
+}
+
+// Workgroups are dealt to the 8 XCDs in turn: an XCD's get a run of tiles.
+__device__ __forceinline__ int xcd_run(int w, int tiles) {
+  const int x = w & 7, most = tiles >> 3, more = tiles & 7;
+  return x * most + min(x, more) + (w >> 3);
+}
+
+// Tile `at` of a launch's (rows of `side`): its expert, the expert's first row and rows, the tile's place.
+struct Place {
+  int64_t g, row;
+  int rows, mb, nb;
+};
+__device__ __forceinline__ int list_tiles(const Int8Args& a, Experts& ex, int side, int nblocks) {
+  if (a.mode == MODE_DENSE) return (int)((a.rows + side - 1) / side) * nblocks;
+  if (threadIdx.x < 64) list_experts(a, ex, side, threadIdx.x);
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(ex.before[ex.n]) * nblocks;
+}
+__device__ __forceinline__ Place place_of(const Int8Args& a, const Experts& ex, int at, int side, int nblocks, int swizzle) {
+  Place p = {0, 0, (int)a.rows, 0, 0};
+  int before = 0, mblocks = (int)((a.rows + side - 1) / side);
+  if (a.mode != MODE_DENSE) {
+    int lo = 0, hi = __builtin_amdgcn_readfirstlane(ex.n) - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (at / nblocks < __builtin_amdgcn_readfirstlane(ex.before[mid + 1])) hi = mid;
+      else lo = mid + 1;
+    }
+    before = __builtin_amdgcn_readfirstlane(ex.before[lo]);
+    mblocks = __builtin_amdgcn_readfirstlane(ex.before[lo + 1]) - before;
+    p.g = __builtin_amdgcn_readfirstlane(ex.id[lo]);
+    p.rows = __builtin_amdgcn_readfirstlane(ex.rows[lo]);
+    p.row = a.mode == MODE_MASKED ? p.g * a.rows : __builtin_amdgcn_readfirstlane(ex.row0[lo]);
+    __syncthreads();                                   // (read by all: the copies may come)
+  }
+  gidx::swizzle_tile(at - before * nblocks, mblocks, nblocks, swizzle, p.mb, p.nb);
+  return p;
+}
+
+template <int FM, int FN, int RING, bool KTAIL>
+__global__ void __launch_bounds__(256, 1)
+int8_ring_kernel(Int8Args a, int nblocks) {
+  using R = Ring<FM, FN, RING>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[R::BYTES];
+  Experts& ex = *reinterpret_cast<Experts*>(lds);
+  const int tiles = list_tiles(a, ex, R::TM, nblocks);
+  if ((int)blockIdx.x >= tiles) return;
+  const Place p = place_of(a, ex, xcd_run(blockIdx.x, tiles), R::TM, nblocks, 8);
+  const int64_t m0 = (int64_t)p.mb * R::TM, n0 = (int64_t)p.nb * R::TN;
+  ring_tile<FM, FN, RING, KTAIL>(a, lds, p.g, p.row + m0, (int)min((int64_t)R::TM, p.rows - m0), n0,
+                                 (int)min((int64_t)R::TN, a.N - n0));
+}
+
+// The tiles that int8_tile_kernel leaves, in quarters where these are no more than the CUs, else in
+// halves of 128 columns.
+__global__ void __launch_bounds__(256, 1)
+int8_rest_kernel(Int8Args a, int nblocks) {
+  using Half = Ring<4, 2, 3>;
+  using Quarter = Ring<2, 2, 4>;
+  static_assert(Half::TM == TS && 2 * Half::TN == TS && 2 * Quarter::TM == TS && 2 * Quarter::TN == TS, "parts of the tiles");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Half::BYTES > Quarter::BYTES ? Half::BYTES : Quarter::BYTES];
+  Experts& ex = *reinterpret_cast<Experts*>(lds);
+  const int tiles = list_tiles(a, ex, TS, nblocks);
+  const int done = (int)full_rounds(tiles, a.round), rest = tiles - done;
+  const int cut = 4 * rest <= a.round ? 4 : 2;
+  if ((int)blockIdx.x >= cut * rest) return;
+  const int h = xcd_run(blockIdx.x, cut * rest);
+  const Place p = place_of(a, ex, done + h / cut, TS, nblocks, 4);
+  const int64_t m0 = (int64_t)p.mb * TS + (cut == 4 ? h % 4 / 2 * Quarter::TM : 0), n0 = (int64_t)p.nb * TS + h % 2 * Half::TN;
+  if (m0 >= p.rows || n0 >= a.N) return;               // (uniform over the workgroup)
+  const int nv = (int)min((int64_t)Half::TN, a.N - n0);
+  if (cut == 4) ring_tile<2, 2, 4, false>(a, lds, p.g, p.row + m0, (int)min((int64_t)Quarter::TM, p.rows - m0), n0, nv);
+  else ring_tile<4, 2, 3, false>(a, lds, p.g, p.row + m0, (int)min((int64_t)TS, p.rows - m0), n0, nv);
 }
 
 // ---------------------------------------------------------------------------
@@ -936,7 +964,8 @@ Kernel choose(const Int8Args& a, int expected_m, int cus) {
     const int64_t tiles = blocks(a.rows, c.tm) * blocks(a.N, c.tn);
     const int64_t kb = blocks(a.K, 128), last = k == TILE256 ? tiles - full_rounds(tiles, cus) : 0;
     int64_t t = c.start + blocks(tiles - last, cus) * (c.round + (a.K % 128 ? c.odd : c.block) * kb);
-    if (last) t += kCost[RING256].start + kCost[RING256].round + kCost[RING256].block * kb;
+    const Cost& r = kCost[4 * last <= cus ? RING128 : RING256];
+    if (last) t += r.start + r.round + r.block * kb;
     if (t < least) {
       least = t;
       best = k;
@@ -953,8 +982,8 @@ SkinnyFn skinny_pick(Kernel k, bool tail) {
   return tail ? int8_skinny_kernel<4, 4, 2, true> : int8_skinny_kernel<4, 4, 2, false>;
 }
 TilesFn ring_pick(Kernel k, bool tail) {
-  if (k == RING128) return tail ? int8_ring_kernel<2, 2, 4, true, false> : int8_ring_kernel<2, 2, 4, false, false>;
-  return tail ? int8_ring_kernel<4, 2, 3, true, false> : int8_ring_kernel<4, 2, 3, false, false>;
+  if (k == RING128) return tail ? int8_ring_kernel<2, 2, 4, true> : int8_ring_kernel<2, 2, 4, false>;
+  return tail ? int8_ring_kernel<4, 2, 3, true> : int8_ring_kernel<4, 2, 3, false>;
 }
 
 }  // namespace
@@ -984,10 +1013,10 @@ hipError_t launch_int8(const Int8Args& args, const DeviceInfo& dev, int expected
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
-    const int64_t rest = args.mode != MODE_DENSE ? (tiles < all.round / 2 ? tiles : all.round / 2)
-                                                 : tiles - full_rounds(tiles, all.round);
-    if (rest > 0)
-      int8_ring_kernel<4, 2, 3, false, true><<<dim3((unsigned)(2 * rest)), dim3(256), 0, stream>>>(all, (int)nb);
+    // (at most round / 2 tiles: their parts are no more than a round)
+    const int64_t rest = args.mode != MODE_DENSE ? tiles : tiles - full_rounds(tiles, all.round);
+    const int64_t parts = 4 * rest < all.round ? 4 * rest : all.round;
+    if (rest > 0) int8_rest_kernel<<<dim3((unsigned)parts), dim3(256), 0, stream>>>(all, (int)nb);
   }
   return hipGetLastError();
 }
@@ -1004,7 +1033,7 @@ void int8_kernels(std::vector<const void*>& out) {
     for (Kernel k : {RING128, RING256}) out.push_back((const void*)ring_pick(k, tail));
   }
   out.push_back((const void*)int8_tile_kernel);
-  out.push_back((const void*)int8_ring_kernel<4, 2, 3, false, true>);
+  out.push_back((const void*)int8_rest_kernel);
 }
 
 }  // namespace fp8g
