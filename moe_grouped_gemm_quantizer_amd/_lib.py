@@ -555,7 +555,8 @@ def moe_route_scored(logits, top_k, expert_ids, weights, counts, routed, prob_su
     if token_mask is not None:
         mask = _out(token_mask, (T,), torch.uint8 if token_mask.dtype is torch.uint8 else torch.bool, "token_mask")
     wp, wb = _room(workspace)
-    _one_device(logits, expert_ids, weights, slots, counts)
+    _one_device(logits, expert_ids, weights, counts, routed, prob_sum, loss, group_offsets, slots, bias, token_mask,
+                workspace)
     st = load().moe_route_scored(ptr, typ, T, E, ld, bia, _score(score), groups, open_groups, group_best, mask,
                                  top_k, 1 if renormalise else 0, scale, loss_coef, align, max_m, ids, wts, cnt,
                                  rtd, psm, los, off, slt, wp, wb, _stream(stream))
@@ -580,7 +581,7 @@ def moe_route_scored_backward(logits, expert_ids, d_weights, d_loss, counts, rou
     dl = None if d_loss is None else _out(d_loss, (1,), torch.float32, "d_loss")
     cnt = _out(counts, (E,), torch.int32, "counts")
     rtd = _out(routed, (1,), torch.int32, "routed")
-    _one_device(logits, expert_ids, d_logits, counts)
+    _one_device(logits, expert_ids, d_weights, d_loss, counts, routed, d_logits)
     st = load().moe_route_scored_backward(ptr, typ, T, E, ld, _score(score), ids, top_k, 1 if renormalise else 0,
                                           scale, loss_coef, dw, dl, cnt, rtd, dptr, ldd, _stream(stream))
     if st:
@@ -815,13 +816,16 @@ def adamw_step(tensors, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay
     if tensors.n and tensors.device != _torch()._C._cuda_getDevice():
         _fail("the tensors are not on the current device")
     torch = _torch()
-    sp = lp = None
+    sp = lp = step_at = lr_at = None
     if isinstance(step, torch.Tensor):
+        step_at = step
         sp, step = _out(step, (1,) if step.dim() else (), torch.int64, "step"), 1
     if isinstance(lr, torch.Tensor):
+        lr_at = lr
         lp, lr = _out(lr, (1,) if lr.dim() else (), torch.float32, "lr"), 0.0
     total = None if sumsq is None else _out(sumsq, (1,), torch.float64, "sumsq")
     nrm = None if norm is None else _out(norm, (1,), torch.float32, "norm")
+    _one_device(step_at, lr_at, sumsq, norm)
     on, table = _stream(stream), tensors.table
     if table is not None:
         if on not in tensors.streams:        # (its memory is not used again before the steps there are done)
@@ -836,10 +840,10 @@ def adamw_step(tensors, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay
 
 def _one_device(*ts):
     """The calls below launch on the current device, whose memory the tensors
-    have to be."""
+    have to be (None: not given)."""
     at = _torch()._C._cuda_getDevice()
     for t in ts:
-        if t.get_device() != at:
+        if t is not None and t.get_device() != at:
             _fail(f"tensors must live on the current device (cuda:{at})")
 
 

@@ -406,3 +406,43 @@ def test_long_list_dropped_after_a_step_on_another_stream():
     junk = [torch.full((size,), 0xFF, dtype=torch.uint8, device=dev()) for _ in range(8)]
     torch.cuda.synchronize()
     assert len(junk) == 8 and all(torch.equal(x, y) for x, y in zip(a.p + a.m, b.p + b.m))
+
+
+def test_long_list_made_on_another_stream():
+    """The list's table is there for a step on any stream, the default one too."""
+    side = torch.cuda.Stream()
+    a, b = (Problem([900] * 60, seed=6) for _ in range(2))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        a.list = fp8g.adamw_tensors(a.p, a.g, a.m, a.v)
+    fp8g.adamw_step(a.list, 1, 1e-2)
+    a.list = None
+    fp8g.adamw_step(b.list, 1, 1e-2, stream=side)
+    b.list = None
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(a.p + a.m, b.p + b.m))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_tensor_of_more_than_32_bits_elements(bits):
+    """Elements past 2^32 step as a short tensor's do (parameters: the states' rounding goes by the
+    element's number)."""
+    n, tail = (1 << 32) + 5000, 4999
+    kind = torch.bfloat16
+    gen = torch.Generator(dev()).manual_seed(2)
+    p, g = torch.zeros(n, device=dev(), dtype=kind), torch.zeros(n, device=dev(), dtype=kind)
+    p[-tail:].normal_(generator=gen)
+    g[-tail:].normal_(generator=gen)
+    p[:5], g[:5] = p[-5:], g[-5:]
+    state = torch.uint8 if bits == 8 else torch.float32
+    zeros = lambda k, t: torch.zeros(k, device=dev(), dtype=t)  # noqa: E731
+    scales = lambda k: dict(m_scales=[zeros(-(-k // 128), torch.uint8)],  # noqa: E731
+                            v_scales=[zeros(-(-k // 128), torch.uint8)]) if bits == 8 else {}
+    small = [p[-tail:].clone(), g[-tail:].clone()]
+    big_m, big_v, m, v = zeros(n, state), zeros(n, state), zeros(tail, state), zeros(tail, state)
+    fp8g.adamw_step(fp8g.adamw_tensors([p], [g], [big_m], [big_v], **scales(n)), 1, 1e-2)
+    fp8g.adamw_step(fp8g.adamw_tensors([small[0]], [small[1]], [m], [v], **scales(tail)), 1, 1e-2)
+    assert torch.equal(p[-tail:], small[0]) and torch.equal(p[:5], small[0][-5:])
+    assert not p[5:-tail].any() and big_m[-tail:].any()
+    if bits == 32:
+        assert torch.equal(big_m[-tail:], m) and torch.equal(big_v[-tail:], v) and not big_m[5:-tail].any()

@@ -339,3 +339,68 @@ def test_offsets_in_any_order_stay_inside(K):
     starts = np.maximum.accumulate(np.clip(off, 0, M))
     want = ref.contiguous(a, sa, b, sb, starts, np.full((M, N), STALE, np.uint16))
     assert np.array_equal(to_host(d).view(np.uint16), want) and len(np.unique(starts)) > 4
+
+
+@pytest.mark.parametrize("K", [65536, 65552])
+def test_offsets_past_32_bits(K):
+    """More than 2^32 elements of x, codes and operands: quantised and multiplied rows at both ends."""
+    M, N = 66000, 144
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device=dev())
+    rows = [0, 1, 32767, 32768, 65535, 65536, M - 2, M - 1]
+    gen = torch.Generator(dev()).manual_seed(1)
+    x[rows] = torch.randn(len(rows), K, device=dev(), generator=gen).to(torch.bfloat16)
+    q = torch.full((M, K), 3, dtype=torch.int8, device=dev())
+    s = torch.full((M,), -1.0, device=dev())
+    fp8g.int8_quantize(x, q, s)
+    qr, sr = ref.quantise(to_host(x[rows].float()))
+    assert np.array_equal(to_host(q[rows]), qr) and np.array_equal(to_host(s[rows]), sr)
+    assert int(s.count_nonzero()) == len(rows) and int(torch.count_nonzero(q[rows[3] + 1:rows[4]])) == 0
+    del x
+    rng = np.random.default_rng(K)
+    b, sb = codes(rng, N, K), scales(rng, N)
+    d = torch.full((M, N), STALE, dtype=torch.int16, device=dev())
+    fp8g.gemm_int8(q, s, to_dev(b), to_dev(sb), d)
+    want = ref.product(qr, sr, b, sb)
+    assert np.array_equal(to_host(d[rows]).view(np.uint16), want)
+    assert int((d[rows[3] + 1:rows[4]] & 0x7FFF).count_nonzero()) == 0
+    off = torch.tensor([0, 32769, 65536, M], dtype=torch.int32, device=dev())
+    three = np.stack([b[::-1], b, b[:, ::-1]])
+    d2 = torch.full((M, N), STALE, dtype=torch.int16, device=dev())
+    fp8g.grouped_gemm_int8_contiguous(q, s, to_dev(three.copy()), to_dev(np.stack([sb, sb, sb])), d2, off)
+    for r, row in enumerate(rows):
+        g = (row >= 32769) + (row >= 65536)
+        assert np.array_equal(to_host(d2[row]).view(np.uint16), ref.product(qr[r:r + 1], sr[r:r + 1], three[g], sb)[0])
+
+
+def test_captured_and_replayed_on_two_streams():
+    """Quantiser and product captured twice, replayed at once on two streams with new inputs: no
+    shared memory of the library's own."""
+    M, N, K = 300, 528, 512
+    gen = torch.Generator(dev()).manual_seed(3)
+    w = torch.randn(N, K, device=dev(), generator=gen)
+    qw, sw = torch.empty(N, K, dtype=torch.int8, device=dev()), torch.empty(N, device=dev())
+    fp8g.int8_quantize(w, qw, sw)
+    torch.cuda.synchronize()
+    work = []
+    for _ in range(2):
+        x = torch.randn(M, K, device=dev(), generator=gen)
+        q, s = torch.empty(M, K, dtype=torch.int8, device=dev()), torch.empty(M, device=dev())
+        d = torch.empty(M, N, dtype=torch.bfloat16, device=dev())
+        side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            fp8g.int8_quantize(x, q, s)
+            fp8g.gemm_int8(q, s, qw, sw, d)
+        work.append((x, q, s, d, side, graph))
+    for t in range(4):
+        for x, *_ in work:
+            x.normal_(generator=gen)
+        torch.cuda.synchronize()
+        for *_, side, graph in work:
+            with torch.cuda.stream(side):
+                graph.replay()
+        torch.cuda.synchronize()
+        for x, q, s, d, *_ in work:
+            q0, s0 = ref.quantise(to_host(x))
+            assert np.array_equal(to_host(q), q0)
+            want = ref.product(q0, s0, to_host(qw), to_host(sw))
+            assert np.array_equal(to_host(d.view(torch.int16)).view(np.uint16), want)

@@ -329,3 +329,32 @@ def test_binding_refuses():
         k = kw.pop("k", 2)
         with pytest.raises(fp8g.Fp8GemmError):
             call(x, k, **kw)
+
+
+def test_more_tokens_than_a_launch_holds():
+    """64 tokens a workgroup of 1024 threads: from 2^28 tokens on more than the 2^32 threads that a
+    launch may have. Two experts, a bias that favours the second."""
+    T, E = (1 << 28) + 12345, 2
+    g = torch.Generator(dev()).manual_seed(1)
+    x = torch.randint(-8, 9, (T, E), device=dev(), generator=g, dtype=torch.int8).to(torch.bfloat16)
+    i, f = torch.int32, torch.float32
+    new = lambda shape, t: torch.full(shape, 77, dtype=t, device=dev())  # noqa: E731
+    out = dict(expert_ids=new((T, 1), i), weights=new((T, 1), f), counts=new((E,), i), routed=new((1,), i),
+               prob_sum=new((E,), f), loss=new((1,), f), group_offsets=new((E + 1,), i), slots=new((T, 1), i))
+    ws = torch.full((fp8g.moe_route_workspace_size(T, E),), 0x5A, dtype=torch.uint8, device=dev())
+    bias = torch.tensor([0.0, 1e-5], device=dev())
+    fp8g.moe_route_scored(x, 1, *out.values(), ws, bias=bias)
+    # (scores of whole numbers up to 8 in size are alike or differ by 5.7e-4 and more)
+    second = x[:, 1] >= x[:, 0]
+    ids = out["expert_ids"][:, 0]
+    assert torch.equal(ids == 1, second) and bool(((ids == 0) | (ids == 1)).all())
+    n1 = int(second.sum())
+    assert out["counts"].tolist() == [T - n1, n1] and out["routed"].item() == T
+    ends = [0, (T - n1 + 127) // 128 * 128]
+    rank = torch.cumsum(second, 0)
+    at = torch.arange(T, device=dev())
+    assert torch.equal(out["slots"][:, 0].long(), torch.where(second, ends[1] + rank - 1, at - rank))
+    del rank, at
+    top = torch.sigmoid(torch.where(second, x[:, 1], x[:, 0]).float())
+    # (two exponentials of a few ulp and the quotients)
+    assert bool(((out["weights"][:, 0] - top).abs() <= 16 * 2.0 ** -24 * top).all())
