@@ -145,7 +145,7 @@ struct ScoredBwdCall {
   int score;
   float scale;
 };
-hipError_t launch_route_scored(const ScoredCall& c, hipStream_t stream);
+hipError_t launch_route_scored(const ScoredCall& c, hipStream_t stream, int cu_count);
 hipError_t launch_route_scored_backward(const ScoredBwdCall& c, hipStream_t stream, int cu_count);
 void route_scored_kernels(std::vector<const void*>& out);
 

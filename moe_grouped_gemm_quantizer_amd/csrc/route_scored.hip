@@ -686,8 +686,12 @@ route_scored_backward_kernel(ScoredBwdArgs a) {
   }
 }
 
-// The kernels for a type and an E: as in route.hip, 16 lanes a row up to 256 experts, 64 above and
-// for up to four tokens.
+// The kernels for a type, an E and a number of tokens: as in route.hip, 16 lanes a row up to 256 experts,
+// 64 above and for up to four tokens (T 4, E 256 7.8 us; five with 16 lanes 11.8). With 12 values a
+// lane and more the workgroups are of 512 threads, twice on a CU, which overlaps one's end with the other's
+// start (T 32768, E 256 47.5 us, of 1024 52.2; T 32 12.4 / 14.2), but where the blocks are no more than
+// the CUs and have two rows for each group of lanes (T 64 18.4 / 14.7, T 4096 30.5 / 26.3, T 16384
+// 37.4 / 31.9). Above 512 experts 1024 threads would spill (T 8192, E 1024 82 / 91).
 typedef void (*RowsFn)(ScoredArgs);
 typedef void (*BwdFn)(ScoredBwdArgs);
 struct Pick {
@@ -696,41 +700,41 @@ struct Pick {
   BwdFn bwd;
   int rows_at_once, lanes;
 };
-template <typename T, int NT>
+enum Width { FEW, NARROW, WIDE };                      // 256, 512 or 1024, 1024 threads
+template <typename T, Width W>
 Pick pick_for(int E) {
-  constexpr bool few = NT == THREADS;
-  constexpr int WIDE = NT > 512 ? 512 : NT;
-#define FP8G_PICK(LPR_, VPT_)                                                                    \
-  Pick { route_scored_rows_kernel<T, LPR_, VPT_, VPT_ >= 12 ? WIDE : NT>,                        \
-         VPT_ >= 12 ? WIDE : NT, route_scored_backward_kernel<T, LPR_, VPT_>,      \
-         THREADS / LPR_, LPR_ }
-  if (E <= 16) return FP8G_PICK(16, 1);
-  if (E <= 32) return FP8G_PICK(16, 2);
-  if (E <= 64) return FP8G_PICK(16, 4);
-  if constexpr (few) {
-    if (E <= 256) return FP8G_PICK(64, 4);
+#define FP8G_PICK(LPR_, VPT_, NT_)                                                        \
+  Pick { route_scored_rows_kernel<T, LPR_, VPT_, NT_>, NT_,                               \
+         route_scored_backward_kernel<T, LPR_, VPT_>, THREADS / LPR_, LPR_ }
+  constexpr int NT = W == FEW ? THREADS : 1024, MANY = W == WIDE ? 1024 : 512;
+  if (E <= 16) return FP8G_PICK(16, 1, NT);
+  if (E <= 32) return FP8G_PICK(16, 2, NT);
+  if (E <= 64) return FP8G_PICK(16, 4, NT);
+  if constexpr (W == FEW) {
+    if (E <= 256) return FP8G_PICK(64, 4, NT);
   } else {
-    if (E <= 128) return FP8G_PICK(16, 8);
-    if (E <= 192) return FP8G_PICK(16, 12);
-    if (E <= 256) return FP8G_PICK(16, 16);
+    if (E <= 128) return FP8G_PICK(16, 8, NT);
+    if (E <= 192) return FP8G_PICK(16, 12, MANY);
+    if (E <= 256) return FP8G_PICK(16, 16, MANY);
   }
-  if (E <= 512) return FP8G_PICK(64, 8);
-  return FP8G_PICK(64, 16);
+  if (E <= 512) return FP8G_PICK(64, 8, NT);
+  return FP8G_PICK(64, 16, (W == FEW ? THREADS : 512));
 #undef FP8G_PICK
 }
 template <typename T>
-Pick pick_of(int E, int64_t tokens) {
-  return tokens <= 4 ? pick_for<T, THREADS>(E) : pick_for<T, 1024>(E);
+Pick pick_of(int E, int64_t tokens, int cus) {
+  if (tokens <= 4) return pick_for<T, FEW>(E);
+  return tokens > ROWS / 2 && tokens <= (int64_t)ROWS * cus ? pick_for<T, WIDE>(E) : pick_for<T, NARROW>(E);
 }
-Pick pick(int type, int E, int64_t T) {
-  return type == TYPE_F32    ? pick_of<float>(E, T)
-         : type == TYPE_BF16 ? pick_of<bf16_t>(E, T)
-                             : pick_of<f16_t>(E, T);
+Pick pick(int type, int E, int64_t T, int cus) {
+  return type == TYPE_F32    ? pick_of<float>(E, T, cus)
+         : type == TYPE_BF16 ? pick_of<bf16_t>(E, T, cus)
+                             : pick_of<f16_t>(E, T, cus);
 }
 
 }  // namespace
 
-hipError_t launch_route_scored(const ScoredCall& c, hipStream_t stream) {
+hipError_t launch_route_scored(const ScoredCall& c, hipStream_t stream, int cu_count) {
   ScoredArgs a;
   a.r = route_args(c.route);
   a.bias = c.bias;
@@ -744,7 +748,7 @@ hipError_t launch_route_scored(const ScoredCall& c, hipStream_t stream) {
   a.scale = c.scale;
   const int64_t nblk = (c.route.T + ROWS - 1) / ROWS;
   if (nblk == 0) return launch_route_places(c.route, stream);
-  const Pick p = pick(c.route.type, c.route.E, c.route.T);
+  const Pick p = pick(c.route.type, c.route.E, c.route.T, cu_count);
   a.part_bits = a.part_bits64 = 0;
   while (c.groups << (a.part_bits + 1) <= p.lanes) ++a.part_bits;
   while (c.groups << (a.part_bits64 + 1) <= 64) ++a.part_bits64;
@@ -779,7 +783,7 @@ hipError_t launch_route_scored_backward(const ScoredBwdCall& c, hipStream_t stre
   a.score = c.score;
   a.coef = r.coef;
   a.scale = c.scale;
-  const Pick p = pick(r.type, r.E, r.T);
+  const Pick p = pick(r.type, r.E, r.T, cu_count);
   int64_t grid = (r.T + p.rows_at_once - 1) / p.rows_at_once;
   if (grid > (int64_t)cu_count * BWD_PER_CU) grid = (int64_t)cu_count * BWD_PER_CU;
   p.bwd<<<dim3((unsigned)grid), dim3(THREADS), 0, stream>>>(a);
@@ -789,8 +793,8 @@ hipError_t launch_route_scored_backward(const ScoredBwdCall& c, hipStream_t stre
 void route_scored_kernels(std::vector<const void*>& out) {
   for (int type : {TYPE_F32, TYPE_BF16, TYPE_F16})
     for (int E : {16, 32, 64, 128, 192, 256, 512, 1024})
-      for (int T : {1, 64}) {
-        const Pick p = pick(type, E, T);
+      for (int T : {1, 5, 64}) {
+        const Pick p = pick(type, E, T, 1);
         out.push_back((const void*)p.rows);
         out.push_back((const void*)p.bwd);
       }

@@ -212,7 +212,7 @@ fp8g_status moe_route_scored(const void* logits, int type, int64_t T, int E, int
   c.open = open_groups;
   c.best = group_best;
   c.scale = scale;
-  return launched(launch_route_scored(c, stream));
+  return launched(launch_route_scored(c, stream, dev.cu_count));
 }
 
 fp8g_status moe_route_scored_backward(const void* logits, int type, int64_t T, int E, int64_t ld, int score,

@@ -25,8 +25,8 @@ TYPES = r"I(f|DF16b|DF16_)"
 def test_scored_routing(names):
     have = set(re.findall(r"24route_scored_rows_kernel" + TYPES + r"Li(\d+)ELi(\d+)ELi(\d+)EEEvNS0_10ScoredArgsE", names))
     few = {(16, 1, 256), (16, 2, 256), (16, 4, 256), (64, 4, 256), (64, 8, 256), (64, 16, 256)}
-    many = {(16, 1, 1024), (16, 2, 1024), (16, 4, 1024), (16, 8, 1024), (16, 12, 512), (16, 16, 512), (64, 8, 1024),
-            (64, 16, 512)}
+    many = {(16, 1, 1024), (16, 2, 1024), (16, 4, 1024), (16, 8, 1024), (16, 12, 512), (16, 16, 512), (16, 12, 1024),
+            (16, 16, 1024), (64, 8, 1024), (64, 16, 512)}
     assert {tuple(map(int, k[1:])) for k in have} == few | many and len(have) == 3 * len(few | many)
     back = set(re.findall(r"28route_scored_backward_kernel" + TYPES + r"Li(\d+)ELi(\d+)EEEv", names))
     assert {tuple(map(int, k[1:])) for k in back} == {k[:2] for k in few | many}
