@@ -86,6 +86,10 @@ __device__ __forceinline__ void store_codes(const Pack<T, W>& p, const RowScale&
 
 // LPR lanes (a wave or the workgroup) a row, up to NV 16-byte pieces of it a lane, held in
 // registers between the maximum and the codes; NV == 0: rows of any length, read twice.
+// An HBM stream: 4096 x 7168 bf16 in 18.1 us, 4.9 TB/s (a large copy: 5.0). A wave a row up to
+// 256 pieces, which spares short rows the workgroup's barrier (4096 x 512 bf16 3.4 us, a workgroup a
+// row 6.3; 8192 x 2048 12.4 / 12.5), and a workgroup above (4096 x 4096 11.2, a wave with 16 pieces a
+// lane 15.4); rows of up to 2048 pieces stay in registers (2048 x 16384 bf16 21.4 us, read twice 27.2).
 template <typename T, int LPR, int NV>
 __global__ void __launch_bounds__(QTHREADS)
 int8_quantize_kernel(const T* __restrict__ x, int64_t rows, int64_t cols, int64_t ldx, int vec,
@@ -255,7 +259,11 @@ __device__ __forceinline__ void list_experts(const Int8Args& a, Experts& ex, int
   }
 }
 
-// 256x256 tiles: four waves of 128x128, one per SIMD, the 256 accumulators of a lane in the
+// 256x256 tiles, bound by the matrix unit and, beside it, the issue of its copies and the clock that the
+// chip holds under it: 4096x8192x8192 in 210 to 230 us, 2.4 to 2.6 POPS (the library's own product 231 us;
+// 128x128 tiles of one workgroup each 319, 256x128 267). Where each weight is read for one row
+// block, HBM: 32 experts 7168x2048 of up to 256 rows 141 us, 3.8 TB/s.
+// Four waves of 128x128, one per SIMD, the 256 accumulators of a lane in the
 // accumulation registers. A workgroup walks tiles (expert, row block, column block); the
 // 128-byte steps of all its tiles form one sequence with two LDS stages. A step's 64
 // matrix instructions (32 pairs):
@@ -278,10 +286,10 @@ constexpr int EARLY_FIRST = 8;                         // of these, issued in a 
 constexpr int STORES = 32;                             // a wave's stores of a full tile
 
 // Of `tiles` on `round` workgroups those that are walked whole: all, but for a last round that would
-// leave half of the workgroups or more without one. Its tiles go to int8_ring_kernel<.., REST> in two
-// halves each, which takes 0.6 of a round (512 rows over 8 experts 4096x7168, all of it such a
-// round, 78 -> 54 us; 4096x6144x7168, 1.5 rounds, 195 -> 165; 4096 rows over 8 experts, 1.4 rounds,
-// 174 -> 161; where weights from memory bound the launch, as 8192x7168x2048 with 3.5, 147 -> 149).
+// leave half of the workgroups or more without one. Its tiles go to int8_rest_kernel in two or four
+// parts, which take 0.6 of a round as halves, 0.35 as quarters (4096x6144x7168, 1.5 rounds, 195 -> 159
+// us; 4096x4608x7168, 1.1, 171 -> 127; 4096 rows over 8 experts, 1.2, 174 -> 139; where weights from
+// memory bound the launch, as 8192x7168x2048 with 3.5, 147 -> 149).
 __host__ __device__ __forceinline__ uint32_t full_rounds(uint32_t tiles, uint32_t round) {
   const uint32_t rest = tiles % round;
   return rest <= round / 2 ? tiles - rest : tiles;
@@ -566,6 +574,9 @@ int8_tile_kernel(Int8Args a, int nblocks, int xcd_remap) {
 // RING - 1/2 steps ahead. One barrier a step, half way: it publishes the stage that has landed
 // and frees the one whose fragments are all in registers. Position r of fragment i of a wave's
 // rows is row FM r + i (columns likewise), so that a lane's results are runs of 4 FN columns.
+// Bound by a step's reads of LDS and its barrier: 0.7 of a 256x256 tile's rate, a loss smaller than that
+// of CUs without work where 256x256 tiles are few (see kCost). 777x2064x1040 takes 11.3 us, of which 6
+// are the launch and the pipeline's first and last steps.
 template <int FM, int FN, int RING>
 struct Ring {
   static constexpr int TM = 64 * FM, TN = 64 * FN, STAGE_BYTES = (TM + TN) * 128, BYTES = RING * STAGE_BYTES;
@@ -804,9 +815,12 @@ int8_rest_kernel(Int8Args a, int nblocks) {
 // Few rows: the work is streaming b, and a again for every column block. A workgroup owns
 // 16 NT output columns and up to 16 MT rows; its four waves take the 128-byte blocks of K in
 // turn, each with a ring of DEPTH stages of its own in LDS, so that no wave waits for another
-// until their sums meet. Whole 128-byte lines go straight into LDS: the same fragments loaded
-// from global memory into registers touch 16 lines of which they take half, and cost twice the
-// cycles.
+// until their sums meet; two or three workgroups on a CU rather than a deeper ring, which overlaps
+// their starts and ends too (16x28672x4096 26.3 us with 3 stages, 37.4 with 8; 32x14336x4096 15.9 with 2,
+// 18.7 with 5; 512x4096x4096 16.8 with one, 19.8 with 2). Whole 128-byte lines go straight into LDS:
+// the same fragments loaded from global memory into registers touch 16 lines of which they take half,
+// and cost twice the cycles. Bound by HBM and by the latency of the first and last steps: 16x4096x7168
+// 8.0 us, 16x8192x8192 15.1, 4.4 TB/s (128x128 tiles 26 and 30).
 constexpr int SK_WAVES = 4;
 
 template <int MT, int NT, int DEPTH, bool KTAIL>
@@ -921,21 +935,22 @@ int8_skinny_kernel(Int8Args a) {
   }
 }
 
-// The kernels, from few rows to many. A launch takes `start` and, for each round of workgroups
-// over the CUs (one fits a CU), `round` and for each 128 bytes of K `block`, or `odd` where K is
-// not a multiple of 128 (rows then start inside a 128-byte line, and a copy touches two lines for
-// one), in 1/100 us: fitted to 200 products of M 8 to 9000, N 256 to 12,800, K 256 to 8960,
-// weights cold (each kernel within 8 to 13% rms). The smallest estimate picks within 0.4% of the
-// fastest on the geometric mean and within 19% at most. A TILE256 launch's short last round is
-// RING256's (60 further products of 300 to 9000 rows: within 2% of the fastest, all of them).
+// The kernels, from few rows to many. A launch takes `start`, for each 128 bytes of K `deep`, and for each
+// round of workgroups over the CUs `round` and for each 128 bytes of K `block`, or `odd` where K is not a
+// multiple of 128 (rows then start inside a 128-byte line, and a copy touches two lines for one), in ns. Of
+// the first three kernels several workgroups fit a CU: their rounds are a quotient, those of the others
+// whole numbers. A TILE256 launch's short last round is in RING128's or RING256's parts. Fitted to 400
+// products of M 1 to 3000 and 200 of 8 to 9000, N 256 to 28,800, K 256 to 8960, weights cold (each kernel
+// within 8 to 13% rms). The smallest estimate picks within 1.2% of the fastest on the geometric mean and
+// within 28% at most (126x448x2304, 4.9 us).
 enum Kernel { SKINNY16, SKINNY32, SKINNY64, RING128, RING256, TILE256, KERNELS };
 struct Cost {
   int tm, tn;
-  int64_t start, round, block, odd;
+  int64_t start, deep, round, block, odd;
 };
 constexpr Cost kCost[KERNELS] = {
-    {16, 16, 180, 160, 5, 6},    {32, 32, 150, 210, 10, 13}, {64, 64, 90, 340, 21, 26},
-    {128, 128, 30, 550, 38, 51}, {256, 128, 0, 890, 65, 83}, {256, 256, 0, 1000, 112, 0},
+    {16, 16, 2700, 20, 460, 67, 68},  {32, 32, 2900, 46, 780, 129, 157}, {64, 64, 3600, 130, 1210, 263, 340},
+    {128, 128, 300, 0, 5500, 380, 510}, {256, 128, 0, 0, 8900, 650, 830}, {256, 256, 0, 0, 10000, 1120, 0},
 };
 
 int64_t blocks(int64_t n, int64_t side) { return (n + side - 1) / side; }
@@ -963,7 +978,8 @@ Kernel choose(const Int8Args& a, int expected_m, int cus) {
     const Cost& c = kCost[k];
     const int64_t tiles = blocks(a.rows, c.tm) * blocks(a.N, c.tn);
     const int64_t kb = blocks(a.K, 128), last = k == TILE256 ? tiles - full_rounds(tiles, cus) : 0;
-    int64_t t = c.start + blocks(tiles - last, cus) * (c.round + (a.K % 128 ? c.odd : c.block) * kb);
+    const int64_t round = c.round + (a.K % 128 ? c.odd : c.block) * kb;
+    int64_t t = c.start + c.deep * kb + (k <= SKINNY64 ? tiles * round / cus : blocks(tiles - last, cus) * round);
     const Cost& r = kCost[4 * last <= cus ? RING128 : RING256];
     if (last) t += r.start + r.round + r.block * kb;
     if (t < least) {
@@ -977,9 +993,9 @@ Kernel choose(const Int8Args& a, int expected_m, int cus) {
 typedef void (*SkinnyFn)(Int8Args);
 typedef void (*TilesFn)(Int8Args, int);
 SkinnyFn skinny_pick(Kernel k, bool tail) {
-  if (k == SKINNY16) return tail ? int8_skinny_kernel<1, 1, 8, true> : int8_skinny_kernel<1, 1, 8, false>;
-  if (k == SKINNY32) return tail ? int8_skinny_kernel<2, 2, 5, true> : int8_skinny_kernel<2, 2, 5, false>;
-  return tail ? int8_skinny_kernel<4, 4, 2, true> : int8_skinny_kernel<4, 4, 2, false>;
+  if (k == SKINNY16) return tail ? int8_skinny_kernel<1, 1, 3, true> : int8_skinny_kernel<1, 1, 3, false>;
+  if (k == SKINNY32) return tail ? int8_skinny_kernel<2, 2, 2, true> : int8_skinny_kernel<2, 2, 2, false>;
+  return tail ? int8_skinny_kernel<4, 4, 1, true> : int8_skinny_kernel<4, 4, 1, false>;
 }
 TilesFn ring_pick(Kernel k, bool tail) {
   if (k == RING128) return tail ? int8_ring_kernel<2, 2, 4, true> : int8_ring_kernel<2, 2, 4, false>;

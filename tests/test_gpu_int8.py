@@ -404,3 +404,12 @@ def test_captured_and_replayed_on_two_streams():
             assert np.array_equal(to_host(q), q0)
             want = ref.product(q0, s0, to_host(qw), to_host(sw))
             assert np.array_equal(to_host(d.view(torch.int16)).view(np.uint16), want)
+
+
+@pytest.mark.parametrize("M,N,K", [(1013, 752, 256), (334, 2896, 896), (371, 2128, 2352), (612, 592, 4352), (145, 560, 3104),
+                                   (45, 5712, 2704), (64, 16400, 144), (700, 4096, 400), (894, 6608, 768),
+                                   (149, 19728, 640), (1500, 8208, 208)])
+def test_dense_kernels_between(M, N, K):
+    """Sizes where the choice among the kernels is close."""
+    got, want = run_dense(np.random.default_rng(M + N), M, N, K)
+    assert np.array_equal(got, want)
