@@ -29,7 +29,6 @@ struct ScoredArgs {
   const float* bias;
   int score, groups, open, best, size;                 // size: experts of a group
   uint32_t per_size;                                   // e / size = e per_size >> 20
-  int vec_bias;
   int part_bits, part_bits64;                          // 1 << these lanes a group, of a row's and of a wave's
   float scale;
 };
@@ -269,6 +268,8 @@ route_scored_rows_kernel(ScoredArgs a) {
   __shared__ uint32_t took[2][MAX_E];
   __shared__ short chosen[ROWS][MAX_K];
   __shared__ float psum[WAVES][LPR * VPT];
+  // (the bias is read again for each row: in registers it would not leave room for the rest)
+  __shared__ __attribute__((aligned(16))) float bias_of[LPR * VPT];
   __shared__ int count[MAX_E], off[MAX_E + 1];
   __shared__ int wave_sum[WAVES];
   __shared__ int n_routed, n_again;
@@ -279,6 +280,7 @@ route_scored_rows_kernel(ScoredArgs a) {
   __shared__ __attribute__((aligned(16))) uint32_t group_key[AT_ONCE][MAX_GROUPS];
   const int E = a.r.E, k = a.r.k;
   for (int e = threadIdx.x; e < E; e += NT) took[0][e] = took[1][e] = 0u;
+  for (int e = threadIdx.x; e < LPR * VPT; e += NT) bias_of[e] = a.bias && e < E ? a.bias[e] : 0.0f;
   if (threadIdx.x == 0) n_routed = n_again = 0;
   // (past the last group: none)
   for (int i = threadIdx.x; i < AT_ONCE * (int)MAX_GROUPS; i += NT) (&group_key[0][0])[i] = 0u;
@@ -302,30 +304,15 @@ route_scored_rows_kernel(ScoredArgs a) {
     chosen[r][l] = (short)id;
     if (id >= 0) atomicOr(&took[r >> 5][id], 1u << (r & 31));
   };
-  float acc[VPT], b[VPT];
+  float acc[VPT];
 #pragma unroll
-  for (int v = 0; v < VPT; ++v) acc[v] = b[v] = 0.0f;
-  if (a.bias) {
-    constexpr int W = VPT % 4 == 0 ? 4 : VPT;          // (a lane's values lie in as many side by side)
-#pragma unroll
-    for (int v = 0; v < VPT; v += W) {
-      const int e0 = L::at(v, l);
-      if (a.vec_bias && e0 + W <= E) {
-        const Pack<float, W> p = *reinterpret_cast<const Pack<float, W>*>(a.bias + e0);
-#pragma unroll
-        for (int w = 0; w < W; ++w) b[v + w] = p.v[w];
-      } else {
-#pragma unroll
-        for (int w = 0; w < W; ++w) b[v + w] = e0 + w < E ? a.bias[e0 + w] : 0.0f;
-      }
-    }
-  }
+  for (int v = 0; v < VPT; ++v) acc[v] = 0.0f;
   // the range of values, but for what the row adds to it (-inf and NaN close an expert)
   float range = 0.0f;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    const float y = __builtin_fabsf(b[v]);
-    range = __builtin_fmaxf(range, b[v] > -__builtin_inff() ? y : 0.0f);
+    const float y = bias_of[L::at(v, l)];
+    range = __builtin_fmaxf(range, y > -__builtin_inff() ? __builtin_fabsf(y) : 0.0f);
   }
   range = max_lanes<LPR>(range);
   float x[VPT];
@@ -350,7 +337,8 @@ route_scored_rows_kernel(ScoredArgs a) {
       sum = row_scores<LPR, VPT>(x, a.score, s);
       if (by_value) {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) val[v] = x[v] > -__builtin_inff() ? s[v] + b[v] : -__builtin_inff();
+        for (int v = 0; v < VPT; ++v)
+          val[v] = x[v] > -__builtin_inff() ? s[v] + bias_of[L::at(v, l)] : -__builtin_inff();
         m = range + (a.score == SCORE_SOFTMAX ? sum.norm : 1.0f);
       } else {
         m = 0.0f;
@@ -744,7 +732,6 @@ hipError_t launch_route_scored(const ScoredCall& c, hipStream_t stream, int cu_c
   a.best = c.best;
   a.size = c.route.E / c.groups;
   a.per_size = (1u << 20) / (uint32_t)a.size + 1u;     // (exact for e below 1024: e size < 2^20)
-  a.vec_bias = (uintptr_t)c.bias % 16 == 0;
   a.scale = c.scale;
   const int64_t nblk = (c.route.T + ROWS - 1) / ROWS;
   if (nblk == 0) return launch_route_places(c.route, stream);
