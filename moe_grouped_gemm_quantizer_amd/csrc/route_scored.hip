@@ -14,6 +14,11 @@
 // neighbours among the chosen and the next, or the last open and the first closed group, are
 // nearer than their errors and not alike (the same logit and bias), the row is put on a list and
 // done again in 64 bits by a wave of its own: about 0.1% of the rows of random fp32 logits.
+//
+// T 32768, E 256, 8 groups, fp32: 31 us for the rows (the data 7.4 at the rate of a large copy), bound by the
+// vector unit (1400 instructions for four rows, 18 us) and at the end by the rows done again, which take 6 us
+// whether few or many: every block is on a CU from the start, and some have such a row. Then 12 for scan and
+// slots.
 
 #include <vector>
 
@@ -675,11 +680,12 @@ route_scored_backward_kernel(ScoredBwdArgs a) {
 }
 
 // The kernels for a type, an E and a number of tokens: as in route.hip, 16 lanes a row up to 256 experts,
-// 64 above and for up to four tokens (T 4, E 256 7.8 us; five with 16 lanes 11.8). With 12 values a
-// lane and more the workgroups are of 512 threads, twice on a CU, which overlaps one's end with the other's
-// start (T 32768, E 256 47.5 us, of 1024 52.2; T 32 12.4 / 14.2), but where the blocks are no more than
-// the CUs and have two rows for each group of lanes (T 64 18.4 / 14.7, T 4096 30.5 / 26.3, T 16384
-// 37.4 / 31.9). Above 512 experts 1024 threads would spill (T 8192, E 1024 82 / 91).
+// 64 above and for up to four tokens (T 4, E 256 7.8 us; five with 16 lanes 11.2). With 12 values a
+// lane and more the workgroups are of 512 threads, two on a CU, which overlaps one's end with the other's
+// start (T 32768, E 256 42.5 us, with 1024 51.9; T 20000 37.7 / 41.4; T 32 11.8 / 14.2), but where the
+// blocks are no more than the CUs and have two rows for each group of lanes (T 33 16.4 / 14.3, T 4096
+// 29.6 / 26.7, T 16384 34.9 / 32.6). Up to 512 experts 64 lanes of 8 values are too few rows at once with 512
+// threads (T 65536, E 512 160 us, with 512 193), above them 1024 threads would spill (T 8192, E 1024 82 / 91).
 typedef void (*RowsFn)(ScoredArgs);
 typedef void (*BwdFn)(ScoredBwdArgs);
 struct Pick {
