@@ -131,21 +131,26 @@ __device__ __forceinline__ double max_wave(double x) {
 }
 
 // One row by a wave in 64 bits: lane l holds experts l, l + 64, ... Lane j gets the j-th choice
-// (-1: none) and its score. few: the k + 1 experts among which the choice surely is, or all are looked
+// (-1: none), its logit and its score. few: the k + 1 experts among which the choice surely is, or all are looked
 // at (null). high, low: LDS of the wave's own, a word each for every expert; 1 << part_bits
 // lanes a group.
 template <typename T, int PER>
 __device__ __forceinline__ int choose64(const T* __restrict__ row, const ScoredArgs& a, int l, const short* few,
-                                        uint32_t* high, uint32_t* low, int part_bits, double& score) {
+                                        uint32_t* high, uint32_t* low, int part_bits, float& xj, double& score) {
   const int E = a.r.E, k = a.r.k;
   const double none = -__builtin_inf();
   double v[PER], top = none, z = 1.0;
+  if (!few || a.score == SCORE_SOFTMAX) {
 #pragma unroll
-  for (int q = 0; q < PER; ++q) {
-    const int e = l + 64 * q;
-    v[q] = e < E ? (double)to_f32(row[e]) : none;
-    top = fmax(top, v[q]);
+    for (int q = 0; q < PER; ++q) {
+      const int e = l + 64 * q;
+      v[q] = e < E ? (double)to_f32(row[e]) : none;
+      top = fmax(top, v[q]);
+    }
   }
+  // (loaded beside the row's: what follows is one chain)
+  const int fe = few && l <= k ? few[l] : -1;
+  const float fx = fe >= 0 ? to_f32(row[fe]) : 0.0f, fb = fe >= 0 && a.bias ? a.bias[fe] : 0.0f;
   if (a.score == SCORE_SOFTMAX) {
     top = max_wave(top);
     top = top > none ? top : 0.0;
@@ -159,26 +164,31 @@ __device__ __forceinline__ int choose64(const T* __restrict__ row, const ScoredA
   };
   const bool by_value = a.bias || a.open < a.groups;
   if (few) {
-    const int e = l <= k ? few[l] : -1;
-    const float x = e >= 0 ? to_f32(row[e]) : 0.0f;
-    const double y = e < 0 ? none : (a.bias ? score64((double)x) + (double)a.bias[e] : (double)x);
+    const double s64 = score64((double)fx);
+    const double y = fe < 0 ? none : (a.bias ? s64 + (double)fb : (double)fx);
     const uint64_t words = __builtin_bit_cast(uint64_t, y);
     int rank = 0;
     for (int i = 0; i <= k; ++i) {
       const double o = __builtin_bit_cast(
           double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)words, i) |
                       (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(words >> 32), i) << 32);
-      const int oe = __builtin_amdgcn_readlane(e, i);
-      rank += o > y || (o == y && oe < e) ? 1 : 0;
+      const int oe = __builtin_amdgcn_readlane(fe, i);
+      rank += o > y || (o == y && oe < fe) ? 1 : 0;
     }
+    // (each candidate's place is its rank)
     if (l < k) low[l] = 0xFFFFFFFFu;
     wave_sync();
-    if (e >= 0 && rank < k) low[rank] = (uint32_t)e;
+    if (fe >= 0 && rank < k) low[rank] = (uint32_t)l;
     wave_sync();
-    const int id = l < k ? (int)low[l] : -1;
+    const int from = l < k ? (int)low[l] : -1;
     wave_sync();
-    score = id >= 0 ? score64((double)to_f32(row[id])) : 0.0;
-    return id;
+    // (by all lanes: a lane that takes nothing may give)
+    const int id = __shfl(fe, from & 63);
+    const float xs = __shfl(fx, from & 63);
+    const double ss = __shfl(s64, from & 63);
+    xj = from >= 0 ? xs : 0.0f;
+    score = from >= 0 ? ss : 0.0;
+    return from >= 0 ? id : -1;
   }
   if (by_value) {
 #pragma unroll
@@ -254,7 +264,8 @@ __device__ __forceinline__ int choose64(const T* __restrict__ row, const ScoredA
 #pragma unroll
     for (int q = 0; q < PER; ++q) v[q] = (uint32_t)(l + 64 * q) == e ? none : v[q];
   }
-  score = id >= 0 ? score64((double)to_f32(row[id])) : 0.0;
+  xj = id >= 0 ? to_f32(row[id]) : 0.0f;
+  score = id >= 0 ? score64((double)xj) : 0.0;
   return id;
 }
 
@@ -278,7 +289,9 @@ route_scored_rows_kernel(ScoredArgs a) {
   __shared__ int count[MAX_E], off[MAX_E + 1];
   __shared__ int wave_sum[WAVES];
   __shared__ int n_routed, n_again;
-  __shared__ short again[ROWS];                        // rows that are done again in 64 bits (~: among all experts)
+  // rows that are done again in 64 bits: among all experts, with a NaN
+  constexpr int UNSURE = 64, BAD = 128;
+  __shared__ short again[ROWS];
   __shared__ short few[ROWS][MAX_K + 1];               // or among these
   __shared__ __attribute__((aligned(8))) float values[AT_ONCE][LPR * VPT];     // where groups are chosen
   __shared__ float group_value[AT_ONCE][MAX_GROUPS];
@@ -502,7 +515,8 @@ route_scored_rows_kernel(ScoredArgs a) {
     const float bj = id >= 0 && a.bias ? a.bias[id] : 0.0f;
     // neighbours among the chosen that are near and not alike; the k-th and the next may be
     // alike and a third near them
-    const uint32_t kn = l == k - 1 ? extra : (uint32_t)__shfl_down((int)mine, 1, LPR);
+    const uint32_t after = (uint32_t)__shfl_down((int)mine, 1, LPR);       // (by all lanes: each gives)
+    const uint32_t kn = l == k - 1 ? extra : after;
     const float xn = __shfl_down(xj, 1, LPR), bn = __shfl_down(bj, 1, LPR);
     const bool close = l < k && kn && (mine >> BITS) - (kn >> BITS) <= NEAR && (l == k - 1 || xj != xn || bj != bn);
     const bool near = reduce_u32<LPR>(close ? 1u : 0u, umax) != 0u && !redo;
@@ -522,28 +536,25 @@ route_scored_rows_kernel(ScoredArgs a) {
       take(t, r, id, w);
       if (l == 0 && id >= 0) atomicAdd(&n_routed, 1);
     }
-    if (in && l == 0 && (redo || near)) again[atomicAdd(&n_again, 1)] = (short)(sure ? r : ~r);
+    if (in && l == 0 && (redo || near)) 
+      again[atomicAdd(&n_again, 1)] = (short)(r | (sure ? 0 : UNSURE) | (bad ? BAD : 0));
   }
   __syncthreads();
   // rows whose values are too near: a wave each
   constexpr int PER = (LPR * VPT + 63) / 64;
   const int wave = threadIdx.x >> 6;
   for (int i = wave; i < n_again; i += WAVES) {
-    const bool sure = again[i] >= 0;
-    const int r = sure ? again[i] : ~again[i];
+    const int r = again[i] & 63;
+    const bool sure = (again[i] & UNSURE) == 0, bad = (again[i] & BAD) != 0;
     const int64_t t = t0 + r;
     const T* const row = (const T*)a.r.logits + t * a.r.ld;
     double score;
+    float xj;
     const int id = choose64<T, PER>(row, a, lane, sure ? few[r] : nullptr, reinterpret_cast<uint32_t*>(&values[wave * (64 / LPR)][0]),
-                                    reinterpret_cast<uint32_t*>(&psum[wave][0]), a.part_bits64, score);
-    bool bad = false;
-    for (int e = lane; e < E; e += 64) {
-      const float x = to_f32(row[e]);
-      bad = bad || x != x || (a.score == SCORE_SOFTMAX && x == __builtin_inff());
-    }
+                                    reinterpret_cast<uint32_t*>(&psum[wave][0]), a.part_bits64, xj, score);
     float w = (float)score;
-    if (a.r.renorm) w = chosen_share<64>(w, id >= 0 ? to_f32(row[id]) : 0.0f, id >= 0);
-    w = __ballot(bad) ? __builtin_nanf("") : w * a.scale;
+    if (a.r.renorm) w = chosen_share<64>(w, xj, id >= 0);
+    w = bad ? __builtin_nanf("") : w * a.scale;
     if (lane < k) {
       a.r.ids[t * k + lane] = id;
       a.r.weights[t * k + lane] = w;

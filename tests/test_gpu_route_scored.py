@@ -358,3 +358,76 @@ def test_more_tokens_than_a_launch_holds():
     top = torch.sigmoid(torch.where(second, x[:, 1], x[:, 0]).float())
     # (two exponentials of a few ulp and the quotients)
     assert bool(((out["weights"][:, 0] - top).abs() <= 16 * 2.0 ** -24 * top).all())
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups,k", [(16, 1, 1), (16, 1, 4), (64, 1, 6), (160, 1, 8), (256, 8, 8), (600, 1, 16)])
+def test_one_near_pair_a_row(E, groups, k, score):
+    """In each row two neighbours of the order, the k-th and the next in half of them, whose values differ
+    by less than fp32's rounding of them, nothing else near: put in order as in 64 bits."""
+    rng = np.random.default_rng(E + k)
+    T = 400
+    bias = some_bias(rng, E)
+    x = (rng.standard_normal((T, E)) * 1.5 - 1).astype(np.float32)
+    crossed = 0
+    for t in range(T):
+        j = k - 1 if t % 2 else int(rng.integers(0, k))
+        for _ in range(12):                                # (softmax: what is moved moves the sum)
+            row = x[t:t + 1].astype(np.float64)
+            v = ref.scores(row, score)[0] + bias
+            order = np.lexsort((np.arange(E), -v))
+            p, q = order[j], order[j + 1]
+            want = v[p] - bias[q]
+            if not 1e-12 < want < 1:
+                break
+            if score == "sigmoid":
+                x[t, q] = np.float32(np.log(want / (1 - want)))
+                break
+            z = np.exp(row[0]).sum() - np.exp(row[0, q])
+            x[t, q] = np.float32(np.log(want * z / (1 - want)))
+        v = np.sort(ref.scores(x[t:t + 1].astype(np.float64), score)[0] + bias)[::-1]
+        crossed += v[j] - v[j + 1] < 2.0 ** -22
+    assert crossed > T / 10                                # (softmax of few experts: one that is moved moves the others)
+    for renorm in (False, True):
+        check(torch.from_numpy(x).to(dev()), k, bias, score, groups, groups, 1, renorm=renorm)
+
+
+@pytest.mark.parametrize("E,groups,opened,best", [(16, 4, 2, 1), (60, 3, 1, 2), (64, 8, 4, 2), (160, 8, 3, 2), (256, 8, 4, 2),
+                                                  (256, 32, 5, 1), (600, 6, 3, 2), (1024, 16, 7, 2)])
+def test_one_near_pair_of_groups_a_row(E, groups, opened, best):
+    """In each row the last open and the first closed group's values differ by less than fp32's rounding
+    of them."""
+    rng = np.random.default_rng(E + groups)
+    T, size, k = 300, E // groups, min(6, opened * (E // groups))
+    bias = some_bias(rng, E)
+    x = (rng.standard_normal((T, E)) * 1.5 - 1).astype(np.float32)
+    near = 0
+    for t in range(T):
+        v = (ref.scores(x[t:t + 1].astype(np.float64), "sigmoid")[0] + bias).reshape(groups, size)
+        value = np.sort(v, 1)[:, ::-1][:, :best].sum(1)
+        order = np.lexsort((np.arange(groups), -value))
+        a, b = order[opened - 1], order[opened]
+        e = b * size + int(v[b].argmax())
+        want = value[a] - (np.sort(v[b])[-2] if best == 2 else 0.0) - bias[e]
+        if 1e-12 < want < 1 - 1e-7:
+            x[t, e] = np.float32(np.log(want / (1 - want)))
+            near += 1
+    assert near > T / 2
+    check(torch.from_numpy(x).to(dev()), k, bias, "sigmoid", groups, opened, best, renorm=True)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,k", [(16, 4), (64, 6), (160, 8), (256, 8), (512, 8), (1000, 16)])
+def test_logits_one_step_apart(E, k, score):
+    """Without a bias: two neighbours of the order (three in every other row) one fp32 step apart or alike."""
+    rng = np.random.default_rng(E + k)
+    T = 300
+    x = (rng.standard_normal((T, E)) * 1.5 - 1).astype(np.float32)
+    for t in range(T):
+        j = int(rng.integers(0, k))
+        order = np.argsort(-x[t], kind="stable")
+        p, q, r = order[j], order[j + 1], order[j + 2] if j + 2 < E else order[j - 1]
+        x[t, q] = np.nextafter(x[t, p], np.float32(np.inf if t % 3 == 0 else -np.inf)) if t % 3 < 2 else x[t, p]
+        if t % 2:
+            x[t, r] = x[t, q]
+    check(torch.from_numpy(x).to(dev()), k, None, score, renorm=True)
