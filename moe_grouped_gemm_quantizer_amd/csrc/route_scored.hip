@@ -39,9 +39,10 @@ struct ScoredArgs {
 };
 
 // Sums of scores below this are formed again from exponentials shifted by the largest logit: both
-// scores are exp(x) times a factor of the row there (sigmoid to 2^-90), and shares of a sum do not
-// depend on it, however far below fp32's range the scores are.
-constexpr float LITTLE = 0x1p-90f;
+// scores are exp(x) times a factor of the row there (sigmoid to 2^-32), and shares of a sum do not
+// depend on it. A share of 2^-94 and above is as exact as the others, however far below fp32's range
+// the scores are.
+constexpr float LITTLE = 0x1p-32f;
 
 // A row's scores, and what of them its share of the loss is: 1 / sum s (0 for a row without any,
 // NaN where a logit is NaN, or with softmax infinite).
