@@ -537,7 +537,7 @@ enum { FP8G_SCORE_SIGMOID = 0, FP8G_SCORE_SOFTMAX = 1 };
  *                     is decided as in 64-bit arithmetic.
  *   weights[t][j]     scale * s[expert_ids[t][j]], with renormalise over the
  *                     row's sum of the chosen s (their shares of it, however
- *                     small the scores are);
+ *                     small the scores are; one below 2^-94 may be 0);
  *                     0 where the id is -1. A row with a NaN logit (with
  *                     softmax: or +inf) has NaN in all k weights; with
  *                     softmax its v are NaN too, so that it chooses nothing

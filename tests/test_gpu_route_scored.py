@@ -431,3 +431,36 @@ def test_logits_one_step_apart(E, k, score):
         if t % 2:
             x[t, r] = x[t, q]
     check(torch.from_numpy(x).to(dev()), k, None, score, renorm=True)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_gradient_against_differences(score, renorm):
+    """Central differences in 64 bits of sum(dw weights) + dl loss, experts and counts held."""
+    rng = np.random.default_rng(21)
+    T, E, k, scale, coef, dl = 9, 20, 3, 2.5, 50.0, 1.5
+    x = logits(rng, T, E)
+    o = call(x, k, torch.from_numpy(some_bias(rng, E)).to(dev()), score, 4, 2, 2, None, renorm, scale, coef)
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    got = gradient(x, o, torch.from_numpy(dw).to(dev()), torch.full((1,), dl, device=dev()), score=score,
+                   renormalise=renorm, scale=scale, loss_coef=coef).double().cpu().numpy()
+    ids, counts = o["expert_ids"].cpu().numpy().astype(np.int64), o["counts"].cpu().numpy()
+    base = x.double().cpu().numpy()
+
+    def value(x):
+        s = ref.scores(x, score)
+        w = np.take_along_axis(s, ids, 1)
+        w = scale * (w / w.sum(1, keepdims=True) if renorm else w)
+        share = (s / s.sum(1, keepdims=True)).sum(0)
+        return (dw * w).sum() + dl * coef * (E * counts / (k * T) * share / T).sum()
+    h, want = 1e-4, np.zeros((T, E))
+    for i in np.ndindex(T, E):
+        up, down = base.copy(), base.copy()
+        up[i] += h
+        down[i] -= h
+        want[i] = (value(up) - value(down)) / (2 * h)
+    _, size = ref.backward(base, ids, dw.astype(np.float64), dl, counts, T, score, renorm, scale, coef)
+    # differences: h^2 / 6 of a third derivative, which is below 8 of these sizes (each is a product of
+    # at most three scores' slopes), and 2^-52 of the value over h
+    tol = 96 * 2.0 ** -24 * size + h * h * 2 * size.max() + 2.0 ** -52 * abs(value(base)) * 4 / h
+    assert (np.abs(got - want) <= tol).all()
