@@ -12,8 +12,10 @@
 // that is cut off, by 16 bits of a hash of (seed, step, tensor, element). r is never rounded to
 // 0 unless it is 0: m / (r + eps) would then be as large as eps is small.
 //
-// An HBM stream: every tensor is read and written once. The list travels in the kernel's arguments,
-// MAX_T tensors a launch, or lies in device memory for a launch over all of them.
+// An HBM stream: every tensor is read and written once (300 tensors of 50M, fp32 states, 241 us, 5.8 TB/s; 8 x
+// 29M with 8-bit states 676, 5.5 TB/s). The list travels in the kernel's arguments, MAX_T tensors a
+// launch, or lies in device memory for a launch over all of them (300 tensors of 50M: 6 launches 274 us, one
+// 241; of 5M 54 / 27).
 
 #include <math.h>
 #include <vector>
@@ -62,6 +64,18 @@ struct Hyper {
   uint32_t seed, key;
   float size, inv, keep;                               // Factors', where the host knows step and lr
 };
+// The chunk's tensor, c the same in all lanes.
+template <typename Ends>
+__device__ __forceinline__ int find_tensor(Ends end, int n, int c) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (c < end[mid]) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
 // Tensors by value, from number `base` of the caller's list on; end: chunks of a tensor and those
 // before it.
 struct Some {
@@ -69,51 +83,41 @@ struct Some {
   int n, chunk, base;
   int end[MAX_T];
   Entry list[MAX_T];
-  // (c: this workgroup's chunk, the same in all lanes)
-  __device__ __forceinline__ int find(int c) const {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (c < end[mid]) hi = mid;
-      else lo = mid + 1;
-    }
-    return lo;
-  }
+  __device__ __forceinline__ int find(int c) const { return find_tensor(end, n, c); }
   __device__ __forceinline__ Entry at(int i) const { return list[i]; }
 };
 static_assert(sizeof(Some) <= 4096, "a kernel's arguments");
 
-// All of them in device memory, a launch's chunks from number chunk0 on. 64 ends are looked at at
-// once, and a tensor's entry is loaded by a lane each dword.
+// All of them in device memory, a launch's chunks from number chunk0 on. The table is read through the
+// scalar cache, which the tensors' stream does not pass (by vector loads, 64 ends at once, 300 tensors of
+// 50M with 8-bit states took 190 us).
+#define FP8G_CONSTANT __attribute__((address_space(4)))
 struct All {
   Hyper h;
   int n, chunk, base, chunk0;
   const int* end;
   const Entry* list;
   __device__ __forceinline__ int find(int c) const {
-    const int lane = threadIdx.x & 63;
-    int lo = 0, len = n;
-    while (len > 64) {
-      const int stride = (len + 63) >> 6;
-      const int last = min((lane + 1) * stride, len) - 1;
-      const int before = __popcll(__ballot(c >= end[lo + last]));     // (past the list: its last, after c)
-      lo += before * stride;
-      len = min(stride, len - before * stride);
-    }
-    return lo + __popcll(__ballot(lane < len && c >= end[lo + min(lane, len - 1)]));
+    return find_tensor((const FP8G_CONSTANT int*)(uintptr_t)end, n, c);
   }
   __device__ __forceinline__ Entry at(int i) const {
-    constexpr int W = sizeof(Entry) / 4;
-    const int lane = threadIdx.x & 63;
-    const uint32_t mine = reinterpret_cast<const uint32_t*>(list + i)[min(lane, W - 1)];
-    uint32_t w[W];
-#pragma unroll
-    for (int k = 0; k < W; ++k) w[k] = (uint32_t)__builtin_amdgcn_readlane((int)mine, k);
-    Entry e;
-    __builtin_memcpy(&e, w, sizeof(e));
-    return e;
+    const FP8G_CONSTANT Entry* const e = (const FP8G_CONSTANT Entry*)(uintptr_t)(list + i);
+    Entry o;
+    o.p = e->p;
+    o.g = e->g;
+    o.m = e->m;
+    o.v = e->v;
+    o.copy = e->copy;
+    o.ms = e->ms;
+    o.vs = e->vs;
+    o.numel = e->numel;
+    o.first = e->first;
+    o.types = e->types;
+    o.ctype = e->ctype;
+    return o;
   }
 };
+#undef FP8G_CONSTANT
 template <typename A>
 constexpr bool is_all = __is_same(A, All);
 int64_t ends_bytes(int n) { return (n + 1) / 2 * 8; }
@@ -496,10 +500,10 @@ adamw_kernel(Args a) {
 }
 
 // A list's chunk. Small ones where HBM is the bound: they reach all CUs and end evenly (2048 /
-// 8192 elements: 300 tensors of 50M, fp32 parameters, fp32 states 266 / 295 us, 8-bit states 189 /
-// 207; 8 x 29M 8-bit 690 / 734; 3M elements 15.2 / 18.9). Large lists of 16-bit parameters with
+// 8192 elements: 300 tensors of 50M, fp32 parameters, fp32 states 246 / 277 us, 8-bit states 168 /
+// 173; 8 x 29M 8-bit 676 / 743; 3M elements 18.6 / 21.1). Large lists of 16-bit parameters with
 // 8-bit states are bound by the vector unit, which what a workgroup does once (the clipping
-// factor in fp64, the search) keeps busy too (2 x 50M bf16 239 / 214).
+// factor in fp64, the search) keeps busy too (2 x 50M bf16 241 / 219, 300 of 50M 127 / 116).
 int chunk_for(const AdamwCall& c) {
   if (!c.ms) return CHUNK_MIN;
   int64_t total = 0, narrow = 0;
