@@ -567,7 +567,10 @@ route_scored_rows_kernel(ScoredArgs a) {
   finish_block<T, LPR, VPT, NT>(a.r, block, acc, took, chosen, psum, count, off, wave_sum, n_routed);
 }
 
-constexpr int BWD_PER_CU = 4;                          // workgroups per CU of the backward pass
+// Workgroups per CU of the backward pass: two where a lane holds much of a row and its factors, which each
+// workgroup forms once (2 / 4 / 8: T 32768 E 256 bf16 18.1 / 20.4 / 25.9 us, fp32 18.9 / 19.9 / 21.7,
+// T 8192 E 1024 18.5 / 20.3 / 22.0), four where rows are short (T 65536 E 64 14.3 / 12.1 / 11.7).
+int bwd_per_cu(int E) { return E > 128 ? 2 : 4; }
 
 struct ScoredBwdArgs {
   const void* logits;
@@ -584,7 +587,8 @@ struct ScoredBwdArgs {
 // dw, and for the chosen
 //   softmax: c = u (d - sum d u) with renormalise, else s d;   dx = q (f - sum f q - [else] sum s d) + c
 //   sigmoid: c = u (1 - s) (d - sum d u), else s (1 - s) d;   dx = q (1 - s) (f - sum f q) + c
-// which divides by no sum that could be little, and forms 1 - s without cancellation.
+// which divides by no sum that could be little, and forms 1 - s without cancellation. Vector unit and loads take
+// about as long (T 20011 E 160 fp32 10.1 us, 2.5 TB/s; T 32768 E 256 18.9, 3.6 TB/s).
 template <typename T, int LPR, int VPT>
 __global__ void __launch_bounds__(THREADS)
 route_scored_backward_kernel(ScoredBwdArgs a) {
@@ -790,7 +794,8 @@ hipError_t launch_route_scored_backward(const ScoredBwdCall& c, hipStream_t stre
   a.scale = c.scale;
   const Pick p = pick(r.type, r.E, r.T, cu_count);
   int64_t grid = (r.T + p.rows_at_once - 1) / p.rows_at_once;
-  if (grid > (int64_t)cu_count * BWD_PER_CU) grid = (int64_t)cu_count * BWD_PER_CU;
+  const int64_t most = (int64_t)cu_count * bwd_per_cu(r.E);
+  if (grid > most) grid = most;
   p.bwd<<<dim3((unsigned)grid), dim3(THREADS), 0, stream>>>(a);
   return hipGetLastError();
 }
