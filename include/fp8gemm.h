@@ -717,8 +717,10 @@ fp8g_status grad_clip(const void* const* grads, void* const* outs, const int64_t
  *    otherwise 8 bits: exp_avgs holds m and exp_avg_sqs holds sqrt(v) as e4m3
  *    codes (uint8 [numel]), and the scale arrays one exponent byte (e8m0, 2^(b
  *    - 127)) for each 128 elements (uint8 [ceil(numel / 128)]): the smallest
- *    power of two that brings the block's largest value to 448 or below. Codes
- *    of zeros are a fresh state, whatever the scales. A value is rounded up
+ *    power of two that brings the block's largest value to 448 or below. A
+ *    step writes bytes 1 .. 247; byte 0 is read as the scale 0, byte 255 as
+ *    NaN for every code but 0. Codes of zeros (of either sign) are a fresh
+ *    state, whatever the scales, which may be unset. A value is rounded up
  *    with the probability of the part that is cut off: 16 bits of a hash of
  *    (seed, t, the tensor's number in the list, element) decide, so that the
  *    same call gives the same bits. sqrt(v) becomes code 0 only where it is 0.

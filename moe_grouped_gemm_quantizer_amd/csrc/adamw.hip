@@ -379,11 +379,23 @@ __device__ __forceinline__ void chunk8(const Entry& t, int index, int64_t at, in
                               : __builtin_amdgcn_cvt_pk_f32_fp8((int)cv[k / 4], false);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float r = dv[h] * fv;
         xm[k + h] = dm[h] * fm;
-        xr[k + h] = r * r;
-        move(xg[k + h], xm[k + h], xr[k + h], f);
+        xr[k + h] = dv[h] * fv;
       }
+    }
+    // (byte 255, which no step writes, is e8m0's NaN; a code of 0 is 0 under it as under every scale)
+    if (max(sm, sv) == 255u) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const uint32_t bm = cm[k / 4] >> (8 * (k % 4)) & 0x7Fu, bv = cv[k / 4] >> (8 * (k % 4)) & 0x7Fu;
+        if (sm == 255u) xm[k] = bm ? __builtin_nanf("") : 0.0f;
+        if (sv == 255u) xr[k] = bv ? __builtin_nanf("") : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      xr[k] = xr[k] * xr[k];
+      move(xg[k], xm[k], xr[k], f);
     }
     float lo = xr[0], hi = xr[0];
 #pragma unroll
