@@ -160,6 +160,23 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _torchs_stream(stream, handle):
+    """The Stream object that `stream` (as _stream takes it) means, or None where
+    it is not one of torch's own: a handle made elsewhere may be destroyed while
+    torch's allocator still wants to record an event on it."""
+    torch = _torch()
+    if stream is None or isinstance(stream, int):
+        # (not ExternalStream(handle): that of 0 is no default stream but another, new one)
+        s = torch.cuda.current_stream()
+        if s.cuda_stream != handle:
+            s = torch.cuda.default_stream()
+    else:
+        s = stream
+    if s.cuda_stream != handle or (handle != 0 and s.stream_id == handle):
+        return None                          # (a foreign stream's id is its handle)
+    return s
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -812,7 +829,9 @@ def adamw_step(tensors, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay
     sumsq (float64 device tensor of one element, grad_norm_sq's): the gradients are
     clipped to max_norm within the step, norm (float32, one element, or None) is
     written, and a sum that is infinite or NaN leaves the step out. seed: of the
-    8-bit states' rounding."""
+    8-bit states' rounding. stream: a torch stream or a handle; on one that torch did
+    not make (or whose handle alone is given, unless it is the current or default
+    stream's) a long list goes by value, so that nothing has to outlive the call."""
     if tensors.n and tensors.device != _torch()._C._cuda_getDevice():
         _fail("the tensors are not on the current device")
     torch = _torch()
@@ -828,10 +847,16 @@ def adamw_step(tensors, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay
     _one_device(step_at, lr_at, sumsq, norm)
     on, table = _stream(stream), tensors.table
     if table is not None:
-        if on not in tensors.streams:        # (its memory is not used again before the steps there are done)
-            table.record_stream(torch.cuda.ExternalStream(on))
-            tensors.streams.add(on)
-        table = table.data_ptr()
+        if on in tensors.streams:
+            table = table.data_ptr()
+        else:
+            own = _torchs_stream(stream, on)
+            if own is None:                  # (nothing is kept until a foreign stream is done: the list by value)
+                table = None
+            else:                            # (its memory is not used again before the steps there are done)
+                table.record_stream(own)
+                tensors.streams.add(on)
+                table = table.data_ptr()
     st = load().adamw_step(*map(_at, tensors.lists), tensors.n, sp, step, lp, lr, beta1, beta2, eps, weight_decay,
                            total, max_norm, nrm, seed & 0xFFFFFFFF, table, on)
     if st:

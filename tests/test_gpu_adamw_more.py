@@ -69,3 +69,80 @@ def test_scale_byte_255_of_other_codes_is_nan():
     assert (m[odd] & 127 == 127).all() and (r[odd] == 127).all()
     dec = ref.decode(m, got[4].cpu().numpy())
     assert np.isfinite(dec[~odd]).all()
+
+
+def long_list(seed=0, n=60):
+    """More tensors than one launch takes by value: parameters and the list."""
+    gen = torch.Generator(device=dev()).manual_seed(seed)
+    ps, gs = [[torch.randn(300 + i, device=dev(), generator=gen) for i in range(n)] for _ in range(2)]
+    ms, vs = [[torch.zeros_like(p) for p in ps] for _ in range(2)]
+    return ps, fp8g.adamw_tensors(ps, gs, ms, vs)
+
+
+class Spy:
+    """A list's table that writes down the streams it is recorded on."""
+
+    def __init__(self, lst):
+        self.table, self.on = lst.table, []
+        lst.table = self
+
+    def record_stream(self, stream):
+        self.on.append(stream.cuda_stream)
+        self.table.record_stream(stream)
+
+    def data_ptr(self):
+        return self.table.data_ptr()
+
+
+def test_the_table_is_recorded_on_the_stream_of_the_step():
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    assert side.cuda_stream != 0 and other.cuda_stream != side.cuda_stream
+    default = torch.cuda.default_stream().cuda_stream
+    wants = []
+    for made_on, kw, want in [(side, {}, [default]), (side, dict(stream=0), [default]),
+                              (side, dict(stream=torch.cuda.default_stream()), [default]),
+                              (side, dict(stream=other), [other.cuda_stream]), (side, dict(stream=side), []),
+                              (side, dict(stream=side.cuda_stream), []), (None, {}, []), (None, dict(stream=0), []),
+                              (None, dict(stream=side), [side.cuda_stream]),
+                              # (handles that may be anyone's: the list goes by value)
+                              (None, dict(stream=side.cuda_stream), []),
+                              (None, dict(stream=torch.cuda.ExternalStream(side.cuda_stream)), [])]:
+        want_p, ref_list = long_list()
+        fp8g.adamw_step(ref_list, 1, 1e-2)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(made_on):
+            ps, lst = long_list()
+        torch.cuda.synchronize()
+        spy = Spy(lst)
+        for step in (1, 2):                            # (once for each stream)
+            fp8g.adamw_step(lst, step, 1e-2, **kw)
+            if step == 1:
+                torch.cuda.synchronize()
+                wants.append(all(torch.equal(a, b) for a, b in zip(want_p, ps)))
+        assert spy.on == want, kw
+        torch.cuda.synchronize()
+    assert all(wants)
+
+
+def test_a_dropped_list_keeps_its_table_until_the_default_stream_is_done():
+    """Made on a side stream, stepped on the default one: no allocation of the side stream gets the table's
+    place while the step waits."""
+    side = torch.cuda.Stream()
+    want, ref_list = long_list()
+    fp8g.adamw_step(ref_list, 1, 1e-2)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        ps, lst = long_list()
+    torch.cuda.synchronize()
+    x = torch.randn(4096, 4096, device=dev())
+    for _ in range(20):
+        x = x @ x * 1e-4
+    fp8g.adamw_step(lst, 1, 1e-2)
+    at, size = lst.table.data_ptr(), lst.table.numel()
+    lst = None
+    with torch.cuda.stream(side):
+        new = [torch.empty(size, dtype=torch.uint8, device=dev()) for _ in range(8)]
+    busy = not torch.cuda.default_stream().query()
+    assert not busy or at not in [t.data_ptr() for t in new]
+    torch.cuda.synchronize()
+    assert busy and all(torch.equal(a, b) for a, b in zip(want, ps))
