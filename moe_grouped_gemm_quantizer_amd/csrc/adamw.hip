@@ -193,6 +193,14 @@ __device__ __forceinline__ float root(float x) {
   return __builtin_fmaf(__builtin_fmaf(-s, s, x), 0.5f * q, s);
 }
 
+// The square root within one ulp. The instruction takes a subnormal as 0, which with eps = 0 made an
+// infinite step of a finite one: those are brought up by 2^64 first. (The stream hides these
+// instructions: 300 tensors of 50M 245 us with and without them.)
+__device__ __forceinline__ float root_of_state(float v) {
+  const bool small = v < 0x1p-126f;
+  return __builtin_amdgcn_sqrtf(small ? v * 0x1p64f : v) * (small ? 0x1p-32f : 1.0f);
+}
+
 // N values of type T as fp32: in 16-byte accesses (the address is aligned to what they move),
 // or one by one, `left` of them.
 template <typename T, int N>
@@ -285,7 +293,7 @@ __device__ __forceinline__ void chunk32(const Entry& t, int64_t at, int n, const
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       move(xg[k], xm[k], xv[k], f);
-      xp[k] = moved(xp[k], xm[k], __builtin_amdgcn_sqrtf(xv[k]), f);
+      xp[k] = moved(xp[k], xm[k], root_of_state(xv[k]), f);
     }
     if (whole) {
       Raw<P, N> rp;

@@ -146,3 +146,26 @@ def test_a_dropped_list_keeps_its_table_until_the_default_stream_is_done():
     assert not busy or at not in [t.data_ptr() for t in new]
     torch.cuda.synchronize()
     assert busy and all(torch.equal(a, b) for a, b in zip(want, ps))
+
+
+@pytest.mark.parametrize("kinds", [("f32", "f32"), ("f32", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("n", [3, 1000])
+def test_subnormal_squares_without_eps(n, kinds):
+    """eps = 0 and v down to the smallest subnormal: the step is m / sqrt(v), about lr, and finite."""
+    types = {"f32": torch.float32, "bf16": torch.bfloat16}
+    rng = np.random.default_rng(n)
+    top = np.exp(np.linspace(np.log(1e-21), np.log(1e-17), n)) * rng.choice([-1, 1], n)
+    p = torch.zeros(n, dtype=types[kinds[0]], device=dev())
+    g = torch.from_numpy(top).float().to(dev()).to(types[kinds[1]])
+    m, v = [torch.zeros(n, device=dev()) for _ in range(2)]
+    b1, b2, lr = 0.9, 0.999, 1e-2
+    fp8g.adamw_step(fp8g.adamw_tensors([p], [g], [m], [v]), 1, lr, beta1=b1, beta2=b2, eps=0.0, weight_decay=0.0)
+    wm, wv, _ = ref.states(g.float().cpu().numpy(), np.zeros(n, np.float32), np.zeros(n, np.float32), None, b1, b2)
+    assert np.array_equal(m.cpu().numpy(), wm) and np.array_equal(v.cpu().numpy(), wv)
+    assert (wv > 0).all() and (wv < 2.0 ** -126).any()
+    want = -lr / (1 - b1) * wm.astype(np.float64) / (np.sqrt(wv.astype(np.float64)) / np.sqrt(1 - b2))
+    # half steps of fp32: lr's factor, the root's factor, the root 2, their product, the reciprocal 2, two
+    # products; the difference with 0 is exact; then the type's
+    tol = 8 * 2.0 ** -24 * np.abs(want)
+    tol += torch.finfo(p.dtype).eps / 2 * (np.abs(want) + tol)
+    assert (np.abs(p.double().cpu().numpy() - want) <= tol).all()
