@@ -707,6 +707,8 @@ fp8g_status grad_clip(const void* const* grads, void* const* outs, const int64_t
  * in fp32, p' rounded once to the parameter's type (bf16 and fp16 parameters
  * lose updates below half their step: keep fp32 ones and let the call write
  * the 16-bit copies).
+ * An eps between 0 and 2^-126 counts as 2^-126. With eps = 0 an element whose
+ * gradient and states are 0 becomes NaN (0 / 0).
  * If *sumsq is infinite or NaN the step is left out: only norm is written.
  *
  * All lists are HOST arrays of n entries, read before the call returns:

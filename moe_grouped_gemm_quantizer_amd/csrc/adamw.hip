@@ -567,7 +567,8 @@ Hyper hyper(const AdamwCall& c) {
   h.c1 = (float)(1.0 - c.beta1);
   h.b2 = (float)c.beta2;
   h.c2 = (float)(1.0 - c.beta2);
-  h.eps = (float)c.eps;
+  // (the reciprocal of a subnormal is infinite, and an element without gradient and states then NaN)
+  h.eps = c.eps > 0.0 && c.eps < 0x1p-126 ? 0x1p-126f : (float)c.eps;
   h.max_norm = c.max_norm;
   h.step = c.step;
   h.seed = c.seed;

@@ -169,3 +169,27 @@ def test_subnormal_squares_without_eps(n, kinds):
     tol = 8 * 2.0 ** -24 * np.abs(want)
     tol += torch.finfo(p.dtype).eps / 2 * (np.abs(want) + tol)
     assert (np.abs(p.double().cpu().numpy() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-37, 1e-38, 1e-40, 1e-45, 1e-60, 1e-300])
+def test_an_eps_below_fp32s_normal_numbers(eps, bits):
+    """Where gradient and states are 0 nothing moves, however small eps is; elsewhere it makes no difference."""
+    n = 300
+    p = torch.linspace(-1, 1, n, device=dev())
+    g = torch.zeros(n, device=dev())
+    g[::3] = 1e-3
+    start = p.clone()
+
+    def states():
+        if bits == 32:
+            return [[torch.zeros(n, device=dev())] for _ in range(2)], {}
+        return ([[torch.zeros(n, dtype=torch.uint8, device=dev())] for _ in range(2)],
+                {k: [torch.zeros(3, dtype=torch.uint8, device=dev())] for k in ("m_scales", "v_scales")})
+    st, sc = states()
+    fp8g.adamw_step(fp8g.adamw_tensors([p], [g], *st, **sc), 1, 1e-2, eps=eps, weight_decay=0.0)
+    q, (st, sc) = start.clone(), states()
+    fp8g.adamw_step(fp8g.adamw_tensors([q], [g], *st, **sc), 1, 1e-2, eps=1e-30, weight_decay=0.0)
+    torch.cuda.synchronize()
+    assert torch.equal(p, q)
+    assert torch.equal(p[1::3], start[1::3]) and bool((p[::3] < start[::3]).all())
