@@ -8,7 +8,9 @@ loaded, every call raises.
 """
 
 import array
+import bisect
 import ctypes
+import itertools
 import operator
 import os
 
@@ -744,6 +746,21 @@ def grad_clip(grads, outs, sumsq, max_norm, norm, stream=None):
                             _stream(stream)), "grad_clip")
 
 
+def _overlapping(starts, ends, read):
+    """Whether any of the memory ranges starts[i] .. ends[i] overlaps another of
+    them or one of `read`, pairs (which may overlap each other). Empty: 0, 0."""
+    # (each sorted by itself: where none overlap, the next start is never below the i-th end)
+    starts, ends = sorted(starts), sorted(ends)
+    if any(map(operator.gt, ends, starts[1:])):
+        return True
+    for lo, hi in read:
+        # (they lie apart: only the last one that starts below hi can reach into it)
+        i = bisect.bisect_left(starts, hi) - 1
+        if lo < hi and i >= 0 and ends[i] > lo:
+            return True
+    return False
+
+
 class AdamwTensors:
     """The tensors of an AdamW step (made by adamw_tensors): their pointers,
     sizes and types as HOST arrays, for a long list as a table in device memory
@@ -761,7 +778,8 @@ def adamw_tensors(params, grads, exp_avgs, exp_avg_sqs, copies=None, m_scales=No
     size. States: exp_avgs and exp_avg_sqs float32 of the same sizes, or, with
     m_scales and v_scales (uint8 [ceil(numel/128)] each), uint8 e4m3 codes of m and
     sqrt(v) (zeros: a fresh state). copies: bfloat16 or float16 tensors that
-    receive the parameters, or None; single ones may be None."""
+    receive the parameters, or None; single ones may be None. What the step
+    writes may not overlap another tensor of the list."""
     torch = _torch()
     eight = m_scales is not None or v_scales is not None
     if eight and (m_scales is None or v_scales is None):
@@ -794,15 +812,19 @@ def adamw_tensors(params, grads, exp_avgs, exp_avg_sqs, copies=None, m_scales=No
         if not (all(map(cls.is_contiguous, ts)) and set(map(cls.get_device, ts)) <= {at}):
             _fail(f"{what} must be contiguous and on the current device")
     ptr = [array.array("Q", [0 if t is None else t.data_ptr() for t in ts]) for ts in lists]
-    written = [p for ps in ptr[:1] + ptr[2:] for p in ps if p]
-    if len(set(written)) != len(written):
-        _fail("a tensor that the step writes is in the list twice")
-    if not set(written).isdisjoint(ptr[1]):
-        _fail("a gradient must not be a tensor that the step writes")
+    typ = [array.array("i", [0 if t is None else _TYPES[t.dtype] for t in lists[i]]) for i in (0, 1, 6)]
+    wide = [[4 if k == 0 else 2 for k in ks] for ks in typ[:2]]
+    one = 1 if eight else 4
+    ends = [list(map(operator.add, ps, map(operator.mul, ks, ws)))
+            for ps, ks, ws in ((ptr[0], numels, wide[0]), (ptr[1], numels, wide[1]), (ptr[2], numels, [one] * n),
+                               (ptr[3], numels, [one] * n), (ptr[4], blocks, [1 if eight else 0] * n),
+                               (ptr[5], blocks, [1 if eight else 0] * n),
+                               (ptr[6], numels, [2 if p else 0 for p in ptr[6]]))]
+    if _overlapping(itertools.chain(*ptr[:1], *ptr[2:]), itertools.chain(*ends[:1], *ends[2:]), zip(ptr[1], ends[1])):
+        _fail("a tensor that the step writes overlaps another tensor of the list")
     out = AdamwTensors()
     # (the memory, whatever becomes of the tensors)
     out.held = [[t.untyped_storage() for t in ts if t is not None] for ts in lists]
-    typ = [array.array("i", [0 if t is None else _TYPES[t.dtype] for t in lists[i]]) for i in (0, 1, 6)]
     out.lists = (ptr[0], typ[0], ptr[1], typ[1], ptr[2], ptr[3], ptr[4] if eight else (), ptr[5] if eight else (),
                  ptr[6] if copies is not None else (), typ[2], array.array("q", numels))
     out.n = n

@@ -193,3 +193,29 @@ def test_an_eps_below_fp32s_normal_numbers(eps, bits):
     torch.cuda.synchronize()
     assert torch.equal(p, q)
     assert torch.equal(p[1::3], start[1::3]) and bool((p[::3] < start[::3]).all())
+
+
+def test_overlapping_tensors_are_refused():
+    def z(n, dtype=torch.float32):
+        return torch.zeros(n, dtype=dtype, device=dev())
+    flat, codes = z(1000), z(1000, torch.uint8)
+
+    def lst(**kw):
+        base = dict(params=[z(100), z(100)], grads=[z(100), z(100)], exp_avgs=[z(100), z(100)],
+                    exp_avg_sqs=[z(100), z(100)])
+        return fp8g.adamw_tensors(**dict(base, **kw))
+    lst(params=[flat[:100], flat[100:200]], grads=[flat[200:300]] * 2, exp_avgs=[flat[300:400], flat[400:500]])
+    # (shared gradients, empty tensors anywhere)
+    lst(params=[flat[:100], flat[50:50]], grads=[z(100), flat[20:20]], exp_avgs=[z(100), z(0)], exp_avg_sqs=[z(100), z(0)])
+    eight = dict(exp_avgs=[codes[:100], codes[100:200]], exp_avg_sqs=[codes[200:300], codes[300:400]],
+                 m_scales=[codes[400:401], codes[401:402]], v_scales=[codes[402:403], codes[403:404]])
+    lst(**eight)
+    for bad in [dict(params=[flat[:100], flat[64:164]]), dict(params=[flat[:100], z(100)], exp_avgs=[flat[99:199], z(100)]),
+                dict(params=[flat[64:164], z(100)], grads=[flat[:100], z(100)]),
+                dict(params=[flat[64:164], z(100)], grads=[z(100), flat[100:200]]),
+                dict(params=[flat[:100], z(100)], copies=[None, flat.view(torch.bfloat16)[199:299]]),
+                dict(eight, v_scales=[codes[402:403], codes[399:400]]), dict(eight, m_scales=[codes[150:151], codes[401:402]]),
+                dict(eight, grads=[codes[:400].view(torch.float32), z(100)])]:
+        with pytest.raises(ValueError, match="overlaps"):
+            lst(**bad)
+    lst(params=[flat[:100], z(100)], copies=[None, flat.view(torch.bfloat16)[200:300]])
