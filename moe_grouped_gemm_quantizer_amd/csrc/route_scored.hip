@@ -270,6 +270,14 @@ __device__ __forceinline__ int choose64(const T* __restrict__ row, const ScoredA
   return id;
 }
 
+// The whole number below x; 0 for NaN and below 0, -inf among them. (The instruction itself: the language's
+// conversion leaves these open, and a bound before it costs an instruction for each value.)
+__device__ __forceinline__ uint32_t whole_units(float x) {
+  uint32_t u;
+  asm("v_cvt_u32_f32 %0, %1" : "=v"(u) : "v"(x));
+  return u;
+}
+
 // One block of 64 tokens per workgroup, LPR lanes a row, as in route.hip.
 template <typename T, int LPR, int VPT, int NT>
 __global__ void __launch_bounds__(NT, NT == 512 ? (LPR == 16 ? 4 : 2) : 1)
@@ -480,8 +488,7 @@ route_scored_rows_kernel(ScoredArgs a) {
     uint32_t key[VPT];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      const uint32_t u = (uint32_t)__builtin_fmaf(val[v], units, least_units);
-      key[v] = (u << BITS) + number - (uint32_t)L::at(v, 0);
+      key[v] = (whole_units(__builtin_fmaf(val[v], units, least_units)) << BITS) + number - (uint32_t)L::at(v, 0);
     }
     if (a.open < a.groups) {
 #pragma unroll
