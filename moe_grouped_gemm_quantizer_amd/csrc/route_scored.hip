@@ -286,9 +286,19 @@ route_scored_rows_kernel(ScoredArgs a) {
   constexpr int AT_ONCE = NT / LPR, WAVES = NT / 64;
   constexpr int BITS = LPR * VPT <= 256 ? 8 : 10;      // of a key, for the expert's number
   constexpr uint32_t LOW = (1u << BITS) - 1u;
-  // Two values are surely in the keys' order where these differ by more than NEAR: each is off by up to
-  // 4 ulp of the score and half a one of the sum with the bias, in units of 2^-23 of the range's
-  // half (2^-21 for 10 BITS) 2.25 at most, and by 4 of the key's own forming.
+  // Two values whose keys differ by more than NEAR are surely in the keys' order. With r the largest |bias|, n
+  // the largest score (sigmoid: 1) and m = n + r half the range, a key's unit is m 2^-23 (10 BITS: m 2^-21).
+  // The difference of two near values is off by, in m 2^-24,
+  //   the sums with the bias: 1 each, 2;
+  //   sigmoid: 4 ulp of each score, 8. In all 10, 5 units (1.3);
+  //   softmax: 4 (2 ulp) of each exponential, 0.4 n for its argument's rounding (d e^-d), 1 for the product with
+  //     1 / sum: 10.8 n of both. And the error of 1 / sum, which they share, times the scores' difference: the
+  //     terms' 4 and at most 3.4 (4.5) for their arguments, 19 (21) additions, the division: 27.4 (30.5). That
+  //     difference is at most n, and for near values, being their biases', 2 r. 10.8 n + 27.4 min(n, 2 r) is
+  //     largest at n = 2 r = 2/3 m: 25.5 (27.5), with the sums 27.5 (29.5), 13.7 units (3.7);
+  //   the logits themselves (no bias, no groups): nothing.
+  // Forming a key rounds to half a whole number (a quarter) and cuts: 2 units (1.5) for two. `units`, being the
+  // same for both, scales their difference alone.
   constexpr uint32_t NEAR = BITS == 8 ? 16 : 8;
   __shared__ uint32_t took[2][MAX_E];
   __shared__ short chosen[ROWS][MAX_K];
@@ -475,7 +485,9 @@ route_scored_rows_kernel(ScoredArgs a) {
       open = reduce_u32<LPR>(bits, [](uint32_t p, uint32_t q) { return p | q; });
       least = reduce_f32<LPR>(least, [](float p, float q) { return __builtin_fminf(p, q); });
       most = max_lanes<LPR>(most);
-      // (two values a side, each off by 5.5 2^-24 of m at most, their sums' rounding and the keys' five bits)
+      // (two values a side, off as said at NEAR: 4 times 5.4 n, 30.5 min(2 n, 4 r), 4 sums with the bias, and the
+      // groups' own sums, up to 2 m, 4: 63 m 2^-24 at most, half of what is asked for. That values alike in the
+      // upper bits of their keys went by the group's number shows here as well.)
       redo = redo || (most > -__builtin_inff() && !(least - most > m * 0x1p-17f));
       wave_sync();
     }
