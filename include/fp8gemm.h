@@ -805,8 +805,9 @@ fp8g_status int8_quantize(const void* x, int type, int64_t rows, int64_t cols, i
  * M >= 0; N > 0, K > 0, multiples of 16; K <= 131056, up to which no sum
  * leaves 32 bits.
  * Errors (nothing is launched): FP8G_ERR_SHAPE, _NULL_PTR, _ALIGN as stated;
- * _UNSUPPORTED for a larger K, N > 2^27, M > 2^30 or more than 2^31 - 1
- * tiles of 128x128. M == 0 is a no-op.
+ * _UNSUPPORTED for a larger K, N > 2^27, M > 2^30 or more than 2^24 - 1
+ * tiles of 128x128 (over all experts in the calls below, each with a ragged
+ * one of its own). M == 0 is a no-op.
  */
 fp8g_status gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const float* sb, uint16_t* d,
                       int64_t M, int64_t N, int64_t K, hipStream_t stream);

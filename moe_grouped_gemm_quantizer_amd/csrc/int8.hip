@@ -972,11 +972,12 @@ Kernel choose(const Int8Args& a, int expected_m, int cus) {
     if (one || row_blocks(a, 128) * blocks(a.N, 128) <= cus) return RING128;
     return a.K % 128 ? RING256 : TILE256;
   }
-  int best = 0;
+  int best = RING128;
   int64_t least = INT64_MAX;
   for (int k = 0; k < (a.K % 128 ? TILE256 : KERNELS); ++k) {
     const Cost& c = kCost[k];
     const int64_t tiles = blocks(a.rows, c.tm) * blocks(a.N, c.tn);
+    if (tiles >= (1 << 24)) continue;                  // (2^32 threads; 128x128 tiles are fewer: checked before)
     const int64_t kb = blocks(a.K, 128), last = k == TILE256 ? tiles - full_rounds(tiles, cus) : 0;
     const int64_t round = c.round + (a.K % 128 ? c.odd : c.block) * kb;
     int64_t t = c.start + c.deep * kb + (k <= SKINNY64 ? tiles * round / cus : blocks(tiles - last, cus) * round);

@@ -11,7 +11,6 @@ using namespace fp8g;
 namespace {
 
 inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
-constexpr int64_t kInt31 = 0x7FFFFFFF;
 constexpr int64_t kMaxK = (1 << 17) - 16;             // K 2^14 < 2^31: the sum fits 32 bits
 constexpr int64_t kMaxRows = int64_t(1) << 30;
 inline fp8g_status launched(hipError_t e) { return e == hipSuccess ? FP8G_OK : FP8G_ERR_LAUNCH; }
@@ -31,10 +30,11 @@ fp8g_status check_ptrs(const Int8Args& a) {
   return FP8G_OK;
 }
 
-// Tiles of 128x128 for row blocks `mb`, over all experts.
+// Tiles of 128x128 for row blocks `mb`, over all experts. A launch holds fewer than 2^32 threads, 256 a tile.
+constexpr int64_t kMaxTiles = (1 << 24) - 1;
 bool too_many_tiles(int64_t mb, int64_t N, int64_t G) {
   const int64_t nb = (N + 127) / 128;
-  return mb > kInt31 / nb || G > kInt31 / (mb * nb > 0 ? mb * nb : 1);
+  return mb > kMaxTiles / nb || G > kMaxTiles / (mb * nb > 0 ? mb * nb : 1);
 }
 
 fp8g_status run(const Int8Args& a, int expected_m, hipStream_t stream) {
