@@ -7,6 +7,7 @@ import torch
 import moe_grouped_gemm_quantizer_amd as fp8g
 from tests import adamw_ref as ref
 from tests.gpu_util import dev
+from tests.test_gpu_adamw import Problem
 
 pytestmark = pytest.mark.gpu
 
@@ -219,3 +220,65 @@ def test_overlapping_tensors_are_refused():
         with pytest.raises(ValueError, match="overlaps"):
             lst(**bad)
     lst(params=[flat[:100], z(100)], copies=[None, flat.view(torch.bfloat16)[200:300]])
+
+
+# 8-bit states, 2^24 elements and more, most of them of 16-bit parameters: chunks of 8192 elements rather than 2048
+LARGE = 1 << 24
+
+
+@pytest.mark.parametrize("sizes,p,copy", [
+    ([LARGE + 4099], "bf16", None),
+    ([70000, LARGE + 8192 * 3 + 1, 1, 8192, 8193, 0, 16384], "f16", None),
+    # (a long list, fp32 parameters and copies among it)
+    ([300000 + 137 * i for i in range(60)], ["f32" if i % 7 == 3 else "bf16" for i in range(60)], ["f16", None, "bf16"]),
+])
+def test_large_chunks_by_the_definition(sizes, p, copy):
+    """Every parameter, code and scale byte against NumPy."""
+    kinds = [p] * len(sizes) if isinstance(p, str) else p
+    assert sum(sizes) >= LARGE and 2 * sum(n for n, k in zip(sizes, kinds) if k != "f32") > sum(sizes)
+    q = Problem(sizes, p, "bf16", 8, copy=copy, seed=len(sizes))
+    assert (q.list.table is not None) == (len(sizes) > 52)
+    q.run(step=5, max_norm=30.0)
+
+
+def test_large_chunks_and_small_ones_give_the_same_bits():
+    """The same tensor first in a list of 16-bit parameters and in one that is mostly fp32."""
+    n = LARGE + 12345
+    gen = torch.Generator(device=dev()).manual_seed(4)
+    p0 = torch.randn(n, device=dev(), generator=gen).bfloat16()
+    g = torch.randn(n, device=dev(), generator=gen)
+    results = []
+    for more in (0, n + 1):
+        ps = [p0.clone()] + [torch.zeros(more, device=dev())] * (more > 0)
+        gs = [g] + [torch.zeros(more, device=dev())] * (more > 0)
+
+        def state(k=1):
+            return [torch.zeros(-(-p.numel() // k), dtype=torch.uint8, device=dev()) for p in ps]
+        st = [state(), state(), state(128), state(128)]
+        lst = fp8g.adamw_tensors(ps, gs, *st[:2], m_scales=st[2], v_scales=st[3])
+        for step in (1, 2):
+            fp8g.adamw_step(lst, step, 1e-2, seed=9)
+        results.append([ps[0]] + [t[0] for t in st])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_large_chunks_by_table_and_by_value():
+    """A long list of large chunks in one launch, and captured in launches of 52 tensors: the same bits."""
+    sizes = [300000 + 31 * i for i in range(60)]
+    kinds = ["f32" if i % 5 == 2 else "f16" for i in range(60)]
+    a, b = (Problem(sizes, kinds, "f32", 8, copy=["bf16", None], seed=2) for _ in range(2))
+    assert sum(sizes) >= LARGE and a.list.table is not None
+    step, lr = torch.ones(1, dtype=torch.int64, device=dev()), torch.full((1,), 1e-2, device=dev())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fp8g.adamw_step(a.list, step, lr, seed=5)
+    for t in (1, 2, 3):
+        step.fill_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        fp8g.adamw_step(b.list, t, float(lr), seed=5)
+        torch.cuda.synchronize()
+        for u, v in ((a.p, b.p), (a.m, b.m), (a.v, b.v), (a.ms, b.ms), (a.vs, b.vs)):
+            assert all(torch.equal(x, y) for x, y in zip(u, v)), t
+        assert all(x is None or torch.equal(x, y) for x, y in zip(a.copies, b.copies))
