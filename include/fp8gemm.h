@@ -503,7 +503,8 @@ fp8g_status moe_route_workspace_size(int64_t T, int E, size_t* bytes);
  *
  * logits, type, T, E, ld, top_k, renormalise, loss_coef, expert_ids, counts,
  * routed: as given to and written by moe_route (ids outside [0, E) are taken
- * as -1). counts and routed may also be sums over several processes' tokens.
+ * as -1; those of a row differ, as moe_route's do). counts and routed may
+ * also be sums over several processes' tokens.
  * d_weights  fp32 [T][top_k], or NULL (no gradient comes through them).
  * d_loss     DEVICE float [1], or NULL (0).
  * d_logits   type, [T][ld_d], ld_d >= E, aligned to its element; elements
@@ -781,7 +782,9 @@ fp8g_status adamw_table(void* const* params, const int* param_types, const void*
  * has its channels as rows, stacked experts [G][N][K] are G N rows).
  *
  * For each row: amax = max |x|; scale = fl32(amax / 127);
- *   q = rne(fl32(x fl32(127 / amax))), never outside -127 .. 127.
+ *   q = rne(fl32(x fl32(127 / amax))), never outside -127 .. 127. Where x 127 /
+ *   amax is half way between two codes, as bf16 values often are (x = amax / 2:
+ *   63.5), either may be the nearer one after the two roundings.
  * A row with amax < 2^-120 counts as zero: scale 0, codes 0. A row with an
  * infinity or NaN gets the scale NaN and codes 0, so that each result formed
  * of it is NaN.
@@ -813,7 +816,7 @@ fp8g_status gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const f
                       int64_t M, int64_t N, int64_t K, hipStream_t stream);
 
 /*
- * grouped_gemm_int8_contiguous -- every expert's product in one launch,
+ * grouped_gemm_int8_contiguous -- every expert's product in one call,
  * contiguous layout: expert g owns rows [group_offsets[g],
  * group_offsets[g + 1]) of a, sa and d.
  *

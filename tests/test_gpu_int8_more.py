@@ -30,3 +30,21 @@ def test_more_rows_than_a_launch_of_small_tiles_holds(M):
         n = min(step, M - at)
         want = (a[at:at + n].float() @ b.float().t() * sa[at:at + n, None] * sb).to(torch.bfloat16)   # (sums below 2^24)
         assert torch.equal(d[at:at + n], want.view(torch.int16)), at
+
+
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16, torch.float16])
+def test_codes_are_the_nearest_whole_numbers(kind):
+    """Of x 127 / amax in 64 bits. Its fp32 form is off by half a step of the quotient and half a one of the
+    product, 127 2^-23 in all: by that much a code may be on the other side of a half."""
+    gen = torch.Generator(dev()).manual_seed(6)
+    x = (torch.randn(2000, 4096, device=dev(), generator=gen) * torch.randn(2000, 1, device=dev(), generator=gen).exp()).to(kind)
+    # (halves themselves are common where amax and x have few bits)
+    x[::2, ::3] = (x[::2].abs().amax(1, keepdim=True) * 0.5).to(kind)
+    q, s = torch.empty(x.shape, dtype=torch.int8, device=dev()), torch.empty(2000, device=dev())
+    fp8g.int8_quantize(x, q, s)
+    y = x.double() * 127 / x.double().abs().amax(1, keepdim=True)
+    assert float((y - q).abs().max()) <= 0.5 + 127 * 2.0 ** -23
+    assert int((q.abs() == 127).any(1).sum()) == 2000
+    again = torch.empty_like(q)
+    fp8g.int8_quantize(x, again, s)
+    assert torch.equal(q, again)
