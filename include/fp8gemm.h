@@ -535,7 +535,10 @@ enum { FP8G_SCORE_SIGMOID = 0, FP8G_SCORE_SOFTMAX = 1 };
  *                     ties to the lower index; -1 past the last. Without a
  *                     bias and with every group open the choice goes by the
  *                     logits (the same order). Which of two values is larger
- *                     is decided as in 64-bit arithmetic.
+ *                     is decided as in 64-bit arithmetic. (Close an expert
+ *                     by -inf: a large negative bias or logit in its place
+ *                     widens the range that values are first compared in, and
+ *                     takes up to three times as long.)
  *   weights[t][j]     scale * s[expert_ids[t][j]], with renormalise over the
  *                     row's sum of the chosen s (their shares of it, however
  *                     small the scores are; one below 2^-94 may be 0);

@@ -12,10 +12,12 @@
 // that is cut off, by 16 bits of a hash of (seed, step, tensor, element). r is never rounded to
 // 0 unless it is 0: m / (r + eps) would then be as large as eps is small.
 //
-// An HBM stream: every tensor is read and written once (300 tensors of 50M, fp32 states, 241 us, 5.8 TB/s; 8 x
-// 29M with 8-bit states 676, 5.5 TB/s). The list travels in the kernel's arguments, MAX_T tensors a
-// launch, or lies in device memory for a launch over all of them (300 tensors of 50M: 6 launches 274 us, one
-// 241; of 5M 54 / 27).
+// An HBM stream: every tensor is read and written once (300 tensors of 50M, fp32 states, 241 to 250 us, 5.6 to
+// 5.8 TB/s; 8 x 29M with 8-bit states 673, 5.6 TB/s). The list travels in the kernel's arguments, MAX_T tensors a
+// launch, or lies in device memory for a launch over all of them (300 tensors of 50M: 6 launches 272 us, one
+// 247; of 5M 54 / 27). Where the step's number or its rate lies on the device, every thread forms the factors in
+// 64 bits: nothing beside fp32 states (300 tensors of 50M 252 us both ways, captured 274 / 272), 4% of a
+// vector-bound step (8 x 29M with 8-bit states 706 / 676, captured 709 / 681; 2 x 50M bf16 205 / 195).
 
 #include <math.h>
 #include <vector>
@@ -128,7 +130,8 @@ struct Factors {
   uint32_t key;
 };
 
-// A 32-bit hash: xor-shifts and odd multipliers.
+// A 32-bit hash: xor-shifts and odd multipliers. (Shifts and multipliers as C. Wellons published them in 2018,
+// found by a search for the least bias.)
 __host__ __device__ __forceinline__ uint32_t mix(uint32_t h) {
   h = (h ^ (h >> 16)) * 0x7FEB352Du;
   h = (h ^ (h >> 15)) * 0x846CA68Bu;
@@ -520,10 +523,10 @@ adamw_kernel(Args a) {
 }
 
 // A list's chunk. Small ones where HBM is the bound: they reach all CUs and end evenly (2048 /
-// 8192 elements: 300 tensors of 50M, fp32 parameters, fp32 states 246 / 277 us, 8-bit states 168 /
-// 173; 8 x 29M 8-bit 676 / 743; 3M elements 18.6 / 21.1). Large lists of 16-bit parameters with
-// 8-bit states are bound by the vector unit, which what a workgroup does once (the clipping
-// factor in fp64, the search) keeps busy too (2 x 50M bf16 241 / 219, 300 of 50M 127 / 116).
+// 8192 elements: 300 tensors of 50M, fp32 parameters, fp32 states 246 / 277 us, 8-bit states 142 /
+// 166; 8 x 29M 8-bit 672 / 741; 3M elements 13.7 / 16.4; 300 bf16 tensors of 5M 18.7 / 21.3). Large lists of
+// 16-bit parameters with 8-bit states are bound by the vector unit, which what a workgroup does once (the
+// clipping factor in fp64, the search) keeps busy too (2 x 50M bf16 208 / 195, 300 of 50M 108 / 102, of 17M 44 / 43).
 int chunk_for(const AdamwCall& c) {
   if (!c.ms) return CHUNK_MIN;
   int64_t total = 0, narrow = 0;

@@ -13,7 +13,11 @@
 // whole numbers of 24 (22) bits of the row's range with the expert's number below; where two
 // neighbours among the chosen and the next, or the last open and the first closed group, are
 // nearer than their errors and not alike (the same logit and bias), the row is put on a list and
-// done again in 64 bits by a wave of its own: about 0.1% of the rows of random fp32 logits.
+// done again in 64 bits by a wave of its own: about 0.1% of the rows of random fp32 logits. It is most rows
+// where a large bias (or, without biases and groups, a large logit) makes the range so wide that its unit
+// is the scores' differences, and all rows where groups are alike. T 32768, E 256, fp32: 42 us, with eight experts
+// closed by a bias of -inf or -10 41, of -1e4 114, of -1e9 115; without groups 34, 34, 87 and 100; closed by a
+// logit, without biases, -inf 33, -1e4 53, -1e9 85; all logits and biases alike 118.
 //
 // T 32768, E 256, 8 groups, fp32: 31 us for the rows (the data 7.4 at the rate of a large copy), bound by the
 // vector unit (1400 instructions for four rows, 18 us) and at the end by the rows done again, which take 6 us
