@@ -744,8 +744,9 @@ fp8g_status grad_clip(const void* const* grads, void* const* outs, const int64_t
  *                    added) or NULL, and DEVICE float [1] or NULL: the norm.
  * table              NULL, or the DEVICE copy of what adamw_table wrote for
  *                    these lists, 8-byte aligned: a long list is then one
- *                    launch, for one of each 52 tensors without it. Not
- *                    read by steps that are captured into a graph.
+ *                    launch, for one of each 52 tensors without it. The step
+ *                    reads it when it runs, so that it has to stay until
+ *                    then; steps that are captured into a graph do not.
  * Errors (nothing is launched): FP8G_ERR_SHAPE (negative sizes, step_value < 1,
  * a beta outside [0, 1), eps negative, a hyperparameter that is not finite,
  * max_norm not > 0 with sumsq), _NULL_PTR (also norm without sumsq), _ALIGN,
