@@ -174,7 +174,7 @@ def _torchs_stream(stream, handle):
             s = torch.cuda.default_stream()
     else:
         s = stream
-    if s.cuda_stream != handle or (handle != 0 and s.stream_id == handle):
+    if not isinstance(s, torch.cuda.Stream) or s.cuda_stream != handle or (handle != 0 and s.stream_id == handle):
         return None                          # (a foreign stream's id is its handle)
     return s
 
